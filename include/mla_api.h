@@ -307,6 +307,35 @@ MLA_API mla_status_t mla_decode_chunk(const mla_plan_t* plan, const mla_cache_t*
                                       const void* q, int32_t B, int32_t Q, void* out, void* workspace,
                                       size_t ws_bytes, void* stream);
 
+/* mla_decode with a sliding window and sinks: the query of sequence b, at position
+ * p = seq_lens[b] - 1, attends over the tokens t <= p with t < n_sink (the first tokens, which
+ * stay visible) or t > p - window (the newest `window` tokens, its own included).  Every other
+ * token is left out: its cache rows may hold anything (infinities and NaN too), and a paged
+ * cache needs no block for a run of 128 hidden tokens (mla_blocks_trim releases them; their
+ * table entries are not read).  Positions stay those of the whole sequence: the query is
+ * rotated at p, the keys keep the rotation they were appended with.  The cost follows the
+ * visible tokens, not the length.  With window >= T_cap it is mla_decode's attention.
+ *   n_sink >= 0, window >= 1; the other arguments, the workspace and L == 0 as for mla_decode
+ * Every cache kind.  Kernel: the head-row tensor-core kernel where its shapes allow
+ * (mla_decode_kernel_choice, 3), else the CUDA-core kernel; MLA_OPT_DECODE_KERNEL = 2 returns
+ * MLA_ERR_UNSUPPORTED (the token-row kernel has no window). */
+MLA_API mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache, const int32_t* seq_lens,
+                                       const void* q, int32_t B, int32_t n_sink, int32_t window, void* out,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/* mla_decode_chunk with a sliding window and sinks: query i of sequence b, at position
+ * p = seq_lens[b] - Q + i, attends over the tokens t <= p with t < n_sink or t > p - window.
+ * Per query this is mla_decode_window with length p + 1.  Cache rows of tokens that no query
+ * of the sequence sees may hold anything; a row that some of its queries see must be finite
+ * (queries share the tiles they read, so what a non-finite row does to the sequence's other
+ * queries is unspecified).  Arguments, workspace (mla_decode_chunk_workspace_bytes) and
+ * supported shapes as for mla_decode_chunk; n_sink >= 0, window >= 1; Q == 1 is
+ * mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED. */
+MLA_API mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* cache,
+                                             const int32_t* seq_lens, const void* q, int32_t B, int32_t Q,
+                                             int32_t n_sink, int32_t window, void* out, void* workspace,
+                                             size_t ws_bytes, void* stream);
+
 /* One serving-loop decode step in a single call: the append of every sequence's new
  * token, then the decode of every sequence's new query.  Token b (row b of x) is the
  * newest token of sequence b: it is appended at position seq_lens[b] - 1 (the length
@@ -369,13 +398,116 @@ enum {
   MLA_DEVERR_SEQ_LEN = 1,     /* a seq_lens entry was < 0 or > T_cap (treated as 0) */
   MLA_DEVERR_APPEND_SLOT = 2, /* an append token had seq_idx/pos out of range (skipped) */
   MLA_DEVERR_TIMEOUT = 4,     /* a pipeline wait exceeded its bound (output invalid) */
-  MLA_DEVERR_BLOCK = 8        /* a paged cache's block table named a block outside the pool */
+  MLA_DEVERR_BLOCK = 8,       /* a paged cache's block table named a block outside the pool */
+  MLA_DEVERR_POOL = 16,       /* mla_blocks_reserve: too few free blocks (nothing allocated) */
+  MLA_DEVERR_ROW = 32         /* mla_blocks_fork, mla_ring_copy: a pair of rows was skipped */
 };
 /* Synchronise the device, read and clear the plan's device error word.
  * *code receives 0 (none) or a bitwise OR of MLA_DEVERR_* values.
  * Returns MLA_OK, MLA_ERR_INVALID_ARG for a NULL plan or code, or MLA_ERR_CUDA when the
  * synchronisation itself failed. */
 MLA_API mla_status_t mla_device_error(mla_plan_t* plan, int32_t* code);
+
+/* ---- Blocks of a paged cache ------------------------------------------------------------
+ * Bookkeeping of the pool blocks that paged caches are made of, on the device and without a
+ * host round trip (every call can be captured into a graph).  It is layer independent: the
+ * layers of a model share one block table and one set of reference counts, and mla_blocks_copy
+ * moves the rows of each layer's cache.
+ *   table  device [B][n_cols] int32: the pool block of tokens [128 j, 128 j + 128) of sequence b
+ *          at column j, -1 for none (mla_cache_t::block_table with T_cap = 128 n_cols)
+ *   refs   device [n_blocks] int32: holders of each block, 0 = free.  At least the number of
+ *          table entries that name the block; more when the caller holds it elsewhere too.
+ *   table_out, refs_out  receive the updated table and counts, all of it; either may be the
+ *          input itself (in place), else the ranges must not overlap (a step in flight then
+ *          keeps reading the old table)
+ *   copies device [max_copies][3] int32: (source block, destination block, rows) to be moved
+ *   status device [MLA_BLOCKS_STATUS_INTS] int32, zeroed by the caller before its first use:
+ *          [0] entries of copies the last reserve or compact wrote
+ *          [1] error bits (MLA_DEVERR_*), or-ed in by every call until the caller clears them
+ *          [2] blocks in use after the last reserve or compact
+ *          [3] blocks the last reserve allocated, or the last compact moved
+ * Table entries outside [-1, n_blocks) set MLA_DEVERR_BLOCK and count as none.  Calls that
+ * share buffers must be ordered on one stream.  These calls need no plan.  All return
+ * MLA_ERR_INVALID_ARG for a null pointer, a size that is not positive or too large (n_cols
+ * or n_blocks above 2^24, B * n_cols above 2^30) or an output that partly overlaps its input,
+ * MLA_ERR_ALIGNMENT for a pointer that is not 4-byte aligned (16-byte: workspace). */
+#define MLA_BLOCKS_STATUS_INTS 4
+
+/* Workspace of mla_blocks_reserve and mla_blocks_compact in bytes; 0 for invalid sizes. */
+MLA_API size_t mla_blocks_workspace_bytes(int32_t B, int32_t n_cols, int32_t n_blocks);
+
+/* Share sequences: for every i, row dst[i] of the table becomes the first
+ * ceil(seq_lens[src[i]] / 128) entries of row src[i] and -1 behind them.  Each block gains a
+ * holder per new entry; what row dst[i] held before is released.  One source may have many
+ * destinations.  Sequences that then append to a shared, partly filled block need
+ * mla_blocks_reserve first (copy on write).
+ *   src, dst device [n] int32 rows in [0, B); seq_lens device [B] int32 in [0, 128 n_cols]
+ * A pair is skipped and MLA_DEVERR_ROW set when a row is out of range, when an earlier pair
+ * has the same dst, or when its src is the dst of a pair with another source; a source length
+ * out of range skips the pair and sets MLA_DEVERR_SEQ_LEN.  src[i] == dst[i] cuts the row to
+ * its length.  The residual window of MLA_CACHE_INT4_G32_R128 is per sequence and layer:
+ * mla_ring_copy. */
+MLA_API mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols,
+                                     int32_t n_blocks, const int32_t* src, const int32_t* dst, int32_t n,
+                                     const int32_t* seq_lens, int32_t* table_out, int32_t* refs_out, int32_t* status,
+                                     void* stream);
+
+/* Make room for tokens [seq_lens[b], new_lens[b]) of every sequence, so that they can be
+ * appended: a free block for each column they touch that has none, and a private copy of a
+ * partly filled last block (seq_lens[b] % 128 > 0) that others hold too.  Of several sequences
+ * in the table that write into the same block, in order of b, each copies while another holder
+ * is left; with no holder elsewhere the last one keeps the block.  New blocks are the free
+ * blocks of lowest id, given out in the order (b, column), with one holder each; the copied
+ * block loses a holder.  `copies` lists the rows to move, in order of b (at most one per
+ * sequence: seq_lens[b] % 128 rows); run mla_blocks_copy with every layer's cache before the
+ * append.  When the pool has too few free blocks nothing is allocated for any sequence: table
+ * and counts stay, no copies are listed, and MLA_DEVERR_POOL is set.
+ *   seq_lens, new_lens device [B] int32, 0 <= seq_lens <= new_lens <= 128 n_cols: a sequence
+ *     outside that gets nothing and sets MLA_DEVERR_SEQ_LEN; one whose partly filled block is
+ *     missing from the table sets MLA_DEVERR_BLOCK
+ *   max_copies >= B; workspace >= mla_blocks_workspace_bytes(B, n_cols, n_blocks) bytes */
+MLA_API mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols,
+                                        int32_t n_blocks, const int32_t* seq_lens, const int32_t* new_lens,
+                                        int32_t* table_out, int32_t* refs_out, int32_t* copies, int32_t max_copies,
+                                        int32_t* status, void* workspace, size_t ws_bytes, void* stream);
+
+/* Release what no later query reads: every table entry whose block holds no token of
+ * [0, min(n_sink, L)) or [L - window, L), L = seq_lens[b], becomes -1 and its block loses a
+ * holder.  With the n_sink and window of mla_decode_window the next steps of every sequence
+ * keep all they see.  Blocks behind the length are released too; L = 0 frees the whole row.
+ *   seq_lens device [B] int32 in [0, 128 n_cols]: out of range leaves the row as it is and
+ *     sets MLA_DEVERR_SEQ_LEN;  n_sink >= 0, window >= 0 (0 with n_sink = 0 frees every row) */
+MLA_API mla_status_t mla_blocks_trim(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols,
+                                     int32_t n_blocks, const int32_t* seq_lens, int32_t n_sink, int32_t window,
+                                     int32_t* table_out, int32_t* refs_out, int32_t* status, void* stream);
+
+/* Move the blocks in use to the front of the pool: with m blocks in use, those with ids >= m,
+ * in ascending order, go to the free ids below m, in ascending order; counts and table entries
+ * follow.  `copies` lists the moves (whole blocks, at most n_blocks / 2 of them) and is also
+ * the renaming for holders outside the table; run mla_blocks_copy with every layer's cache
+ * before anything reads or writes through the new table.
+ *   max_copies >= n_blocks / 2; workspace >= mla_blocks_workspace_bytes(B, n_cols, n_blocks) */
+MLA_API mla_status_t mla_blocks_compact(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols,
+                                        int32_t n_blocks, int32_t* table_out, int32_t* refs_out, int32_t* copies,
+                                        int32_t max_copies, int32_t* status, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/* Copy the first `rows` token rows of block `source` to block `destination` in every array of
+ * one layer's paged cache (c_kv, c_scales, k_rope), for each of the status[0] entries of
+ * `copies`.  Rows behind them are left as they were.  Destinations must be distinct and none
+ * of them a source, as reserve and compact list them.  An entry with a block outside the pool
+ * or rows outside [0, 128] is skipped and sets MLA_DEVERR_BLOCK in status[1].
+ *   cfg describes the cache (MLA_ERR_INVALID_ARG for one that is not paged); its block_table
+ *   is not read.  status[0] above max_copies counts as max_copies. */
+MLA_API mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* copies,
+                                     int32_t max_copies, int32_t* status, void* stream);
+
+/* Copy the residual window (MLA_CACHE_INT4_G32_R128: ring rows and their positions) of
+ * sequence src[i] to sequence dst[i] in one layer's cache, for a fork.  A pair is skipped and
+ * MLA_DEVERR_ROW set in status[1] under the conditions of mla_blocks_fork's rows.
+ *   src, dst device [n] int32 in [0, cache->B).  MLA_ERR_INVALID_ARG for a cache without a ring. */
+MLA_API mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src,
+                                   const int32_t* dst, int32_t n, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

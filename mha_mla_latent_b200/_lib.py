@@ -22,6 +22,8 @@ MLA_RESID_WINDOW = 128
 MLA_OPT_DECODE_KERNEL, MLA_OPT_DECODE_SPLITS, MLA_OPT_PROFILE_EVENTS, MLA_OPT_OVERLAP_LAUNCH = 1, 2, 3, 4
 MLA_OPT_WAIT_LIMIT_US, MLA_OPT_TEST_SKIP_COPY, MLA_OPT_PROFILE_KERNELS = 5, 6, 8
 MLA_DEVERR_SEQ_LEN, MLA_DEVERR_APPEND_SLOT, MLA_DEVERR_TIMEOUT, MLA_DEVERR_BLOCK = 1, 2, 4, 8
+MLA_DEVERR_POOL, MLA_DEVERR_ROW = 16, 32
+MLA_BLOCKS_STATUS_INTS = 4
 MLA_BLOCK_TOKENS = 128
 
 EXPORTED = (
@@ -29,7 +31,9 @@ EXPORTED = (
     "mla_plan_create", "mla_plan_destroy", "mla_plan_set_option", "mla_append",
     "mla_decode_workspace_bytes", "mla_decode", "mla_device_error", "mla_decode_noalloc",
     "mla_fixed_pairs", "mla_decode_step", "mla_decode_step_host", "mla_decode_chunk",
-    "mla_decode_chunk_workspace_bytes", "mla_decode_kernel_choice",
+    "mla_decode_chunk_workspace_bytes", "mla_decode_kernel_choice", "mla_decode_window",
+    "mla_decode_chunk_window", "mla_blocks_workspace_bytes", "mla_blocks_fork", "mla_blocks_reserve",
+    "mla_blocks_trim", "mla_blocks_compact", "mla_blocks_copy", "mla_ring_copy",
 )
 MLA_PAIRS_FULL, MLA_PAIRS_HIGH, MLA_PAIRS_UNIFORM, MLA_PAIRS_LOW = 0, 1, 2, 5
 MLA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -80,6 +84,15 @@ def _load():
         "mla_decode_step": (i32, [vp, cachep, vp, vp, vp, i32, vp, vp, sz, vp]),
         "mla_decode_chunk": (i32, [vp, cachep, vp, vp, i32, i32, vp, vp, sz, vp]),
         "mla_decode_chunk_workspace_bytes": (sz, [vp, i32, i32]),
+        "mla_decode_window": (i32, [vp, cachep, vp, vp, i32, i32, i32, vp, vp, sz, vp]),
+        "mla_decode_chunk_window": (i32, [vp, cachep, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]),
+        "mla_blocks_workspace_bytes": (sz, [i32, i32, i32]),
+        "mla_blocks_fork": (i32, [vp, vp, i32, i32, i32, vp, vp, i32, vp, vp, vp, vp, vp]),
+        "mla_blocks_reserve": (i32, [vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "mla_blocks_trim": (i32, [vp, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp]),
+        "mla_blocks_compact": (i32, [vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "mla_blocks_copy": (i32, [cfgp, cachep, vp, i32, vp, vp]),
+        "mla_ring_copy": (i32, [cfgp, cachep, vp, vp, i32, vp, vp]),
         "mla_decode_step_host": (i32, [vp, cachep, vp, vp, vp, i32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -254,6 +267,135 @@ def mla_decode_chunk(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, s
                                int(q.shape[1]), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream))
     if check:
         _check(st, "mla_decode_chunk")
+    return st
+
+
+def mla_decode_window(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, n_sink, window, stream=None,
+                      check=True):
+    """mla_decode over the first n_sink tokens and the newest `window` tokens of each sequence."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = _lib.mla_decode_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), int(q.shape[0]),
+                                int(n_sink), int(window), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mla_decode_window")
+    return st
+
+
+def mla_decode_chunk_window(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, n_sink, window, stream=None,
+                            check=True):
+    """mla_decode_chunk with each query seeing the first n_sink tokens and the `window` tokens
+    up to its own: q and out are [B][Q][H][d_h]."""
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = _lib.mla_decode_chunk_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), int(q.shape[0]),
+                                      int(q.shape[1]), int(n_sink), int(window), _ptr(out), _ptr(workspace), ws_bytes,
+                                      _stream(stream))
+    if check:
+        _check(st, "mla_decode_chunk_window")
+    return st
+
+
+def mla_blocks_workspace_bytes(B: int, n_cols: int, n_blocks: int) -> int:
+    return int(_lib.mla_blocks_workspace_bytes(int(B), int(n_cols), int(n_blocks)))
+
+
+def _int32(**tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a device tensor")
+
+
+def _table_args(table, refs, table_out, refs_out, status, seq_lens=None):
+    """Checks the block table's tensors and returns (B, n_cols, n_blocks)."""
+    _int32(table=table, refs=refs, table_out=table_out, refs_out=refs_out, status=status)
+    if table.dim() != 2 or refs.dim() != 1 or table_out.shape != table.shape or refs_out.shape != refs.shape:
+        raise ValueError("table is [B][n_cols], refs [n_blocks]; table_out and refs_out have their shapes")
+    if status.numel() < MLA_BLOCKS_STATUS_INTS:
+        raise ValueError(f"status holds {MLA_BLOCKS_STATUS_INTS} int32")
+    if seq_lens is not None:
+        _int32(seq_lens=seq_lens)
+        if seq_lens.numel() != table.shape[0]:
+            raise ValueError("a length per table row is needed")
+    return int(table.shape[0]), int(table.shape[1]), int(refs.shape[0])
+
+
+def _n_copies(copies) -> int:
+    _int32(copies=copies)
+    if copies.dim() != 2 or copies.shape[1] != 3:
+        raise ValueError("copies is [max_copies][3]")
+    return int(copies.shape[0])
+
+
+def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status, stream=None, check=True):
+    """Row dst[i] of the table shares the blocks of row src[i] (its first seq_lens[src[i]] tokens)."""
+    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
+    _int32(src=src, dst=dst)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst have one entry per pair")
+    st = _lib.mla_blocks_fork(_ptr(table), _ptr(refs), B, C, n, _ptr(src), _ptr(dst), int(src.numel()), _ptr(seq_lens),
+                              _ptr(table_out), _ptr(refs_out), _ptr(status), _stream(stream))
+    if check:
+        _check(st, "mla_blocks_fork")
+    return st
+
+
+def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, copies, status, workspace, stream=None,
+                       check=True):
+    """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence, shared partial blocks copied on write."""
+    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
+    _int32(new_lens=new_lens)
+    if new_lens.numel() != B:
+        raise ValueError("a new length per table row is needed")
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = _lib.mla_blocks_reserve(_ptr(table), _ptr(refs), B, C, n, _ptr(seq_lens), _ptr(new_lens), _ptr(table_out),
+                                 _ptr(refs_out), _ptr(copies), _n_copies(copies), _ptr(status), _ptr(workspace),
+                                 ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mla_blocks_reserve")
+    return st
+
+
+def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, status, stream=None, check=True):
+    """Releases the blocks without a token among the first n_sink or the newest `window` ones."""
+    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
+    st = _lib.mla_blocks_trim(_ptr(table), _ptr(refs), B, C, n, _ptr(seq_lens), int(n_sink), int(window),
+                              _ptr(table_out), _ptr(refs_out), _ptr(status), _stream(stream))
+    if check:
+        _check(st, "mla_blocks_trim")
+    return st
+
+
+def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspace, stream=None, check=True):
+    """Moves the blocks in use to the lowest ids; `copies` lists the moves."""
+    B, C, n = _table_args(table, refs, table_out, refs_out, status)
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = _lib.mla_blocks_compact(_ptr(table), _ptr(refs), B, C, n, _ptr(table_out), _ptr(refs_out), _ptr(copies),
+                                 _n_copies(copies), _ptr(status), _ptr(workspace), ws_bytes, _stream(stream))
+    if check:
+        _check(st, "mla_blocks_compact")
+    return st
+
+
+def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None, check=True):
+    """Moves the listed rows in one layer's cache (run it once per layer)."""
+    _int32(status=status)
+    st = _lib.mla_blocks_copy(ctypes.byref(cfg), ctypes.byref(cache), _ptr(copies), _n_copies(copies), _ptr(status),
+                              _stream(stream))
+    if check:
+        _check(st, "mla_blocks_copy")
+    return st
+
+
+def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True):
+    """Copies the residual windows of sequences src to sequences dst in one layer's cache."""
+    _int32(src=src, dst=dst, status=status)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst have one entry per pair")
+    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _ptr(src), _ptr(dst), int(src.numel()),
+                            _ptr(status), _stream(stream))
+    if check:
+        _check(st, "mla_ring_copy")
     return st
 
 

@@ -28,7 +28,6 @@ class LatentCache:
                 raise ValueError(f"a paged cache needs T_cap a multiple of {BT} and n_blocks > 0")
             self.block_table = torch.as_tensor(block_table, dtype=torch.int32).to(device).contiguous()
             assert tuple(self.block_table.shape) == (B, T_cap // BT)
-            self._table = self.block_table.cpu().numpy()
             self.n_blocks = int(n_blocks)
             rows, cap = self.n_blocks, BT
         else:
@@ -60,7 +59,7 @@ class LatentCache:
         if not self.paged:
             return torch.full_like(t, b), t
         BT = _lib.MLA_BLOCK_TOKENS
-        return torch.from_numpy(self._table[b])[t // BT].long(), t % BT
+        return self.block_table[b].cpu()[t // BT].long(), t % BT   # as the device holds it: a BlockPool changes it
 
     def _rows(self, arr, b, t0, t1):
         pb, pt = self._loc(b, t0, t1)
@@ -117,6 +116,80 @@ class LatentCache:
     def nbytes_used(self, seq_lens) -> int:
         per_tok = _lib.mla_cache_bytes_per_token(self.cfg)
         return int(sum(int(x) for x in seq_lens)) * per_tok
+
+
+class BlockPool:
+    """The blocks that the paged caches of a model's layers are made of: one block table
+    [B][T_cap/128] (-1: no block) and one count of holders per block, kept on the device by the
+    mla_blocks_* entry points.  Layers made with `layer` share the table; what a call moves is
+    moved in every one of them.  Nothing here waits for the device but `errors` and `in_use`."""
+
+    def __init__(self, B: int, T_cap: int, n_blocks: int, device="cuda"):
+        BT = _lib.MLA_BLOCK_TOKENS
+        if B <= 0 or T_cap <= 0 or T_cap % BT or n_blocks <= 0:
+            raise ValueError(f"a pool needs B > 0, T_cap a multiple of {BT} and n_blocks > 0")
+        self.B, self.T_cap, self.n_blocks, self.device = int(B), int(T_cap), int(n_blocks), device
+        new = lambda *s: torch.empty(*s, dtype=torch.int32, device=device)  # noqa: E731
+        self.table = new(B, T_cap // BT).fill_(-1)
+        self.refs = new(n_blocks).zero_()
+        self.status = new(_lib.MLA_BLOCKS_STATUS_INTS).zero_()
+        self.copies = new(max(B, n_blocks // 2, 1), 3)
+        self.workspace = torch.empty(_lib.mla_blocks_workspace_bytes(B, T_cap // BT, n_blocks), dtype=torch.uint8,
+                                     device=device)
+        self.layers = []
+
+    def layer(self, cfg: "_lib.MlaConfig") -> LatentCache:
+        """A layer's cache over this pool's blocks."""
+        c = LatentCache(cfg, self.B, self.T_cap, self.device, block_table=self.table, n_blocks=self.n_blocks)
+        if c.block_table.data_ptr() != self.table.data_ptr():
+            raise ValueError("the layer does not share the pool's table")
+        self.layers.append(c)
+        return c
+
+    def _int32(self, x):
+        return torch.as_tensor(x, dtype=torch.int32).to(self.device).contiguous()
+
+    def _move(self, stream):
+        for c in self.layers:
+            _lib.mla_blocks_copy(c.cfg, c.struct, self.copies, self.status, stream=stream)
+
+    def fork(self, src, dst, seq_lens, stream=None) -> None:
+        """Sequence dst[i] shares the blocks of the first seq_lens[src[i]] tokens of src[i]
+        (the residual windows are copied)."""
+        src, dst, lens = self._int32(src), self._int32(dst), self._int32(seq_lens)
+        _lib.mla_blocks_fork(self.table, self.refs, src, dst, lens, self.table, self.refs, self.status, stream=stream)
+        for c in self.layers:
+            if c.c_resid is not None:
+                _lib.mla_ring_copy(c.cfg, c.struct, src, dst, self.status, stream=stream)
+
+    def reserve(self, seq_lens, new_lens, stream=None) -> None:
+        """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence; shared, partly
+        filled blocks are copied on write."""
+        _lib.mla_blocks_reserve(self.table, self.refs, self._int32(seq_lens), self._int32(new_lens), self.table,
+                                self.refs, self.copies, self.status, self.workspace, stream=stream)
+        self._move(stream)
+
+    def trim(self, seq_lens, n_sink: int, window: int, stream=None) -> None:
+        """Releases the blocks that mla_decode_window does not read any more; a sequence of
+        length 0 is freed."""
+        _lib.mla_blocks_trim(self.table, self.refs, self._int32(seq_lens), n_sink, window, self.table, self.refs,
+                             self.status, stream=stream)
+
+    def compact(self, stream=None) -> None:
+        """Moves the blocks in use to the front of the pool."""
+        _lib.mla_blocks_compact(self.table, self.refs, self.table, self.refs, self.copies, self.status,
+                                self.workspace, stream=stream)
+        self._move(stream)
+
+    def errors(self) -> int:
+        """The error bits (MLA_DEVERR_*) since the last call of this method."""
+        code = int(self.status[1].item())
+        self.status[1].zero_()
+        return code
+
+    def in_use(self) -> int:
+        """Blocks with a holder."""
+        return int((self.refs > 0).sum().item())
 
 
 def workspace(plan: "_lib.Plan", B: int, device="cuda") -> torch.Tensor:

@@ -1,0 +1,564 @@
+// Blocks of a paged cache: forking, reserving (with copy on write), trimming and compacting
+// the block table and its reference counts on the device, and copying blocks' rows.
+//
+// The state is a table [B][C] of pool blocks (-1: none) and a count of holders per block; a
+// block is free when its count is 0, so the counts are the whole allocator: the free blocks of
+// lowest id come out of a prefix sum over them, and results do not depend on thread order.
+#include <algorithm>
+
+#include "decode_common.cuh"
+
+namespace mla {
+namespace blocks {
+
+constexpr int kBT = MLA_BLOCK_TOKENS;
+constexpr int kThreads = 1024;        // the single-CTA kernels
+constexpr int kTile = kThreads * 32;  // ids per step of a pass over the counts: a 32-bit word per thread
+constexpr int kMaxBlocks = 1 << 24;   // 2^31 token rows, the most a cache may hold
+constexpr int kShortRow = 8;          // columns a thread walks by itself; longer runs go to a warp
+
+struct Table {
+  const int32_t* in;
+  int32_t* out;
+  int32_t* refs;      // updated in place (the output counts)
+  int32_t B, C, n_blocks;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void flag(int32_t* status, int32_t bit) { atomicOr(status + 1, bit); }
+
+// A table entry's block, or -1 for none (an entry outside the pool counts as none).
+__device__ __forceinline__ int entry(const Table& t, int32_t e) {
+  if (e >= 0 && e < t.n_blocks) return e;
+  if (e != -1) flag(t.status, MLA_DEVERR_BLOCK);
+  return -1;
+}
+
+__device__ __forceinline__ bool length_ok(const Table& t, int L) { return L >= 0 && (long long)L <= (long long)t.C * kBT; }
+
+// The pair that writes row r (the first i with dst[i] == r), or -1: none, or a pair to skip.
+// Whole CTA; flags what is skipped.
+__device__ int pair_of(const int32_t* src, const int32_t* dst, int n, int r, int rows, int32_t* status) {
+  __shared__ int s_first, s_count, s_written;
+  if (threadIdx.x == 0) { s_first = INT_MAX; s_count = 0; s_written = 0; }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    if (dst[i] == r) {
+      atomicMin(&s_first, i);
+      atomicAdd(&s_count, 1);
+    }
+  __syncthreads();
+  const int i = s_first == INT_MAX ? -1 : s_first;
+  if (i < 0) return -1;
+  if (s_count > 1 && threadIdx.x == 0) flag(status, MLA_DEVERR_ROW);
+  const int s = src[i];
+  bool ok = s >= 0 && s < rows;
+  if (ok && s != r)   // a source that another pair rewrites
+    for (int j = threadIdx.x; j < n; j += blockDim.x)
+      if (dst[j] == s && src[j] != s) s_written = 1;
+  __syncthreads();
+  ok = ok && !s_written;
+  if (!ok && threadIdx.x == 0) flag(status, MLA_DEVERR_ROW);
+  return ok ? i : -1;
+}
+
+// Destinations outside the table (no row looks for them).
+__device__ void check_rows(const int32_t* dst, int n, int rows, int32_t* status) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    if (dst[i] < 0 || dst[i] >= rows) flag(status, MLA_DEVERR_ROW);
+}
+
+// ------------------------------------------------------------------ fork
+// One CTA per table row.
+__global__ void __launch_bounds__(128) fork_kernel(Table t, const int32_t* __restrict__ src,
+                                                   const int32_t* __restrict__ dst, int n,
+                                                   const int32_t* __restrict__ seq_lens) {
+  const int r = blockIdx.x;
+  if (r == 0) check_rows(dst, n, t.B, t.status);
+  int i = pair_of(src, dst, n, r, t.B, t.status);
+  int cols = 0, s = 0;
+  if (i >= 0) {
+    s = src[i];
+    const int L = seq_lens[s];
+    if (!length_ok(t, L)) {
+      if (threadIdx.x == 0) flag(t.status, MLA_DEVERR_SEQ_LEN);
+      i = -1;
+    }
+    cols = (int)(((long long)L + kBT - 1) / kBT);
+  }
+  const int32_t* row = t.in + (size_t)r * t.C;
+  const int32_t* from = t.in + (size_t)s * t.C;
+  int32_t* out = t.out + (size_t)r * t.C;
+  for (int j = threadIdx.x; j < t.C; j += blockDim.x) {
+    const int32_t old = row[j];
+    if (i < 0) {
+      if (t.out != t.in) out[j] = old;
+      continue;
+    }
+    const int was = entry(t, old), now = j < cols ? entry(t, from[j]) : -1;
+    if (was >= 0) atomicSub(t.refs + was, 1);
+    if (now >= 0) atomicAdd(t.refs + now, 1);
+    out[j] = now;
+  }
+}
+
+// ------------------------------------------------------------------ trim
+__global__ void __launch_bounds__(256) trim_kernel(Table t, const int32_t* __restrict__ seq_lens, int n_sink,
+                                                   int window) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)t.B * t.C) return;
+  const int b = (int)(i / t.C);
+  const long long t0 = (i - (long long)b * t.C) * kBT, L = seq_lens[b];
+  int32_t e = t.in[i];
+  if (!length_ok(t, (int)L)) {
+    flag(t.status, MLA_DEVERR_SEQ_LEN);
+  } else {
+    const bool keep = t0 < min((long long)n_sink, L) || (window > 0 && t0 < L && t0 + kBT > L - window);
+    const int id = entry(t, e);
+    if (!keep) {
+      if (id >= 0) atomicSub(t.refs + id, 1);
+      e = -1;
+    }
+  }
+  t.out[i] = e;
+}
+
+// ------------------------------------------------------------------ passes over the counts
+// Bit i of the returned word: `pick(id, count)` of id = base + 32 * threadIdx.x + i (false past
+// the pool).  Warp w reads its 1024 ids in 32 coalesced loads; lane k keeps the k-th ballot.
+template <typename F>
+__device__ __forceinline__ uint32_t count_word(const int32_t* refs, int n_blocks, int base, F pick) {
+  const int lane = threadIdx.x & 31, w0 = base + (threadIdx.x >> 5) * 1024;
+  uint32_t word = 0;
+#pragma unroll 8
+  for (int k = 0; k < 32; ++k) {
+    const int id = w0 + 32 * k + lane;
+    const uint32_t m = __ballot_sync(0xffffffffu, id < n_blocks && pick(id, __ldcg(refs + min(id, n_blocks - 1))));
+    if (lane == k) word = m;
+  }
+  return word;
+}
+
+// Writes the ids of `word`'s set bits to list[first ...], those below `limit` only.
+__device__ __forceinline__ void list_bits(uint32_t word, int id0, int32_t* list, int first, int limit) {
+  while (word && first < limit) {
+    list[first++] = id0 + __ffs(word) - 1;
+    word &= word - 1;
+  }
+}
+
+// ------------------------------------------------------------------ reserve
+struct ReserveWs {
+  int32_t* need;    // [B] new blocks of earlier rows
+  int32_t* copy;    // [B] index of the row's copy in the list, -1: none
+  int32_t* writers; // [n_blocks] rows that write into a shared block ...
+  int32_t* last;    // [n_blocks] ... and the last of them (valid at shared blocks only)
+  int32_t* free_ids;  // [n_blocks]
+};
+
+// One row's range of columns without a block yet, and the shared block it writes into (-1).
+struct Row {
+  int L, c0, c1, shared;
+};
+__device__ __forceinline__ Row row_of(const Table& t, const int32_t* seq_lens, const int32_t* new_lens, int b, bool report) {
+  Row r{seq_lens[b], 0, 0, -1};
+  const int N = new_lens[b];
+  if (!length_ok(t, r.L) || !length_ok(t, N) || N < r.L) {
+    if (report) flag(t.status, MLA_DEVERR_SEQ_LEN);
+    r.L = 0;
+    return r;
+  }
+  r.c0 = (int)(((long long)r.L + kBT - 1) / kBT);
+  r.c1 = (int)(((long long)N + kBT - 1) / kBT);
+  if (N > r.L && r.L % kBT) {
+    const int32_t e = t.out[(size_t)b * t.C + r.L / kBT];
+    if (e < 0 || e >= t.n_blocks) {
+      if (report) flag(t.status, MLA_DEVERR_BLOCK);
+    } else if (__ldcg(t.refs + e) > 1) {
+      r.shared = e;
+    }
+  }
+  return r;
+}
+
+// One CTA; table and counts in place (t.out, t.refs).
+__global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_t* __restrict__ seq_lens,
+                                                           const int32_t* __restrict__ new_lens, ReserveWs ws,
+                                                           int32_t* copies) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // 1. writers of every shared block: how many, and the last one
+  for (int b = tid; b < t.B; b += kThreads) {
+    const Row r = row_of(t, seq_lens, new_lens, b, true);
+    if (r.shared >= 0) { ws.writers[r.shared] = 0; ws.last[r.shared] = -1; }
+  }
+  __syncthreads();
+  for (int b = tid; b < t.B; b += kThreads) {
+    const Row r = row_of(t, seq_lens, new_lens, b, false);
+    if (r.shared >= 0) { atomicAdd(ws.writers + r.shared, 1); atomicMax(ws.last + r.shared, b); }
+  }
+  __syncthreads();
+  // A writer copies while another holder is left: all but the last one when the writers are
+  // all the holders.
+  auto copies_block = [&](const Row& r, int b) {
+    return r.shared >= 0 && (__ldcg(t.refs + r.shared) > __ldcg(ws.writers + r.shared) || __ldcg(ws.last + r.shared) != b);
+  };
+  // 2. new blocks per row (long runs of columns: a warp per row), then their prefix sums
+  for (int b = tid; b < t.B; b += kThreads) {
+    const Row r = row_of(t, seq_lens, new_lens, b, false);
+    int need = copies_block(r, b) ? 1 : 0;
+    ws.copy[b] = need;
+    if (r.c1 - r.c0 <= kShortRow)
+      for (int j = r.c0; j < r.c1; ++j) need += entry(t, t.out[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+    ws.need[b] = need;
+  }
+  __syncthreads();
+  for (int b = warp; b < t.B; b += kThreads / 32) {
+    const int c0 = (int)(((long long)seq_lens[b] + kBT - 1) / kBT), c1 = (int)(((long long)new_lens[b] + kBT - 1) / kBT);
+    if (c1 - c0 <= kShortRow || !length_ok(t, seq_lens[b]) || !length_ok(t, new_lens[b])) continue;
+    int n = 0;
+    for (int j = c0 + lane; j < c1; j += 32) n += entry(t, t.out[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) ws.need[b] += n;
+  }
+  __syncthreads();
+  int total = 0, n_copies = 0;
+  for (int base = 0; base < t.B; base += kThreads) {
+    const int b = base + tid;
+    const int need = b < t.B ? ws.need[b] : 0, cp = b < t.B ? ws.copy[b] : 0;
+    int tot_n, tot_c;
+    const int ex_n = block_exscan(need, &tot_n, s_warp), ex_c = block_exscan(cp, &tot_c, s_warp);
+    if (b < t.B) {
+      ws.need[b] = total + ex_n;
+      ws.copy[b] = cp ? n_copies + ex_c : -1;
+    }
+    total += tot_n;
+    n_copies += tot_c;
+  }
+  // 3. the free blocks of lowest id
+  const int want = min(total, t.n_blocks);
+  int n_free = 0;
+  for (int base = 0; base < t.n_blocks; base += kTile) {
+    const uint32_t word = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c <= 0; });
+    int tot;
+    const int ex = block_exscan(__popc(word), &tot, s_warp);
+    list_bits(word, base + 32 * tid, ws.free_ids, n_free + ex, want);
+    n_free += tot;
+  }
+  const bool ok = total <= n_free;
+  if (tid == 0) {
+    t.status[0] = ok ? n_copies : 0;
+    t.status[2] = t.n_blocks - n_free + (ok ? total : 0);
+    t.status[3] = ok ? total : 0;
+    if (!ok) flag(t.status, MLA_DEVERR_POOL);
+  }
+  if (!ok) return;
+  // 4. counts, table and copy list.  Rows are independent: a row's new ids are free_ids[need[b] ...].
+  __syncthreads();
+  for (int b = tid; b < t.B; b += kThreads) {
+    // (not row_of: the counts change in this loop; copy[] and need[] carry what was decided)
+    int at = ws.need[b];
+    const int L = seq_lens[b], N = new_lens[b];
+    if (ws.copy[b] >= 0) {
+      int32_t* e = t.out + (size_t)b * t.C + L / kBT;
+      int32_t* c = copies + 3 * (size_t)ws.copy[b];
+      c[0] = *e; c[1] = ws.free_ids[at]; c[2] = L % kBT;
+      atomicSub(t.refs + *e, 1);
+      *e = ws.free_ids[at++];
+      t.refs[*e] = 1;
+    }
+    if (!length_ok(t, L) || !length_ok(t, N) || N < L) continue;
+    const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
+    if (c1 - c0 > kShortRow) continue;
+    for (int j = c0; j < c1; ++j) {
+      int32_t* e = t.out + (size_t)b * t.C + j;
+      if (*e >= 0 && *e < t.n_blocks) continue;
+      *e = ws.free_ids[at++];
+      t.refs[*e] = 1;
+    }
+  }
+  for (int b = warp; b < t.B; b += kThreads / 32) {
+    const int L = seq_lens[b], N = new_lens[b];
+    const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
+    if (c1 - c0 <= kShortRow || !length_ok(t, L) || !length_ok(t, N)) continue;
+    int at = ws.need[b] + (ws.copy[b] >= 0 ? 1 : 0);
+    for (int j0 = c0; j0 < c1; j0 += 32) {
+      const int j = j0 + lane;
+      int32_t* e = t.out + (size_t)b * t.C + min(j, c1 - 1);
+      const bool none = j < c1 && (*e < 0 || *e >= t.n_blocks);
+      const uint32_t m = __ballot_sync(0xffffffffu, none);
+      if (none) {
+        const int id = ws.free_ids[at + __popc(m & ((1u << lane) - 1))];
+        *e = id;
+        t.refs[id] = 1;
+      }
+      at += __popc(m);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ compact
+struct CompactWs {
+  int32_t* remap;   // [n_blocks] new id of every block in use
+  int32_t* holes;   // [n_blocks / 2] free ids below the number of blocks in use, ascending
+  int32_t* movers;  // [n_blocks / 2] ids in use from there on, ascending
+};
+
+// One CTA; the counts in place (t.refs).
+__global__ void __launch_bounds__(kThreads) compact_kernel(Table t, CompactWs ws, int32_t* copies) {
+  __shared__ int s_warp[32];
+  const int tid = threadIdx.x;
+  int live = 0;
+  for (int base = 0; base < t.n_blocks; base += kTile) {
+    const uint32_t word = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c > 0; });
+    int tot;
+    block_exscan(__popc(word), &tot, s_warp);
+    live += tot;
+  }
+  int n_holes = 0, n_movers = 0;
+  for (int base = 0; base < t.n_blocks; base += kTile) {
+    const uint32_t used = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c > 0; });
+    const int id0 = base + 32 * tid;
+    // bits below the border: ids id0 .. live - 1
+    const int below = max(0, min(32, live - id0)), in_pool = max(0, min(32, t.n_blocks - id0));
+    const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+    const uint32_t hole = ~used & lo & (in_pool == 32 ? 0xffffffffu : (1u << in_pool) - 1u), mover = used & ~lo;
+    int tot_h, tot_m;
+    const int ex_h = block_exscan(__popc(hole), &tot_h, s_warp), ex_m = block_exscan(__popc(mover), &tot_m, s_warp);
+    list_bits(hole, id0, ws.holes, n_holes + ex_h, t.n_blocks / 2);
+    list_bits(mover, id0, ws.movers, n_movers + ex_m, t.n_blocks / 2);
+    n_holes += tot_h;
+    n_movers += tot_m;
+  }
+  for (int i = tid; i < t.n_blocks; i += kThreads) ws.remap[i] = i < live ? i : -1;
+  __syncthreads();
+  const int n = n_movers;   // as many blocks in use behind the border as free ones before it
+  for (int k = tid; k < n; k += kThreads) {
+    const int from = ws.movers[k], to = ws.holes[k];
+    ws.remap[from] = to;
+    t.refs[to] = __ldcg(t.refs + from);
+    t.refs[from] = 0;
+    copies[3 * (size_t)k] = from; copies[3 * (size_t)k + 1] = to; copies[3 * (size_t)k + 2] = kBT;
+  }
+  if (tid == 0) {
+    t.status[0] = n;
+    t.status[2] = live;
+    t.status[3] = n;
+  }
+}
+
+// Entries follow their blocks; one that names a free block behind the border becomes -1.
+__global__ void __launch_bounds__(256) remap_kernel(Table t, const int32_t* __restrict__ remap) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)t.B * t.C) return;
+  const int id = entry(t, t.in[i]);
+  t.out[i] = id >= 0 ? remap[id] : -1;
+}
+
+// ------------------------------------------------------------------ copies
+struct CopyArgs {
+  const int32_t* copies;
+  int32_t max_copies, n_blocks;
+  int32_t* status;
+  char* base[3];        // c_kv, c_scales, k_rope (null: none)
+  uint32_t row[3];      // bytes per token row
+};
+constexpr int kCopyThreads = 256;
+constexpr uint32_t kChunk = 16384;   // bytes per CTA step
+
+// Work items: (copy, array, 16 KB chunk); a block's rows are contiguous in each array.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
+  const int n = min(a.status[0], a.max_copies);
+  uint32_t chunks[3], per = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    chunks[k] = a.base[k] ? (a.row[k] * kBT + kChunk - 1) / kChunk : 0;
+    per += chunks[k];
+  }
+  const long long items = (long long)n * per;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int32_t* c = a.copies + 3 * (it / per);
+    uint32_t chunk = (uint32_t)(it % per);
+    int k = 0;
+    while (chunk >= chunks[k]) chunk -= chunks[k++];
+    const int src = c[0], dst = c[1], rows = c[2];
+    if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_blocks || rows < 0 || rows > kBT) {
+      if (threadIdx.x == 0) flag(a.status, MLA_DEVERR_BLOCK);
+      continue;
+    }
+    const size_t block = (size_t)a.row[k] * kBT;
+    const uint32_t bytes = a.row[k] * rows, o0 = chunk * kChunk, o1 = min(bytes, o0 + kChunk);
+    const char* s = a.base[k] + block * src;
+    char* d = a.base[k] + block * dst;
+    const uint32_t v1 = o1 & ~15u;
+    for (uint32_t o = o0 + 16 * threadIdx.x; o < v1; o += 16 * kCopyThreads)
+      *reinterpret_cast<uint4*>(d + o) = *reinterpret_cast<const uint4*>(s + o);
+    // the end of the last row, where rows are not whole 16-byte units
+    for (uint32_t o = max(o0, v1) + threadIdx.x; o < o1; o += kCopyThreads) d[o] = s[o];
+  }
+}
+
+// ------------------------------------------------------------------ residual ring
+__global__ void __launch_bounds__(256) ring_kernel(mla_cache_t c, uint32_t row_bytes, const int32_t* __restrict__ src,
+                                                   const int32_t* __restrict__ dst, int n, int32_t* status) {
+  const int r = blockIdx.x;
+  if (r == 0) check_rows(dst, n, c.B, status);
+  const int i = pair_of(src, dst, n, r, c.B, status);
+  if (i < 0 || src[i] == r) return;
+  const size_t bytes = (size_t)row_bytes * MLA_RESID_WINDOW;   // a multiple of 16: 128 rows
+  const uint4* s = reinterpret_cast<const uint4*>((const char*)c.c_resid + bytes * src[i]);
+  uint4* d = reinterpret_cast<uint4*>((char*)c.c_resid + bytes * r);
+  for (size_t o = threadIdx.x; o < bytes / 16; o += blockDim.x) d[o] = s[o];
+  for (int o = threadIdx.x; o < MLA_RESID_WINDOW; o += blockDim.x)
+    c.resid_pos[(size_t)r * MLA_RESID_WINDOW + o] = c.resid_pos[(size_t)src[i] * MLA_RESID_WINDOW + o];
+}
+
+// ------------------------------------------------------------------ host side
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// True when [a, a + n) and [b, b + n) share bytes without being the same range.
+bool overlap(const void* a, const void* b, size_t n) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x != y && x < y + n && y < x + n;
+}
+
+bool sizes_ok(int32_t B, int32_t C, int32_t n_blocks) {
+  return B > 0 && C > 0 && n_blocks > 0 && C <= kMaxBlocks && n_blocks <= kMaxBlocks && (long long)B * C <= (1 << 30);
+}
+
+mla_status_t check_table(const int32_t* table, const int32_t* refs, int32_t B, int32_t C, int32_t n_blocks,
+                         const int32_t* table_out, const int32_t* refs_out, const int32_t* status) {
+  if (!table || !refs || !table_out || !refs_out || !status || !sizes_ok(B, C, n_blocks)) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(table) || !aligned4(refs) || !aligned4(table_out) || !aligned4(refs_out) || !aligned4(status))
+    return MLA_ERR_ALIGNMENT;
+  if (overlap(table, table_out, (size_t)B * C * 4) || overlap(refs, refs_out, (size_t)n_blocks * 4))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+
+cudaError_t copy_ints(int32_t* to, const int32_t* from, size_t n, cudaStream_t s) {
+  return to == from ? cudaSuccess : cudaMemcpyAsync(to, from, n * 4, cudaMemcpyDeviceToDevice, s);
+}
+
+// Workspace: two ints per row and three per block (reserve), two per block (compact).
+size_t workspace_ints(int32_t B, int32_t n_blocks) { return 2 * (size_t)B + 3 * (size_t)n_blocks; }
+
+}  // namespace blocks
+}  // namespace mla
+
+using namespace mla::blocks;
+
+extern "C" {
+
+size_t mla_blocks_workspace_bytes(int32_t B, int32_t n_cols, int32_t n_blocks) {
+  return sizes_ok(B, n_cols, n_blocks) ? (workspace_ints(B, n_blocks) * 4 + 255) & ~(size_t)255 : 0;
+}
+
+mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
+                             const int32_t* src, const int32_t* dst, int32_t n, const int32_t* seq_lens,
+                             int32_t* table_out, int32_t* refs_out, int32_t* status, void* stream) {
+  const mla_status_t st = check_table(table, refs, B, n_cols, n_blocks, table_out, refs_out, status);
+  if (st != MLA_OK) return st;
+  if (!src || !dst || !seq_lens || n <= 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(src) || !aligned4(dst) || !aligned4(seq_lens)) return MLA_ERR_ALIGNMENT;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = copy_ints(refs_out, refs, n_blocks, s);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  fork_kernel<<<B, 128, 0, s>>>(Table{table, table_out, refs_out, B, n_cols, n_blocks, status}, src, dst, n, seq_lens);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
+                                const int32_t* seq_lens, const int32_t* new_lens, int32_t* table_out,
+                                int32_t* refs_out, int32_t* copies, int32_t max_copies, int32_t* status,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  const mla_status_t st = check_table(table, refs, B, n_cols, n_blocks, table_out, refs_out, status);
+  if (st != MLA_OK) return st;
+  if (!seq_lens || !new_lens || !copies || !workspace || max_copies < B) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(copies) || ((uintptr_t)workspace & 15)) return MLA_ERR_ALIGNMENT;
+  if (ws_bytes < mla_blocks_workspace_bytes(B, n_cols, n_blocks)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = copy_ints(refs_out, refs, n_blocks, s);
+  if (e == cudaSuccess) e = copy_ints(table_out, table, (size_t)B * n_cols, s);
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  int32_t* w = (int32_t*)workspace;
+  ReserveWs ws;
+  ws.need = w; ws.copy = w + B;
+  ws.writers = w + 2 * (size_t)B; ws.last = ws.writers + n_blocks; ws.free_ids = ws.last + n_blocks;
+  reserve_kernel<<<1, kThreads, 0, s>>>(Table{table_out, table_out, refs_out, B, n_cols, n_blocks, status}, seq_lens,
+                                        new_lens, ws, copies);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_blocks_trim(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
+                             const int32_t* seq_lens, int32_t n_sink, int32_t window, int32_t* table_out,
+                             int32_t* refs_out, int32_t* status, void* stream) {
+  const mla_status_t st = check_table(table, refs, B, n_cols, n_blocks, table_out, refs_out, status);
+  if (st != MLA_OK) return st;
+  if (!seq_lens || n_sink < 0 || window < 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(seq_lens)) return MLA_ERR_ALIGNMENT;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (copy_ints(refs_out, refs, n_blocks, s) != cudaSuccess) return MLA_ERR_CUDA;
+  const unsigned grid = (unsigned)(((long long)B * n_cols + 255) / 256);
+  trim_kernel<<<grid, 256, 0, s>>>(Table{table, table_out, refs_out, B, n_cols, n_blocks, status}, seq_lens, n_sink, window);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_blocks_compact(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
+                                int32_t* table_out, int32_t* refs_out, int32_t* copies, int32_t max_copies,
+                                int32_t* status, void* workspace, size_t ws_bytes, void* stream) {
+  const mla_status_t st = check_table(table, refs, B, n_cols, n_blocks, table_out, refs_out, status);
+  if (st != MLA_OK) return st;
+  if (!copies || !workspace || max_copies < n_blocks / 2) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(copies) || ((uintptr_t)workspace & 15)) return MLA_ERR_ALIGNMENT;
+  if (ws_bytes < mla_blocks_workspace_bytes(B, n_cols, n_blocks)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (copy_ints(refs_out, refs, n_blocks, s) != cudaSuccess) return MLA_ERR_CUDA;
+  int32_t* w = (int32_t*)workspace;
+  CompactWs ws{w, w + n_blocks, w + n_blocks + n_blocks / 2};
+  const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
+  compact_kernel<<<1, kThreads, 0, s>>>(t, ws, copies);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return MLA_ERR_CUDA;
+  remap_kernel<<<(unsigned)(((long long)B * n_cols + 255) / 256), 256, 0, s>>>(t, ws.remap);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* copies,
+                             int32_t max_copies, int32_t* status, void* stream) {
+  mla_status_t st = mla_validate_config(cfg);
+  if (st != MLA_OK) return st;
+  if ((st = mla_validate_cache(*cfg, cache)) != MLA_OK) return st;
+  if (!cache->block_table || !copies || !status || max_copies <= 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(copies) || !aligned4(status)) return MLA_ERR_ALIGNMENT;
+  const bool quant = mla_kind_quant(cfg->cache_kind);
+  const uint32_t eb = cfg->dtype == MLA_F32 ? 4 : 2;
+  CopyArgs a;
+  a.copies = copies; a.max_copies = max_copies; a.n_blocks = cache->n_blocks; a.status = status;
+  a.base[0] = (char*)cache->c_kv;
+  a.row[0] = quant ? (uint32_t)(cfg->d_c * mla_quant_bits(cfg->cache_kind) / 8) : (uint32_t)cfg->d_c * eb;
+  a.base[1] = quant ? (char*)cache->c_scales : nullptr;
+  a.row[1] = quant ? (uint32_t)(cfg->d_c / 32 * 2) : 0;
+  a.base[2] = cfg->r_pairs > 0 ? (char*)cache->k_rope : nullptr;
+  a.row[2] = (uint32_t)(cfg->n_kv_heads * 2 * cfg->r_pairs) * eb;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  copy_kernel<<<4 * sms, kCopyThreads, 0, (cudaStream_t)stream>>>(a);
+  return cuda_status(cudaGetLastError());
+}
+
+mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src, const int32_t* dst,
+                           int32_t n, int32_t* status, void* stream) {
+  mla_status_t st = mla_validate_config(cfg);
+  if (st != MLA_OK) return st;
+  if ((st = mla_validate_cache(*cfg, cache)) != MLA_OK) return st;
+  if (!cache->c_resid || !src || !dst || !status || n <= 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned4(src) || !aligned4(dst) || !aligned4(status)) return MLA_ERR_ALIGNMENT;
+  ring_kernel<<<cache->B, 256, 0, (cudaStream_t)stream>>>(*cache, (uint32_t)cfg->d_c * 2, src, dst, n, status);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

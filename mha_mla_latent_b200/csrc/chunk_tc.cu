@@ -92,6 +92,7 @@ struct ChunkArgs {
   int NC, NK, NRAW;        // latent stages, RoPE-key stages, code stages
   uint32_t off_q, off_ar, off_p, off_c, off_k, off_raw, off_bar, off_misc;
   uint32_t c_stage, k_stage, raw_stage;
+  MlaWindow win;           // sliding window with sinks (the kernel's WIN form)
 };
 
 struct Bars {
@@ -127,19 +128,34 @@ struct Misc {
   int abort_flag;
 };
 
+// Walk over a worker's tiles: unit v, tokens [t0, t1) of the piece, tile start t.  With a
+// sliding window (WIN) these are tokens of the unit's span, and token() is the tile's first
+// cached token.
+template <bool WIN>
 struct TileIter {
+  const ChunkArgs* a;
   const Sched* s;
   int pc, pc_end;
   int v, t0, t1;
   int t;
-  __device__ void init(const Sched* sc, int w) {
-    s = sc;
-    pc = sc->worker_first[w];
-    pc_end = sc->worker_first[w + 1];
+  Span span;
+  __device__ void init(const ChunkArgs* args, int w) {
+    a = args;
+    s = &args->sched;
+    pc = s->worker_first[w];
+    pc_end = s->worker_first[w + 1];
     t = 0;
     if (pc < pc_end) load();
   }
-  __device__ void load() { v = s->piece_b[pc]; t0 = s->piece_t0[pc]; t1 = s->piece_t1[pc]; t = t0; }
+  __device__ void load() {
+    v = s->piece_b[pc]; t0 = s->piece_t0[pc]; t1 = s->piece_t1[pc]; t = t0;
+    if (WIN) span = unit_span(unit_len(a->seq_lens, v, a->q_chunk, a->qper), unit_queries(v, a->q_chunk, a->qper), kCT, a->win);
+  }
+  __device__ int token() const { return WIN ? span.token(t) : t; }
+  // Rows of this tile that no query of the unit sees, between the sinks and the window:
+  // [hidden_begin(), hidden_end()), empty when begin >= end.
+  __device__ int hidden_begin() const { return WIN ? max(0, a->win.n_sink - token()) : 0; }
+  __device__ int hidden_end() const { return WIN ? min(kCT, span.lo - token()) : 0; }
   __device__ bool valid() const { return pc < pc_end; }
   __device__ bool first_of_piece() const { return t == t0; }
   __device__ bool last_of_piece() const { return t + kCT >= t1; }
@@ -195,12 +211,14 @@ __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 1
 // ROWS: rows per unit (see Geo); QB: code width of a quantised latent cache (4 or 2),
 // whose rows warps 2-3 dequantise into the latent ring, 0 for a bf16 latent loaded by TMA;
 // RESID: the int4 cache's residual window (decode only: the window follows the one query's
-// length); PAGED: cache addressed through a block table.
+// length); PAGED: cache addressed through a block table; WIN: sliding window with sinks (the
+// walk leaves out the tiles between them, and each row masks the tokens its query does not
+// see).
 //
 // Rings: the latent tile of tile n sits in stage n % NC until MMA2(n) has read it; its RoPE
 // keys in stage n % NK, released after MMA1(n) when the RoPE scores run on the tensor cores
 // (a.rtc), else after MMA2(n) (the softmax warps read them).
-template <int ROWS, int QB, bool RESID, bool PAGED>
+template <int ROWS, int QB, bool RESID, bool PAGED, bool WIN>
 __global__ void __launch_bounds__(Crew<ROWS, QB>::WARPS * 32, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
                const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ ChunkArgs a) {
@@ -279,8 +297,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
       // Two cursors over the CTA's tiles: the latent (or code) ring with the query boxes, and
       // the RoPE-key ring, whose stages free up at different times; each copy is issued as
       // soon as its stage is free.
-      TileIter ic, ik;
-      ic.init(&a.sched, w);
+      TileIter<WIN> ic, ik;
+      ic.init(&a, w);
       ik = ic;
       int nc = 0, nk = 0, u = 0, q_loads = 0;
       bool ok = true;
@@ -299,7 +317,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
                 tma_load_2d(sbase_u32 + a.off_q + kb * kQBox, &tm_q, bars.q_full(), kb * 64, qrow0(ic.v));
               ++q_loads;
             }
-            const MlaLoc lc = chunk_loc<PAGED>(a, ic.v / a.nqb, ic.t);   // a 64-token tile lies in one block
+            const MlaLoc lc = chunk_loc<PAGED>(a, ic.v / a.nqb, ic.token());   // a 64-token tile lies in one block
             const int row = lc.pb * lc.cap + lc.pt;
             if (!QUANT) {   // latent boxes
               const uint32_t st = sbase_u32 + a.off_c + cs * a.c_stage;
@@ -319,7 +337,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
         if (ik.valid() && nk < nc) {   // keys never run ahead of their tile's latent copy
           const int ks = nk % a.NK;
           if (nk < a.NK || mbar_test(bars.k_empty(ks), ((nk / a.NK) - 1) & 1)) {
-            const MlaLoc lc = chunk_loc<PAGED>(a, ik.v / a.nqb, ik.t);
+            const MlaLoc lc = chunk_loc<PAGED>(a, ik.v / a.nqb, ik.token());
             const int row = lc.pb * lc.cap + lc.pt;
             const uint32_t st = sbase_u32 + a.off_k + ks * a.k_stage;
             mbar_expect_tx(bars.k_full(ks), (uint32_t)n_kbox * kTBox);
@@ -361,8 +379,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
     if (lane == 0) {
       const uint32_t idesc1 = idesc_bf16_f32(GG::M, kCT, false, false);   // S[row][t]
       const uint32_t idesc2 = idesc_bf16_f32(GG::M, dcp, false, true);    // O[row][d]
-      TileIter it;
-      it.init(&a.sched, w);
+      TileIter<WIN> it;
+      it.init(&a, w);
       int n = 0, u = 0;
       bool ok = true;
       int pend_n = -1, pend_u = 0;
@@ -452,28 +470,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
     // ============================================================ dequantisation
     // thread = token row of the tile (with four dequantising warps: a token row and the
     // groups of one parity): codes * scale -> bf16 into the latent stage's swizzled boxes;
-    // rows past the unit's last token are zeroed (MMA2 multiplies them by P = 0)
+    // rows past the unit's last token, and rows no query of the unit sees, are zeroed (MMA2
+    // multiplies them by P = 0)
     constexpr int NPART = Crew<ROWS, QB>::NDQ / 2;   // threads per token row
     const int dqt = Crew<ROWS, QB>::dq_index(warp) * 32 + lane;
     const int tok = dqt & 63, part = dqt >> 6;        // token row, group parity (NPART = 2)
-    TileIter it;
-    it.init(&a.sched, w);
+    TileIter<WIN> it;
+    it.init(&a, w);
     int n = 0;
     bool ok = true;
     int lo_v = -1, lo = INT_MAX;   // residual window (decode): tokens from lo on may sit in the ring
     // this token's group scales (up to 8 per token) come from global memory with plain loads,
     // issued two tiles ahead so their latency hides behind the dequantisation of two tiles
-    auto load_scales = [&](const TileIter& ti, __half (&sc)[8]) {
+    auto load_scales = [&](const TileIter<WIN>& ti, __half (&sc)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sc[j] = __float2half(0.f);
       if (!ti.valid() || tok >= ti.t1 - ti.t) return;
-      const MlaLoc lc = chunk_loc<PAGED>(a, ti.v / a.nqb, ti.t);
+      const MlaLoc lc = chunk_loc<PAGED>(a, ti.v / a.nqb, ti.token());
       const __half* sp = a.scales + ((size_t)lc.pb * lc.cap + lc.pt + tok) * (dc / 32);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (j < dc / 32) sc[j] = __ldg(sp + j);
     };
-    TileIter pf = it;
+    TileIter<WIN> pf = it;
     __half scl[8], scl1[8], scl2[8];   // tiles n, n + 1, n + 2
     load_scales(pf, scl);
     if (pf.valid()) pf.next();
@@ -493,18 +512,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
       const int nvalid = min(kCT, it.t1 - it.t);
       const uint8_t* raw = sbase + a.off_raw + rs * a.raw_stage;
       uint8_t* C = sbase + a.off_c + cs * a.c_stage;
-      const int tp = it.t + tok;
+      const int tp = it.token() + tok;
+      const bool live = tok < nvalid && !(WIN && tok >= it.hidden_begin() && tok < it.hidden_end());
       const size_t rslot = (size_t)it.v * MLA_RESID_WINDOW + (tp & (MLA_RESID_WINDOW - 1));
       // latent value j of the row goes to box j / 64, 16-byte chunk (j % 64) / 8 (swizzled)
       auto put = [&](int chunk, uint4 v) {
         *reinterpret_cast<uint4*>(C + (chunk >> 3) * kTBox + sw128(tok, chunk)) = v;
       };
-      if (RESID && tok < nvalid && tp >= lo && __ldg(a.cache.resid_pos + rslot) == tp) {
+      if (RESID && live && tp >= lo && __ldg(a.cache.resid_pos + rslot) == tp) {
         // one of the window's tokens: its unquantised row from the ring
         const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) +
                                                           rslot * dc);
         for (int j = part; j < dc / 8; j += NPART) put(j, __ldg(src + j));
-      } else if (tok < nvalid) {
+      } else if (live) {
         const uint8_t* codes = raw + tok * a.code_row;
         float svs[8];
 #pragma unroll
@@ -575,8 +595,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
     const int g = hd / (a.H / n_kv);
     float* xmax = reinterpret_cast<float*>(sbase + a.off_misc + 16);   // [2][2][2][16]
     float* xsum = xmax + 128;                                           // [2][2][16]
-    TileIter it;
-    it.init(&a.sched, w);
+    TileIter<WIN> it;
+    it.init(&a, w);
     int n = 0, u = 0;
     bool ok = true;
     float m = -INFINITY, l = 0.f;
@@ -627,7 +647,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
       if (lane == 0) mbar_arrive(bars.s_empty(sb));
       // RoPE score against the tile's keys: row tt of the swizzled key stage, KV head g's chunk
       const uint8_t* krb = sbase + a.off_k + ks * a.k_stage + (g >> 3) * kTBox;
-      const int lim_t = min(it.t1, p_row + 1) - it.t;   // tokens [0, lim_t) of the tile count
+      // tokens [0, lim_t) of the tile count; with a window those of them before sink_t or from
+      // win_t on
+      const int lim_t = min(it.t1 - it.t, p_row + 1 - it.token());
+      const int sink_t = WIN ? a.win.n_sink - it.token() : 0, win_t = WIN ? p_row + 1 - a.win.window - it.token() : 0;
       float mx = -INFINITY;
       {
         uint4 kw[16];   // all 16 keys in flight before the first use
@@ -639,7 +662,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
         for (int t = 0; t < 16; ++t) {
           const int tt = tb + t;
           float v = rope_dot8_bf16(s[t], qb, kw[t]);
-          v = tt < lim_t ? v : -INFINITY;
+          v = tt < lim_t && (!WIN || tt >= win_t || tt < sink_t) ? v : -INFINITY;
           s[t] = v;
           mx = fmaxf(mx, v);
         }
@@ -697,6 +720,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
           const int box = i / ((kCT - nvalid) * 8), rem = i % ((kCT - nvalid) * 8);
           *reinterpret_cast<uint4*>(C + box * kTBox + (nvalid + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
+      }
+      if (WIN && !QUANT && it.hidden_begin() < it.hidden_end()) {   // the same for rows no query of the unit sees
+        const int h0 = it.hidden_begin(), nh = it.hidden_end() - h0;
+        uint8_t* C = sbase + a.off_c + (n % a.NC) * a.c_stage;
+        for (int i = sidx; i < nh * 8 * n_cbox; i += 128)
+          *reinterpret_cast<uint4*>(C + i / (nh * 8) * kTBox + (h0 + i % (nh * 8) / 8) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
       }
       if (n >= 2) {
         ok = wwait(bars.p_empty(pb), ((n >> 1) - 1) & 1);
@@ -759,8 +788,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
     const int hd = r % a.H;                  // its head; its query is r / H of the unit
     const int n_kv = R / 8;
     const int g = hd / (a.H / n_kv);         // KV head of this row's head
-    TileIter it;
-    it.init(&a.sched, w);
+    TileIter<WIN> it;
+    it.init(&a, w);
     int n = 0, u = 0;
     bool ok = true;
     float m = -INFINITY, l = 0.f;
@@ -823,12 +852,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars.s_empty(sb));
-      const int lim_t = min(it.t1, p_row + 1) - it.t;   // tokens [0, lim_t) of the tile count
+      // tokens [0, lim_t) of the tile count; with a window those of them before sink_t or from
+      // win_t on
+      const int lim_t = min(it.t1 - it.t, p_row + 1 - it.token());
+      const int sink_t = WIN ? a.win.n_sink - it.token() : 0, win_t = WIN ? p_row + 1 - a.win.window - it.token() : 0;
       float mx = -INFINITY;
       if (rtc) {
 #pragma unroll
         for (int t = 0; t < TPL; ++t) {
-          const float v = t < lim_t ? s[t] : -INFINITY;
+          const float v = t < lim_t && (!WIN || t >= win_t || t < sink_t) ? s[t] : -INFINITY;
           s[t] = v;
           mx = fmaxf(mx, v);
         }
@@ -848,7 +880,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
           for (int t = 0; t < 16; ++t) {
             const int tt = t0 + t;
             float v = rope_dot8_bf16(s[tt], qb, kw[t]);
-            v = tt < lim_t ? v : -INFINITY;
+            v = tt < lim_t && (!WIN || tt >= win_t || tt < sink_t) ? v : -INFINITY;
             s[tt] = v;
             mx = fmaxf(mx, v);
           }
@@ -900,6 +932,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
           const int box = i / ((kCT - nvalid) * 8), rem = i % ((kCT - nvalid) * 8);
           *reinterpret_cast<uint4*>(C + box * kTBox + (nvalid + rem / 8) * 128 + (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
         }
+      }
+      if (WIN && !QUANT && it.hidden_begin() < it.hidden_end()) {   // the same for rows no query of the unit sees
+        const int h0 = it.hidden_begin(), nh = it.hidden_end() - h0;
+        uint8_t* C = sbase + a.off_c + (n % a.NC) * a.c_stage;
+        for (int i = r; i < nh * 8 * n_cbox; i += ROWS)
+          *reinterpret_cast<uint4*>(C + i / (nh * 8) * kTBox + (h0 + i % (nh * 8) / 8) * 128 + i % 8 * 16) = make_uint4(0, 0, 0, 0);
       }
       if (n >= 2) {
         ok = wwait(bars.p_empty(pb), ((n >> 1) - 1) & 1);
@@ -1003,7 +1041,7 @@ struct ChunkLayoutSmem {
 // The rings take what is left.  A key stage is free after MMA1 (RoPE scores on the tensor
 // cores) or once the softmax warps hold its keys in registers, a latent stage only after
 // MMA2, so the latent ring gets up to two stages more than the key ring.
-static ChunkLayoutSmem chunk_smem_rtc(int dc, int R, int qbits, int rows, bool rtc) {
+static ChunkLayoutSmem chunk_smem_rtc(int dc, int R, int qbits, int rows, bool rtc, int min_nk = 2, int nraw = 3) {
   const uint32_t budget = 232448 - 1024;
   const int dcp = (dc + 63) / 64 * 64;
   const int n_cbox = dcp / 64, n_kbox = (R + 63) / 64;
@@ -1012,13 +1050,13 @@ static ChunkLayoutSmem chunk_smem_rtc(int dc, int R, int qbits, int rows, bool r
   L.c_stage = (uint32_t)n_cbox * kTBox;
   L.k_stage = (uint32_t)n_kbox * kTBox;
   L.raw_stage = qbits ? (((uint32_t)kCT * (dc * qbits / 8)) + 127) & ~127u : 0;
-  L.NRAW = qbits ? 3 : 0;
+  L.NRAW = qbits ? nraw : 0;
   const uint32_t box = (uint32_t)rows * 128u;
   const uint32_t fixed = (uint32_t)(n_cbox + (rtc ? n_kbox : 0)) * box + 2 * box + L.NRAW * L.raw_stage;
   auto size = [&](int nc, int nk) {
     return fixed + nc * L.c_stage + nk * L.k_stage + 8 * (2 * nc + 2 * nk + 2 * L.NRAW + kFixedBars) + 16 + kXchgBytes + 256;
   };
-  int nc = 2, nk = 2;
+  int nc = 2, nk = min_nk;
   while (true) {   // the latent ring up to two stages ahead of the key ring, then alternately
     const bool want_c = nc < nk + 2;
     if (want_c && nc < 6 && size(nc + 1, nk) <= budget) { ++nc; continue; }
@@ -1042,6 +1080,19 @@ static ChunkLayoutSmem chunk_smem_rtc(int dc, int R, int qbits, int rows, bool r
   return L;
 }
 
+typedef decltype(&attn_tc_kernel<128, 0, false, false, false>) AttnKernel;
+
+template <bool WIN> static AttnKernel attn_kernel(int rows, int qbits, bool resid, bool paged) {
+  if (rows == 128)
+    return qbits == 4 ? (paged ? attn_tc_kernel<128, 4, false, true, WIN> : attn_tc_kernel<128, 4, false, false, WIN>)
+           : qbits == 2 ? (paged ? attn_tc_kernel<128, 2, false, true, WIN> : attn_tc_kernel<128, 2, false, false, WIN>)
+                        : (paged ? attn_tc_kernel<128, 0, false, true, WIN> : attn_tc_kernel<128, 0, false, false, WIN>);
+  return qbits == 4 ? (resid ? (paged ? attn_tc_kernel<32, 4, true, true, WIN> : attn_tc_kernel<32, 4, true, false, WIN>)
+                             : (paged ? attn_tc_kernel<32, 4, false, true, WIN> : attn_tc_kernel<32, 4, false, false, WIN>))
+         : qbits == 2 ? (paged ? attn_tc_kernel<32, 2, false, true, WIN> : attn_tc_kernel<32, 2, false, false, WIN>)
+                      : (paged ? attn_tc_kernel<32, 0, false, true, WIN> : attn_tc_kernel<32, 0, false, false, WIN>);
+}
+
 // The RoPE scores of a 128-row unit go to the tensor cores (block-diagonal query rows in
 // MMA1) when their operand leaves room for at least three latent and two key stages; else,
 // and always for 32 rows (whose MMA1 would double on mostly zero rows while only two
@@ -1050,7 +1101,9 @@ static ChunkLayoutSmem chunk_smem(int dc, int R, int qbits, int rows) {
   if (rows == 32) return chunk_smem_rtc(dc, R, qbits, rows, false);
   const ChunkLayoutSmem t = chunk_smem_rtc(dc, R, qbits, rows, true);
   if (t.total <= 232448 && t.NC >= 3 && t.NK >= 2) return t;
-  return chunk_smem_rtc(dc, R, qbits, rows, false);
+  const ChunkLayoutSmem n = chunk_smem_rtc(dc, R, qbits, rows, false);
+  if (n.total <= 232448) return n;
+  return chunk_smem_rtc(dc, R, qbits, rows, false, 1, 2);   // the widest quantised latents: shallow rings fit
 }
 
 }  // namespace chunk
@@ -1093,7 +1146,7 @@ bool mla_decode_t_supported(const mla_plan& p, const mla_cache_t& c) {
 
 cudaError_t mla_launch_chunk_tc(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, int B, int Q,
                                 const Sched& sched, const void* qlat, const float* qrope, float* opart,
-                                float* mlpart, int P, int G, cudaStream_t s, int rows) {
+                                float* mlpart, int P, int G, cudaStream_t s, int rows, MlaWindow win) {
   using namespace mla::chunk;
   const mla_config_t& cfg = p.cfg;
   const int dc = cfg.d_c, R = p.R, H = cfg.n_heads;
@@ -1130,17 +1183,9 @@ cudaError_t mla_launch_chunk_tc(const mla_plan& p, const mla_cache_t& c, const i
   a.off_q = L.off_q; a.off_ar = L.off_ar; a.off_p = L.off_p; a.off_c = L.off_c; a.off_k = L.off_k;
   a.off_raw = L.off_raw; a.off_bar = L.off_bar; a.off_misc = L.off_misc;
   a.c_stage = L.c_stage; a.k_stage = L.k_stage; a.raw_stage = L.raw_stage;
+  a.win = win;
   const bool paged = c.block_table != nullptr, resid = qbits == 4 && c.c_resid != nullptr;
-  decltype(&attn_tc_kernel<128, 0, false, false>) kern;
-  if (rows == 128)
-    kern = qbits == 4 ? (paged ? attn_tc_kernel<128, 4, false, true> : attn_tc_kernel<128, 4, false, false>)
-           : qbits == 2 ? (paged ? attn_tc_kernel<128, 2, false, true> : attn_tc_kernel<128, 2, false, false>)
-                        : (paged ? attn_tc_kernel<128, 0, false, true> : attn_tc_kernel<128, 0, false, false>);
-  else
-    kern = qbits == 4 ? (resid ? (paged ? attn_tc_kernel<32, 4, true, true> : attn_tc_kernel<32, 4, true, false>)
-                               : (paged ? attn_tc_kernel<32, 4, false, true> : attn_tc_kernel<32, 4, false, false>))
-           : qbits == 2 ? (paged ? attn_tc_kernel<32, 2, false, true> : attn_tc_kernel<32, 2, false, false>)
-                        : (paged ? attn_tc_kernel<32, 0, false, true> : attn_tc_kernel<32, 0, false, false>);
+  const AttnKernel kern = win.window > 0 ? attn_kernel<true>(rows, qbits, resid, paged) : attn_kernel<false>(rows, qbits, resid, paged);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L.total);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;

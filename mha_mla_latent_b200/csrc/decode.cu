@@ -40,6 +40,7 @@ struct AbsorbArgs {
   // many queries per sequence: query rows s = b * q_chunk + i sit at position
   // seq_lens[b] - q_chunk + i; the schedule runs over units of q_block queries (1, 1: decode)
   int q_chunk, q_block;
+  MlaWindow win;              // sliding window with sinks (window = 0: none)
 };
 
 constexpr int kAbsRows = 8;       // (b, h) rows per CTA, CUDA-core form: one per warp
@@ -64,7 +65,7 @@ __device__ __forceinline__ void absorb_body(const AbsorbArgs& a, int blk_id, flo
   if (blk_id == 0) {  // the split-K schedule
     const int nunits = a.q_chunk > 1 ? (a.B / a.q_chunk) * ((a.q_chunk + a.q_block - 1) / a.q_block) : a.B;
     build_schedule(a.seq_lens, nunits, a.T_cap, a.tile, a.G, a.sched, a.err, reinterpret_cast<int32_t*>(sm),
-                   a.sched_ints, a.q_chunk, a.q_block);
+                   a.sched_ints, a.q_chunk, a.q_block, a.win);
     return;
   }
   const int blk = blk_id - 1;
@@ -225,6 +226,7 @@ struct DecodeArgs {
   float* mlpart;    // [H][P][2]
   int P;            // piece capacity
   Sched sched;
+  MlaWindow win;    // sliding window with sinks (window = 0: none)
 };
 
 constexpr int kSimtTile = 32;
@@ -256,19 +258,26 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
     if (tid < H) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
     // residual window: tokens from lo on may be read unquantised from the ring
     const int lo = (INT4 && a.cache.c_resid) ? __ldg(a.seq_lens + b) - MLA_RESID_WINDOW : INT_MAX;
+    const Span span = a.win.window > 0 ? unit_span(__ldg(a.seq_lens + b), 1, kSimtTile, a.win) : Span();
     float O[kSimtMaxE];
 #pragma unroll
     for (int e = 0; e < kSimtMaxE; ++e) O[e] = 0.f;
     __syncthreads();
     for (int t = t0; t < t1; t += kSimtTile) {
       const int n = min(kSimtTile, t1 - t);
-      const MlaLoc lc = mla_loc(a.cache, b, t, a.err);   // a 32-token tile lies in one block
+      const int ta = span.token(t);                       // the tile's first cached token
+      const MlaLoc lc = mla_loc(a.cache, b, ta, a.err);   // a 32-token tile lies in one block
+      // tile rows [hid0, hid1) lie between the sinks and the window: neither read nor scored
+      const int hid0 = a.win.window > 0 ? max(0, a.win.n_sink - ta) : 0, hid1 = span.lo - ta;
+      auto hidden = [&](int tt) { return tt >= hid0 && tt < hid1; };
       const size_t slot0 = (size_t)lc.pb * lc.cap + lc.pt;
       for (int i = tid; i < n * dc; i += 256) {
         int tt = i / dc, cc = i % dc;
         float v;
-        if (INT4) {
-          const int tp = t + tt;
+        if (hidden(tt)) {
+          v = 0.f;
+        } else if (INT4) {
+          const int tp = ta + tt;
           const size_t rs = (size_t)b * MLA_RESID_WINDOW + (tp & (MLA_RESID_WINDOW - 1));
           if (tp >= lo && a.cache.resid_pos[rs] == tp) {
             v = __bfloat162float(((const __nv_bfloat16*)a.cache.c_resid)[rs * dc + cc]);
@@ -303,13 +312,15 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
         const float* rq = s_qrope + h * r2;
         const float* rk = s_kr + tt * (R + 1) + g * r2;
         for (int j = 0; j < r2; ++j) s += rq[j] * rk[j];
-        s_p[tt * H + h] = s;
+        s_p[tt * H + h] = hidden(tt) ? -INFINITY : s;
       }
       __syncthreads();
       if (tid < H) {
         float mx = s_m[tid];
         for (int tt = 0; tt < n; ++tt) mx = fmaxf(mx, s_p[tt * H + tid]);
-        float al = exp2f(s_m[tid] - mx);   // exp2(-inf) = 0 on the first tile
+        // exp2(-inf) = 0 on the first tile (a tile of the window's walk holds a visible token,
+        // so mx is finite)
+        float al = exp2f(s_m[tid] - mx);
         float l = s_l[tid] * al;
         for (int tt = 0; tt < n; ++tt) {
           float p = exp2f(s_p[tt * H + tid] - mx);
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(CombineArgs a) {
 // Arguments and shared memory of the absorption grid (block 0: the split-K schedule).
 template <typename T>
 void absorb_setup(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q, int B, void* ws,
-                  const DecodeLayout& L, AbsorbArgs* aa, size_t* smem, int* nblocks) {
+                  const DecodeLayout& L, MlaWindow win, AbsorbArgs* aa, size_t* smem, int* nblocks) {
   const mla_config_t& cfg = p.cfg;
   const int H = cfg.n_heads, G = H / cfg.n_kv_heads;
   char* base = (char*)ws;
@@ -587,6 +598,7 @@ void absorb_setup(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_le
   aa->sm_scale = cfg.softmax_scale > 0.0f ? cfg.softmax_scale : (float)(1.0 / sqrt((double)cfg.head_dim));
   aa->q_chunk = 1;
   aa->q_block = 1;
+  aa->win = win;
   {
     const int vecn = 16 / (int)sizeof(T);   // elements per 16-byte load
     aa->vec_ok = ((uintptr_t)q % 16 == 0) && cfg.d_c % vecn == 0 && cfg.head_dim % vecn == 0;
@@ -649,7 +661,7 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
     da.d_c = cfg.d_c; da.R = p.R; da.qlat = aa.qlat; da.qrope = aa.qrope;
     da.opart = (float*)(base + L.off_opart); da.mlpart = (float*)(base + L.off_mlpart);
     da.P = L.P;
-    da.sched = sched;
+    da.sched = sched; da.win = aa.win;
     size_t smem = sizeof(float) * ((size_t)H * cfg.d_c + H * 2 * cfg.r_pairs +
                                    kSimtTile * (cfg.d_c + 1) + kSimtTile * (p.R + 1) +
                                    kSimtTile * H + 3 * H);
@@ -663,7 +675,7 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
   } else if (L.kernel == 4) {
     e = mla_launch_chunk_tc(p, c, seq_lens, B, 1, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
                             (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, s,
-                            H <= 32 ? 32 : 128);
+                            H <= 32 ? 32 : 128, aa.win);
     if (e != cudaSuccess) return e;
   } else {
     e = mla_launch_decode_tc(p, c, seq_lens, B, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
@@ -676,11 +688,11 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
 template <typename T, bool INT4>
 cudaError_t launch_decode_t(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens,
                             const void* q, int B, void* out, void* ws, const DecodeLayout& L,
-                            cudaStream_t s) {
+                            cudaStream_t s, MlaWindow win) {
   AbsorbArgs aa;
   size_t smem_abs;
   int nblk;
-  absorb_setup<T>(p, c, seq_lens, q, B, ws, L, &aa, &smem_abs, &nblk);
+  absorb_setup<T>(p, c, seq_lens, q, B, ws, L, win, &aa, &smem_abs, &nblk);
   cudaError_t e = cudaFuncSetAttribute(absorb_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_abs);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
@@ -722,14 +734,14 @@ cudaError_t launch_step_t(const mla_plan& p, const mla_cache_t& c, const int32_t
   dim3 agrid;
   size_t smem_app = 0, smem_abs;
   int nabs;
-  absorb_setup<bf16>(p, c, seq_lens, q, B, ws, L, &sp.abs, &smem_abs, &nabs);
+  absorb_setup<bf16>(p, c, seq_lens, q, B, ws, L, MlaWindow(), &sp.abs, &smem_abs, &nabs);
   if (!mla_append_step_mma_form(p, x, seq_lens, B, c, &sp.app, &agrid, &smem_app)) {
     // no fused form for this shape: the append, then the decode, as separate launches
     cudaError_t e = mla_profile_event(p, kProfAppend, false, s);
     if (e == cudaSuccess) e = mla_launch_append_step(p, x, seq_lens, B, c, s);
     if (e == cudaSuccess) e = mla_profile_event(p, kProfAppend, true, s);
     if (e != cudaSuccess) return e;
-    return launch_decode_t<bf16, INT4>(p, c, seq_lens, q, B, out, ws, L, s);
+    return launch_decode_t<bf16, INT4>(p, c, seq_lens, q, B, out, ws, L, s, MlaWindow());
   }
   sp.n_abs = nabs;
   sp.app_gx = (int)agrid.x;
@@ -749,14 +761,14 @@ cudaError_t launch_step_t(const mla_plan& p, const mla_cache_t& c, const int32_t
 // with the schedule over (sequence, block of floor(128 / H) queries) units, the chunk
 // attention kernel, and the merge of the units' rows.
 cudaError_t launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q, int B,
-                         int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s) {
+                         int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s, MlaWindow win) {
   using bf16 = __nv_bfloat16;
   const mla_config_t& cfg = p.cfg;
   const int kQB = 128 / cfg.n_heads;   // queries per unit: a unit holds up to 128 (query, head) rows
   AbsorbArgs aa;
   size_t smem_abs;
   int nblk;
-  absorb_setup<bf16>(p, c, seq_lens, q, B * Q, ws, L, &aa, &smem_abs, &nblk);
+  absorb_setup<bf16>(p, c, seq_lens, q, B * Q, ws, L, win, &aa, &smem_abs, &nblk);
   aa.q_chunk = Q;
   aa.q_block = kQB;
   cudaError_t e = cudaFuncSetAttribute(absorb_kernel<bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_abs);
@@ -768,7 +780,7 @@ cudaError_t launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t*
   char* base = (char*)ws;
   const int units = B * ((Q + kQB - 1) / kQB);
   e = mla_launch_chunk_tc(p, c, seq_lens, B, Q, aa.sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
-                          (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, s, 128);
+                          (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, s, 128, win);
   if (e != cudaSuccess) return e;
   return launch_combine<bf16>(p, units, kQB * cfg.n_heads, kQB * cfg.n_kv_heads, Q, kQB, out, ws, L, aa.sched, s);
 }
@@ -840,8 +852,9 @@ DecodeLayout mla_chunk_layout(const mla_plan& p, int B, int Q) {
 }
 
 cudaError_t mla_launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
-                             int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s) {
-  return mla::launch_chunk(p, c, seq_lens, q, B, Q, out, ws, L, s);
+                             int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s,
+                             MlaWindow win) {
+  return mla::launch_chunk(p, c, seq_lens, q, B, Q, out, ws, L, s, win);
 }
 
 Sched mla_sched_view(const DecodeLayout& L, void* ws, int B) {
@@ -861,13 +874,13 @@ Sched mla_sched_view(const DecodeLayout& L, void* ws, int B) {
 
 cudaError_t mla_launch_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens,
                               const void* q, int B, void* out, void* ws, const DecodeLayout& L,
-                              cudaStream_t s) {
+                              cudaStream_t s, MlaWindow win) {
   using namespace mla;
   const bool quant = mla_kind_quant(p.cfg.cache_kind);   // int4 or int2 codes
   if (p.cfg.dtype == MLA_BF16)
-    return quant ? launch_decode_t<__nv_bfloat16, true>(p, c, seq_lens, q, B, out, ws, L, s)
-                : launch_decode_t<__nv_bfloat16, false>(p, c, seq_lens, q, B, out, ws, L, s);
-  return launch_decode_t<float, false>(p, c, seq_lens, q, B, out, ws, L, s);
+    return quant ? launch_decode_t<__nv_bfloat16, true>(p, c, seq_lens, q, B, out, ws, L, s, win)
+                : launch_decode_t<__nv_bfloat16, false>(p, c, seq_lens, q, B, out, ws, L, s, win);
+  return launch_decode_t<float, false>(p, c, seq_lens, q, B, out, ws, L, s, win);
 }
 
 cudaError_t mla_launch_step(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* x,
@@ -882,5 +895,5 @@ cudaError_t mla_launch_step(const mla_plan& p, const mla_cache_t& c, const int32
   if (e == cudaSuccess) e = mla_launch_append_step(p, x, seq_lens, B, c, s);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfAppend, true, s);
   if (e != cudaSuccess) return e;
-  return launch_decode_t<float, false>(p, c, seq_lens, q, B, out, ws, L, s);
+  return launch_decode_t<float, false>(p, c, seq_lens, q, B, out, ws, L, s, MlaWindow());
 }

@@ -56,9 +56,39 @@ __device__ __forceinline__ int unit_len(const int32_t* __restrict__ seq_lens, in
   return L < q_chunk ? -1 : L - q_chunk + min(q_chunk, (k + 1) * q_block);
 }
 
+// What a unit reads under a sliding window with sinks (MlaWindow): the whole tiles that hold
+// a token one of its queries sees.  Those are the sinks' tiles [0, head) and the tiles from
+// the first query's window on; the `gap` tokens between them (whole tiles) are left out.  The
+// schedule and the kernels' tile walk run over the span's own tokens x = 0 .. len - 1, which
+// stand for the cached tokens token(x).  Without a window gap = 0 and token(x) = x.
+struct Span {
+  int len = 0, head = 0, gap = 0;
+  int lo = 0;   // first token of the first query's window: no query of the unit sees [n_sink, lo)
+  __device__ int token(int x) const { return x < head ? x : x + gap; }
+};
+// `L` = unit_len, `nq` = queries of the unit (its last one sits at L - 1), valid lengths only.
+__device__ __forceinline__ Span unit_span(int L, int nq, int tile, MlaWindow win) {
+  Span s;
+  s.len = L;
+  if (win.window > 0) {   // n_sink and window are at most the cache's capacity: no overflow
+    s.lo = max(0, L - nq - win.window + 1);
+    s.head = (win.n_sink + tile - 1) / tile * tile;
+    s.gap = max(0, s.lo / tile * tile - s.head);
+    s.len = L - s.gap;
+  }
+  return s;
+}
+// Queries of unit v (see unit_len).
+__device__ __forceinline__ int unit_queries(int v, int q_chunk, int q_block) {
+  if (q_chunk <= 1) return 1;
+  const int nqb = (q_chunk + q_block - 1) / q_block;
+  return min(q_block, q_chunk - (v % nqb) * q_block);
+}
+
 __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int B, int T_cap,
                                       int tile, int G, Sched out, int32_t* err, int32_t* scratch,
-                                      int scratch_ints, int q_chunk = 1, int q_block = 1) {
+                                      int scratch_ints, int q_chunk = 1, int q_block = 1,
+                                      MlaWindow win = MlaWindow()) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x, nt = blockDim.x;
   const int Pcap = B + G;
@@ -88,6 +118,7 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
     if (b < B) {
       int L = unit_len(seq_lens, b, q_chunk, q_block);
       if (L < 0 || L > T_cap) { raise_error(err, MLA_DEVERR_SEQ_LEN); L = 0; }
+      L = unit_span(L, unit_queries(b, q_chunk, q_block), tile, win).len;
       nti = (L + tile - 1) / tile;
       s.seq_ntiles[b] = nti;
       if (seq_len) seq_len[b] = L;
@@ -149,6 +180,7 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
       if (e > c1) e = c1;
       int L = seq_len ? seq_len[b] : unit_len(seq_lens, b, q_chunk, q_block);
       if (L < 0 || L > T_cap) L = 0;
+      if (!seq_len) L = unit_span(L, unit_queries(b, q_chunk, q_block), tile, win).len;
       s.piece_b[pidx] = b;
       s.piece_t0[pidx] = (int)((t - s.seq_tile0[b]) * tile);
       s.piece_t1[pidx] = (int)min((long long)L, (e - s.seq_tile0[b]) * tile);

@@ -36,6 +36,8 @@ mla_status_t validate_config(const mla_config_t* c) {
 
 }  // namespace
 
+mla_status_t mla_validate_config(const mla_config_t* c) { return validate_config(c); }
+
 mla_status_t mla_validate_cache(const mla_config_t& cfg, const mla_cache_t* c) {
   if (!c || !c->c_kv || c->B <= 0 || c->T_cap <= 0) return MLA_ERR_INVALID_ARG;
   const bool quant = mla_kind_quant(cfg.cache_kind);
@@ -98,6 +100,17 @@ mla_status_t mla_pick_decode_kernel(const mla_plan& p, const mla_cache_t& c, int
       if (head_rows) *kernel = 4;
       else if (token_rows) *kernel = 2;
       break;
+  }
+  if (*kernel == 1 && (size_t)p.cfg.n_heads * p.cfg.d_c > 8192) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+mla_status_t mla_pick_window_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel) {
+  *kernel = 1;
+  if (p.opt_kernel == 2) return MLA_ERR_UNSUPPORTED;   // the token-row kernel has no window
+  if (p.opt_kernel != 1) {
+    if (mla_decode_t_supported(p, c)) *kernel = 4;
+    else if (p.opt_kernel == 3) return MLA_ERR_UNSUPPORTED;
   }
   if (*kernel == 1 && (size_t)p.cfg.n_heads * p.cfg.d_c > 8192) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
@@ -345,6 +358,14 @@ mla_status_t pick_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel) {
   return mla_pick_decode_kernel(p, c, kernel);
 }
 
+// The window arguments of a call, cut to the capacity (no position lies beyond it).
+MlaWindow window_of(const mla_cache_t& c, int32_t n_sink, int32_t window) {
+  MlaWindow w;
+  w.n_sink = std::min(n_sink, c.T_cap);
+  w.window = std::min(window, c.T_cap);
+  return w;
+}
+
 }  // namespace
 
 mla_status_t mla_decode_kernel_choice(const mla_plan_t* plan, const mla_cache_t* cache, int32_t* kernel) {
@@ -379,6 +400,42 @@ mla_status_t mla_decode(const mla_plan_t* plan, const mla_cache_t* cache, const 
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   return cuda_status(mla_launch_decode(*plan, *cache, seq_lens, q, B, out, workspace, L,
                                        (cudaStream_t)stream));
+}
+
+mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache, const int32_t* seq_lens,
+                               const void* q, int32_t B, int32_t n_sink, int32_t window, void* out, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  if (!plan || !seq_lens || !q || !out || !workspace || B <= 0 || n_sink < 0 || window <= 0) return MLA_ERR_INVALID_ARG;
+  mla_status_t st = mla_validate_cache(plan->cfg, cache);
+  if (st != MLA_OK) return st;
+  if (B > cache->B) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)seq_lens & 3))
+    return MLA_ERR_ALIGNMENT;
+  int kernel = 1;
+  if ((st = mla_pick_window_kernel(*plan, *cache, &kernel)) != MLA_OK) return st;
+  DecodeLayout L = mla_decode_layout(*plan, B, kernel);
+  if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_status(mla_launch_decode(*plan, *cache, seq_lens, q, B, out, workspace, L, (cudaStream_t)stream,
+                                       window_of(*cache, n_sink, window)));
+}
+
+mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* cache, const int32_t* seq_lens,
+                                     const void* q, int32_t B, int32_t Q, int32_t n_sink, int32_t window, void* out,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  if (!plan || !seq_lens || !q || !out || !workspace || B <= 0 || Q <= 0 || n_sink < 0 || window <= 0)
+    return MLA_ERR_INVALID_ARG;
+  if (Q == 1)
+    return mla_decode_window(plan, cache, seq_lens, q, B, n_sink, window, out, workspace, ws_bytes, stream);
+  mla_status_t st = mla_validate_cache(plan->cfg, cache);
+  if (st != MLA_OK) return st;
+  if (B > cache->B || Q > cache->T_cap) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)seq_lens & 3))
+    return MLA_ERR_ALIGNMENT;
+  if (!mla_chunk_supported(*plan, *cache) || plan->opt_kernel == 1 || plan->opt_kernel == 2) return MLA_ERR_UNSUPPORTED;
+  DecodeLayout L = mla_chunk_layout(*plan, B, Q);
+  if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  return cuda_status(mla_launch_chunk(*plan, *cache, seq_lens, q, B, Q, out, workspace, L, (cudaStream_t)stream,
+                                      window_of(*cache, n_sink, window)));
 }
 
 size_t mla_decode_chunk_workspace_bytes(const mla_plan_t* plan, int32_t B, int32_t Q) {

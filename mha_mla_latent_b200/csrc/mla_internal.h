@@ -47,8 +47,16 @@ inline __host__ __device__ bool mla_kind_int2(int kind) { return kind == MLA_CAC
 inline __host__ __device__ bool mla_kind_quant(int kind) { return mla_kind_int4(kind) || mla_kind_int2(kind); }
 inline __host__ __device__ int mla_quant_bits(int kind) { return mla_kind_int2(kind) ? 2 : 4; }
 
+// Sliding window with sinks: the query at position p sees the tokens t <= p with t < n_sink
+// or t > p - window.  window == 0: no window (every t <= p).
+struct MlaWindow {
+  int n_sink = 0, window = 0;
+};
+
 // Host validation of a cache view against a config (mla_api.cpp); MLA_OK when usable.
 mla_status_t mla_validate_cache(const mla_config_t& cfg, const mla_cache_t* c);
+// Host validation of a config (mla_api.cpp).
+mla_status_t mla_validate_config(const mla_config_t* c);
 
 // Largest token count the decode-step append path takes (its scratch is sized for it).
 constexpr int kAppMaxSmallTokens = 128;
@@ -161,13 +169,16 @@ bool mla_chunk_supported(const mla_plan& p, const mla_cache_t& c);
 // than 32 heads); rows = 32: one query's heads (decode with up to 32 heads)
 cudaError_t mla_launch_chunk_tc(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, int B, int Q,
                                 const Sched& sched, const void* qlat, const float* qrope, float* opart,
-                                float* mlpart, int P, int G, cudaStream_t s, int rows);
+                                float* mlpart, int P, int G, cudaStream_t s, int rows, MlaWindow win = MlaWindow());
 bool mla_decode_t_capable(const mla_plan& p);
 bool mla_decode_t_supported(const mla_plan& p, const mla_cache_t& c);
 // The decode kernel a call runs (layout kernel id 1, 2 or 4), or the status refusing the call.
 mla_status_t mla_pick_decode_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel);
+// The same for a decode with a sliding window (layout kernel id 1 or 4).
+mla_status_t mla_pick_window_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel);
 cudaError_t mla_launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
-                             int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s);
+                             int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s,
+                             MlaWindow win = MlaWindow());
 
 cudaError_t mla_launch_select_pairs(const mla_config_t& cfg, const void* q, const void* k, int T,
                                     int32_t* pair_idx, float* contrib, cudaStream_t s);
@@ -181,4 +192,4 @@ cudaError_t mla_launch_step(const mla_plan& p, const mla_cache_t& c, const int32
                             const void* q, int B, void* out, void* ws, const DecodeLayout& L, cudaStream_t s);
 cudaError_t mla_launch_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens,
                               const void* q, int B, void* out, void* ws, const DecodeLayout& L,
-                              cudaStream_t s);
+                              cudaStream_t s, MlaWindow win = MlaWindow());

@@ -1,0 +1,302 @@
+"""Sliding-window attention with sinks (mla_decode_window, mla_decode_chunk_window) against the
+definition in float64.
+
+Hidden tokens hold NaN in every cache array, so a kernel that reads one shows it.
+
+Tolerances (derived, not fitted): a bf16 rounding is off by at most u = 2^-8 of the value, its
+root mean square by u / sqrt(3) = 2.3e-3 of it.  An output passes at most five of them that are
+independent: the absorbed query (through scores of standard deviation about 1), the
+probabilities, a dequantised latent, the merged latent and the output itself, so its relative
+L2 error stays below sqrt(5) * 2.3e-3 = 5.1e-3; 1e-2 leaves a factor of two for scores with a
+larger spread.  Element by element an output of size up to 4 is off by at most a few u * 1:
+3e-2, the bound of the other parity tests.  float32: 2^-24 in place of 2^-8 in sums of at most
+a few hundred terms, below 1e-5.  A token too many or too few changes an output over at most a
+few hundred visible tokens by more than its share of the weight, 1 / 300, of an element of
+standard deviation 1 / sqrt(300) ... 1: the small windows below make that several times the
+bound.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.helpers import assert_close
+from tests.window_helpers import BLOCK, Layer, hidden_tokens, make_cache, store
+
+pytestmark = pytest.mark.gpu
+
+LAYERS = {
+    "tiny_f32": dict(dtype="f32", H=4, n_kv=4, d_h=32, r=2, d_c=32),
+    "gqa_f32_r3": dict(dtype="f32", H=6, n_kv=2, d_h=24, r=3, d_c=20),
+    "smollm": dict(H=9, n_kv=3, d_h=64, d_c=32),
+    "smollm_r128": dict(H=9, n_kv=3, d_h=64, d_c=32, cache="int4_r128"),
+    "llama_dc256": dict(d_c=256),
+    "llama_dc64": dict(d_c=64),
+    "llama_dc96": dict(d_c=96),
+    "llama_int4": dict(d_c=128, cache="int4"),
+    "llama_int4_dc256": dict(d_c=256, cache="int4"),
+    "llama_int2": dict(d_c=64, cache="int2"),
+    "llama_r128": dict(d_c=128, cache="int4_r128"),
+    "gqa64_int4": dict(H=64, n_kv=8, d_h=64, d_c=128, cache="int4"),
+    "gqa64": dict(H=64, n_kv=32, d_h=64, d_c=128),
+    "one_head_r13": dict(H=1, n_kv=1, d_h=64, r=13, d_c=64),
+    "nope": dict(H=8, n_kv=8, d_h=32, r=0, d_c=32),
+}
+WINDOWS = [(0, 1), (1, 1), (3, 5), (64, 64), (65, 63), (0, 128), (4, 200), (130, 300), (5000, 7), (0, 5000)]
+LENS = [1, 700, 0, 64, 65, 200, 513, 2, 331]
+
+
+def run_decode(mla, layer, cache, lens, q, n_sink, window, plan=None, out=None):
+    own = plan is None
+    plan = plan or layer.plan(mla)
+    out = torch.full_like(q, float("nan"), device="cuda") if out is None else out
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, q.shape[0]), dtype=torch.uint8, device="cuda")
+    mla.mla_decode_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(), out, ws,
+                          n_sink, window)
+    assert mla.mla_device_error(plan) == 0
+    if own:
+        plan.close()
+    return out
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["contiguous", "paged"])
+@pytest.mark.parametrize("name", list(LAYERS))
+def test_decode_window(name, paged):
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=1)
+    B, T_cap = len(LENS), 768
+    seqs = [layer.sequence(L) for L in LENS]
+    q = layer.queries(B)
+    plan = layer.plan(mla)
+    for n_sink, window in WINDOWS:
+        cache = make_cache(mla, layer, B, T_cap, paged, seed=n_sink + window)
+        for b, s in enumerate(seqs):
+            store(cache, b, s, hidden_tokens(LENS[b], LENS[b] - 1, n_sink, window))
+        got = run_decode(mla, layer, cache, LENS, q, n_sink, window, plan).double().cpu().numpy()
+        for b, L in enumerate(LENS):
+            if L == 0:
+                assert not got[b].any()
+                continue
+            ref = layer.reference(q[b], seqs[b], L - 1, n_sink, window).numpy()
+            assert_close(got[b], ref, layer.dtype, f"{name} sinks {n_sink} window {window} length {L}")
+    plan.close()
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_decode_window_kernels(kernel):
+    """Both kernels that have a window, over the same cache."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=128, cache="int4", seed=2)
+    lens = [1000, 77]
+    seqs = [layer.sequence(L) for L in lens]
+    q = layer.queries(2)
+    cache = make_cache(mla, layer, 2, 1024, True)
+    for b, s in enumerate(seqs):
+        store(cache, b, s, hidden_tokens(lens[b], lens[b] - 1, 10, 150))
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+    got = run_decode(mla, layer, cache, lens, q, 10, 150, plan).double().cpu().numpy()
+    for b, L in enumerate(lens):
+        assert_close(got[b], layer.reference(q[b], seqs[b], L - 1, 10, 150).numpy(), "bf16", f"kernel {kernel} {L}")
+    plan.close()
+
+
+@pytest.mark.parametrize("splits", [1, 7, 1000])
+def test_decode_window_splits(splits):
+    """Any number of workers over the visible tokens, the softmax scale of the config too."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=3, scale=0.05)
+    lens = [3000, 1, 700]
+    seqs = [layer.sequence(L) for L in lens]
+    q = layer.queries(3)
+    cache = make_cache(mla, layer, 3, 3008, False)
+    for b, s in enumerate(seqs):
+        store(cache, b, s, hidden_tokens(lens[b], lens[b] - 1, 70, 900))
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_SPLITS, splits)
+    got = run_decode(mla, layer, cache, lens, q, 70, 900, plan).double().cpu().numpy()
+    for b, L in enumerate(lens):
+        assert_close(got[b], layer.reference(q[b], seqs[b], L - 1, 70, 900).numpy(), "bf16", f"splits {splits} {L}")
+    plan.close()
+
+
+def test_full_window_is_decode():
+    """A window over everything is mla_decode's attention."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=128, seed=4)
+    lens = [900, 130, 1]
+    cache = make_cache(mla, layer, 3, 1024, True)
+    for b, L in enumerate(lens):
+        store(cache, b, layer.sequence(L))
+    q = layer.queries(3)
+    plan = layer.plan(mla)
+    got = run_decode(mla, layer, cache, lens, q, 0, 2 ** 31 - 1, plan)
+    sinks = run_decode(mla, layer, cache, lens, q, 2 ** 31 - 1, 1, plan)
+    ref = torch.empty_like(got)
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, 3), dtype=torch.uint8, device="cuda")
+    mla.mla_decode(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(), ref, ws)
+    torch.cuda.synchronize()
+    for x in (got, sinks):
+        assert_close(x.double().cpu().numpy(), ref.double().cpu().numpy(), "bf16")
+    plan.close()
+
+
+CHUNK_LAYERS = ["smollm", "llama_dc256", "llama_dc64", "llama_int4", "llama_int4_dc256", "llama_int2", "gqa64"]
+
+
+@pytest.mark.parametrize("Q", [1, 2, 5, 70])
+@pytest.mark.parametrize("name", CHUNK_LAYERS)
+def test_chunk_window(name, Q):
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=5)
+    lens = [700, 70, 200, 331]
+    B, T_cap = len(lens), 768
+    seqs = [layer.sequence(L) for L in lens]
+    q = layer.queries(B, Q)
+    plan = layer.plan(mla)
+    for k, (n_sink, window) in enumerate([(0, 1), (3, 5), (64, 64), (65, 130), (4, 300), (1000, 1), (0, 1000)]):
+        cache = make_cache(mla, layer, B, T_cap, k % 2 == 0, seed=k)
+        for b, s in enumerate(seqs):
+            store(cache, b, s, hidden_tokens(lens[b], lens[b] - Q, n_sink, window))
+        out = torch.full_like(q, float("nan"), device="cuda")
+        ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+        mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(),
+                                    out, ws, n_sink, window)
+        assert mla.mla_device_error(plan) == 0
+        got = out.double().cpu().numpy()
+        assert np.isfinite(got).all()
+        for b, L in enumerate(lens):
+            for i in sorted({0, Q // 2, Q - 1}):
+                ref = layer.reference(q[b, i], seqs[b], L - Q + i, n_sink, window).numpy()
+                assert_close(got[b, i], ref, "bf16", f"{name} Q {Q} query {i} sinks {n_sink} window {window} length {L}")
+    plan.close()
+
+
+def test_out_of_range_length():
+    """A length beyond the capacity is flagged and treated as empty; the others are computed."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=6)
+    cache = make_cache(mla, layer, 3, 256, False)
+    seq = layer.sequence(100)
+    for b in range(3):
+        store(cache, b, seq)
+    q = layer.queries(3)
+    plan = layer.plan(mla)
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, 3), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan"), device="cuda")
+    mla.mla_decode_window(plan, cache.struct, torch.tensor([257, 100, -1], dtype=torch.int32, device="cuda"), q.cuda(),
+                          out, ws, 4, 40)
+    assert mla.mla_device_error(plan) == mla.MLA_DEVERR_SEQ_LEN
+    got = out.double().cpu().numpy()
+    assert not got[0].any() and not got[2].any()
+    assert_close(got[1], layer.reference(q[1], seq, 99, 4, 40).numpy(), "bf16")
+    plan.close()
+
+
+def test_long_cache_offsets():
+    """Rows behind 2^32 bytes of every array of a paged cache, at positions near 2^20."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import LatentCache
+    layer = Layer(d_c=256, seed=7)
+    n_blocks, L, window = 70000, (1 << 20) - 30, 300
+    C = (1 << 20) // BLOCK
+    table = np.full((1, C), -1, dtype=np.int32)
+    table[0, -4:] = [69999, 66001, 69998, 3]
+    table[0, 0] = 69990
+    cache = LatentCache(layer.config(mla), 1, 1 << 20, "cuda", block_table=table, n_blocks=n_blocks)
+    assert cache.c_kv.numel() * 2 > 2 ** 32 and cache.k_rope.numel() * 2 > 2 ** 32
+    seq = layer.sequence(2 + window)          # the two sinks, then the window
+    tail = {k: v[2:] for k, v in seq.items() if k != "L"}
+    cache.set_latent_rows(0, 0, seq["c_kv"][:2])
+    cache.set_k_rope_tokens(0, 0, seq["kr"][:2])
+    cache.set_latent_rows(0, L - window, tail["c_kv"])
+    cache.set_k_rope_tokens(0, L - window, tail["kr"])
+    q = layer.queries(1)
+    got = run_decode(mla, layer, cache, [L], q, 2, window).double().cpu().numpy()
+    # the same tokens as a short sequence whose query is rotated at the far position
+    s = dict(c=seq["c"], kr=seq["kr"])
+    far = _reference_at(layer, q[0], s, L - 1)
+    assert_close(got[0], far.numpy(), "bf16")
+
+
+def _reference_at(layer, q, seq, p):
+    """Every row of `seq` visible, the query rotated at p."""
+    q = q.double().clone()
+    turned = q.clone()
+    for h in range(layer.H):
+        k = layer.pairs[h // (layer.H // layer.n_kv)]
+        ang = torch.from_numpy(p * 10000.0 ** (-2.0 * k / layer.d_h))
+        n = seq["c"].shape[0]
+        back = torch.from_numpy((n - 1) * 10000.0 ** (-2.0 * k / layer.d_h))   # what reference() turns by
+        d = ang - back
+        x, y = q[h, 2 * k], q[h, 2 * k + 1]
+        turned[h, 2 * k], turned[h, 2 * k + 1] = x * d.cos() - y * d.sin(), x * d.sin() + y * d.cos()
+    return layer.reference(turned, seq, seq["c"].shape[0] - 1, 0, seq["c"].shape[0])
+
+
+def test_graph_replay_and_two_streams():
+    """A captured call replayed over changed lengths, and two plans' calls at once on two streams."""
+    import mha_mla_latent_b200 as mla
+    layers = [Layer(d_c=64, seed=8), Layer(d_c=128, cache="int4", seed=9)]
+    L = 600
+    seqs = [layer.sequence(L) for layer in layers]
+    caches = [make_cache(mla, layer, 1, 640, True) for layer in layers]
+    for c, s in zip(caches, seqs):
+        store(c, 0, s)
+    plans = [layer.plan(mla) for layer in layers]
+    qs = [layer.queries(1).cuda() for layer in layers]
+    outs = [torch.empty_like(q) for q in qs]
+    wss = [torch.empty(mla.mla_decode_workspace_bytes(p, 1), dtype=torch.uint8, device="cuda") for p in plans]
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    call = lambda k: mla.mla_decode_window(plans[k], caches[k].struct, lens, qs[k], outs[k], wss[k], 3, 100)  # noqa: E731
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                call(k)
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        ref = layers[k].reference(qs[k][0].cpu(), seqs[k], L - 1, 3, 100).numpy()
+        assert_close(outs[k][0].double().cpu().numpy(), ref, "bf16", f"stream {k}")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for n in (600, 37, 471):
+        lens.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = layers[0].reference(qs[0][0].cpu(), seqs[0], n - 1, 3, 100).numpy()
+        assert_close(outs[0][0].double().cpu().numpy(), ref, "bf16", f"replay {n}")
+    for p in plans:
+        assert mla.mla_device_error(p) == 0
+        p.close()
+
+
+def test_refusals():
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=10)
+    plan = layer.plan(mla)
+    cache = make_cache(mla, layer, 2, 256, False)
+    lens = torch.full((2,), 100, dtype=torch.int32, device="cuda")
+    q = layer.queries(2).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, 2), dtype=torch.uint8, device="cuda")
+    call = lambda S, W, w=ws: mla.mla_decode_window(plan, cache.struct, lens, q, out, w, S, W, check=False)  # noqa: E731
+    assert call(0, 0) == mla.MLA_ERR_INVALID_ARG and call(-1, 4) == mla.MLA_ERR_INVALID_ARG
+    assert call(0, -5) == mla.MLA_ERR_INVALID_ARG
+    assert call(0, 4, ws[:256]) == mla.MLA_ERR_WORKSPACE_TOO_SMALL
+    qc = q.unsqueeze(1).expand(2, 300, 32, 128).contiguous()
+    oc = torch.empty_like(qc)
+    chunk = lambda q_, W: mla.mla_decode_chunk_window(plan, cache.struct, lens, q_, oc, ws, 0, W, check=False)  # noqa: E731
+    assert chunk(qc, 4) == mla.MLA_ERR_INVALID_ARG                       # Q > T_cap
+    assert chunk(qc[:, :8].contiguous(), 0) == mla.MLA_ERR_INVALID_ARG
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, 2)
+    assert call(0, 4) == mla.MLA_ERR_UNSUPPORTED
+    assert chunk(qc[:, :8].contiguous(), 4) == mla.MLA_ERR_UNSUPPORTED
+    plan.close()
+    with pytest.raises(mla.MlaError):
+        ring = Layer(d_c=128, cache="int4_r128", seed=11)
+        rp = ring.plan(mla)
+        rc = make_cache(mla, ring, 2, 256, False)
+        mla.mla_decode_chunk_window(rp, rc.struct, lens, qc[:, :8].contiguous(), oc, ws, 0, 4)
