@@ -124,9 +124,15 @@ def _ptr(t):
     raise TypeError(type(t))
 
 
+# torch's current stream of the current device as a raw handle (torch.cuda.current_stream()
+# builds a Stream object each time: about 1.5 us of a call's host time)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -273,9 +279,8 @@ def mla_decode_chunk(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, s
 def mla_decode_window(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, n_sink, window, stream=None,
                       check=True):
     """mla_decode over the first n_sink tokens and the newest `window` tokens of each sequence."""
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = _lib.mla_decode_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), int(q.shape[0]),
-                                int(n_sink), int(window), _ptr(out), _ptr(workspace), ws_bytes, _stream(stream))
+    st = _lib.mla_decode_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), q.shape[0], n_sink, window,
+                                _ptr(out), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_decode_window")
     return st
@@ -285,10 +290,8 @@ def mla_decode_chunk_window(plan: Plan, cache: MlaCache, seq_lens, q, out, works
                             check=True):
     """mla_decode_chunk with each query seeing the first n_sink tokens and the `window` tokens
     up to its own: q and out are [B][Q][H][d_h]."""
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = _lib.mla_decode_chunk_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), int(q.shape[0]),
-                                      int(q.shape[1]), int(n_sink), int(window), _ptr(out), _ptr(workspace), ws_bytes,
-                                      _stream(stream))
+    st = _lib.mla_decode_chunk_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), q.shape[0], q.shape[1],
+                                      n_sink, window, _ptr(out), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_decode_chunk_window")
     return st
@@ -298,43 +301,43 @@ def mla_blocks_workspace_bytes(B: int, n_cols: int, n_blocks: int) -> int:
     return int(_lib.mla_blocks_workspace_bytes(int(B), int(n_cols), int(n_blocks)))
 
 
-def _int32(**tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
-        if t.device.type != "cuda":
-            raise ValueError(f"{name} must be a device tensor")
+_I32 = torch.int32
 
 
-def _table_args(table, refs, table_out, refs_out, status, seq_lens=None):
-    """Checks the block table's tensors and returns (B, n_cols, n_blocks)."""
-    _int32(table=table, refs=refs, table_out=table_out, refs_out=refs_out, status=status)
-    if table.dim() != 2 or refs.dim() != 1 or table_out.shape != table.shape or refs_out.shape != refs.shape:
-        raise ValueError("table is [B][n_cols], refs [n_blocks]; table_out and refs_out have their shapes")
+def _i32(t, name, shape=None):
+    """Device pointer of a contiguous int32 device tensor (of the given shape, where one is given)."""
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be a contiguous int32 device tensor"
+                         + (f" of shape {list(shape)}" if shape is not None else ""))
+    return t.data_ptr()
+
+
+def _table(table, refs):
+    """Pointers and sizes of a block table [B][n_cols] and its holder counts [n_blocks]."""
+    if table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table is [B][n_cols], refs is [n_blocks]")
+    B, C = table.shape
+    return _i32(table, "table"), _i32(refs, "refs"), B, C, refs.shape[0]
+
+
+def _block_status(status):
     if status.numel() < MLA_BLOCKS_STATUS_INTS:
         raise ValueError(f"status holds {MLA_BLOCKS_STATUS_INTS} int32")
-    if seq_lens is not None:
-        _int32(seq_lens=seq_lens)
-        if seq_lens.numel() != table.shape[0]:
-            raise ValueError("a length per table row is needed")
-    return int(table.shape[0]), int(table.shape[1]), int(refs.shape[0])
+    return _i32(status, "status")
 
 
-def _n_copies(copies) -> int:
-    _int32(copies=copies)
+def _block_copies(copies):
     if copies.dim() != 2 or copies.shape[1] != 3:
         raise ValueError("copies is [max_copies][3]")
-    return int(copies.shape[0])
+    return _i32(copies, "copies"), copies.shape[0]
 
 
 def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status, stream=None, check=True):
     """Row dst[i] of the table shares the blocks of row src[i] (its first seq_lens[src[i]] tokens)."""
-    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
-    _int32(src=src, dst=dst)
-    if src.numel() != dst.numel():
-        raise ValueError("src and dst have one entry per pair")
-    st = _lib.mla_blocks_fork(_ptr(table), _ptr(refs), B, C, n, _ptr(src), _ptr(dst), int(src.numel()), _ptr(seq_lens),
-                              _ptr(table_out), _ptr(refs_out), _ptr(status), _stream(stream))
+    t, r, B, C, n = _table(table, refs)
+    st = _lib.mla_blocks_fork(t, r, B, C, n, _i32(src, "src"), _i32(dst, "dst", src.shape), src.numel(),
+                              _i32(seq_lens, "seq_lens", (B,)), _i32(table_out, "table_out", (B, C)),
+                              _i32(refs_out, "refs_out", (n,)), _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_blocks_fork")
     return st
@@ -343,14 +346,11 @@ def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status
 def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, copies, status, workspace, stream=None,
                        check=True):
     """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence, shared partial blocks copied on write."""
-    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
-    _int32(new_lens=new_lens)
-    if new_lens.numel() != B:
-        raise ValueError("a new length per table row is needed")
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = _lib.mla_blocks_reserve(_ptr(table), _ptr(refs), B, C, n, _ptr(seq_lens), _ptr(new_lens), _ptr(table_out),
-                                 _ptr(refs_out), _ptr(copies), _n_copies(copies), _ptr(status), _ptr(workspace),
-                                 ws_bytes, _stream(stream))
+    t, r, B, C, n = _table(table, refs)
+    cp, n_cp = _block_copies(copies)
+    st = _lib.mla_blocks_reserve(t, r, B, C, n, _i32(seq_lens, "seq_lens", (B,)), _i32(new_lens, "new_lens", (B,)),
+                                 _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)), cp, n_cp,
+                                 _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_blocks_reserve")
     return st
@@ -358,9 +358,10 @@ def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, cop
 
 def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, status, stream=None, check=True):
     """Releases the blocks without a token among the first n_sink or the newest `window` ones."""
-    B, C, n = _table_args(table, refs, table_out, refs_out, status, seq_lens)
-    st = _lib.mla_blocks_trim(_ptr(table), _ptr(refs), B, C, n, _ptr(seq_lens), int(n_sink), int(window),
-                              _ptr(table_out), _ptr(refs_out), _ptr(status), _stream(stream))
+    t, r, B, C, n = _table(table, refs)
+    st = _lib.mla_blocks_trim(t, r, B, C, n, _i32(seq_lens, "seq_lens", (B,)), n_sink, window,
+                              _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)),
+                              _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_blocks_trim")
     return st
@@ -368,10 +369,10 @@ def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, 
 
 def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspace, stream=None, check=True):
     """Moves the blocks in use to the lowest ids; `copies` lists the moves."""
-    B, C, n = _table_args(table, refs, table_out, refs_out, status)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = _lib.mla_blocks_compact(_ptr(table), _ptr(refs), B, C, n, _ptr(table_out), _ptr(refs_out), _ptr(copies),
-                                 _n_copies(copies), _ptr(status), _ptr(workspace), ws_bytes, _stream(stream))
+    t, r, B, C, n = _table(table, refs)
+    cp, n_cp = _block_copies(copies)
+    st = _lib.mla_blocks_compact(t, r, B, C, n, _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)),
+                                 cp, n_cp, _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_blocks_compact")
     return st
@@ -379,9 +380,8 @@ def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspa
 
 def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None, check=True):
     """Moves the listed rows in one layer's cache (run it once per layer)."""
-    _int32(status=status)
-    st = _lib.mla_blocks_copy(ctypes.byref(cfg), ctypes.byref(cache), _ptr(copies), _n_copies(copies), _ptr(status),
-                              _stream(stream))
+    cp, n_cp = _block_copies(copies)
+    st = _lib.mla_blocks_copy(ctypes.byref(cfg), ctypes.byref(cache), cp, n_cp, _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_blocks_copy")
     return st
@@ -389,11 +389,8 @@ def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None
 
 def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True):
     """Copies the residual windows of sequences src to sequences dst in one layer's cache."""
-    _int32(src=src, dst=dst, status=status)
-    if src.numel() != dst.numel():
-        raise ValueError("src and dst have one entry per pair")
-    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _ptr(src), _ptr(dst), int(src.numel()),
-                            _ptr(status), _stream(stream))
+    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src"), _i32(dst, "dst", src.shape),
+                            src.numel(), _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_ring_copy")
     return st

@@ -37,104 +37,144 @@ __device__ __forceinline__ int entry(const Table& t, int32_t e) {
 __device__ __forceinline__ bool length_ok(const Table& t, int L) { return L >= 0 && (long long)L <= (long long)t.C * kBT; }
 
 // The pair that writes row r (the first i with dst[i] == r), or -1: none, or a pair to skip.
-// Whole CTA; flags what is skipped.
-__device__ int pair_of(const int32_t* src, const int32_t* dst, int n, int r, int rows, int32_t* status) {
-  __shared__ int s_first, s_count, s_written;
-  if (threadIdx.x == 0) { s_first = INT_MAX; s_count = 0; s_written = 0; }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x)
+// Whole warp; flags what is skipped.
+__device__ __forceinline__ int pair_of(const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n, int r,
+                                       int rows, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  int first = INT_MAX, count = 0;
+  for (int i = lane; i < n; i += 32)
     if (dst[i] == r) {
-      atomicMin(&s_first, i);
-      atomicAdd(&s_count, 1);
+      first = min(first, i);
+      ++count;
     }
-  __syncthreads();
-  const int i = s_first == INT_MAX ? -1 : s_first;
-  if (i < 0) return -1;
-  if (s_count > 1 && threadIdx.x == 0) flag(status, MLA_DEVERR_ROW);
-  const int s = src[i];
-  bool ok = s >= 0 && s < rows;
-  if (ok && s != r)   // a source that another pair rewrites
-    for (int j = threadIdx.x; j < n; j += blockDim.x)
-      if (dst[j] == s && src[j] != s) s_written = 1;
-  __syncthreads();
-  ok = ok && !s_written;
-  if (!ok && threadIdx.x == 0) flag(status, MLA_DEVERR_ROW);
-  return ok ? i : -1;
+  first = __reduce_min_sync(0xffffffffu, first);
+  if (first == INT_MAX) return -1;
+  count = __reduce_add_sync(0xffffffffu, count);
+  const int s = src[first];
+  bool bad = s < 0 || s >= rows;
+  if (!bad && s != r) {   // a source that another pair rewrites
+    bool written = false;
+    for (int j = lane; j < n; j += 32) written |= dst[j] == s && src[j] != s;
+    bad = __any_sync(0xffffffffu, written);
+  }
+  if ((bad || count > 1) && lane == 0) flag(status, MLA_DEVERR_ROW);
+  return bad ? -1 : first;
 }
 
-// Destinations outside the table (no row looks for them).
-__device__ void check_rows(const int32_t* dst, int n, int rows, int32_t* status) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x)
+// Destinations outside the table (no row looks for them); the whole grid takes part.
+__device__ void check_rows(const int32_t* __restrict__ dst, int n, int rows, int32_t* status, int thread, int threads) {
+  for (int i = thread; i < n; i += threads)
     if (dst[i] < 0 || dst[i] >= rows) flag(status, MLA_DEVERR_ROW);
 }
 
-// ------------------------------------------------------------------ fork
-// One CTA per table row.
-__global__ void __launch_bounds__(128) fork_kernel(Table t, const int32_t* __restrict__ src,
-                                                   const int32_t* __restrict__ dst, int n,
-                                                   const int32_t* __restrict__ seq_lens) {
-  const int r = blockIdx.x;
-  if (r == 0) check_rows(dst, n, t.B, t.status);
-  int i = pair_of(src, dst, n, r, t.B, t.status);
-  int cols = 0, s = 0;
-  if (i >= 0) {
-    s = src[i];
-    const int L = seq_lens[s];
-    if (!length_ok(t, L)) {
-      if (threadIdx.x == 0) flag(t.status, MLA_DEVERR_SEQ_LEN);
-      i = -1;
-    }
-    cols = (int)(((long long)L + kBT - 1) / kBT);
+// ------------------------------------------------------------------ clusters
+// The bookkeeping kernels run as one cluster of 8 CTAs: enough threads for tables and counts
+// of some hundred thousand entries, with a barrier in hardware between the phases (the counts
+// are copied before any thread changes one, say), so that a call is a single launch.
+constexpr int kCluster = 8;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void copy_ints(int32_t* out, const int32_t* in, long long n, int thread, int threads) {
+  if (out == in) return;
+  if ((((uintptr_t)out | (uintptr_t)in) & 15) == 0) {
+    const long long n4 = n / 4;
+    for (long long i = thread; i < n4; i += threads)
+      reinterpret_cast<int4*>(out)[i] = __ldg(reinterpret_cast<const int4*>(in) + i);
+    for (long long i = 4 * n4 + thread; i < n; i += threads) out[i] = __ldg(in + i);
+  } else {
+    for (long long i = thread; i < n; i += threads) out[i] = __ldg(in + i);
   }
-  const int32_t* row = t.in + (size_t)r * t.C;
-  const int32_t* from = t.in + (size_t)s * t.C;
-  int32_t* out = t.out + (size_t)r * t.C;
-  for (int j = threadIdx.x; j < t.C; j += blockDim.x) {
-    const int32_t old = row[j];
-    if (i < 0) {
-      if (t.out != t.in) out[j] = old;
-      continue;
+}
+
+// ------------------------------------------------------------------ fork
+// A warp per table row.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+fork_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
+            const int32_t* __restrict__ seq_lens) {
+  pdl_wait();
+  pdl_trigger();
+  const int thread = blockIdx.x * kThreads + threadIdx.x, lane = threadIdx.x & 31;
+  copy_ints(t.refs, refs_in, t.n_blocks, thread, kCluster * kThreads);
+  check_rows(dst, n, t.B, t.status, thread, kCluster * kThreads);
+  cluster_sync();
+  for (int r = thread / 32; r < t.B; r += kCluster * kThreads / 32) {
+    int i = pair_of(src, dst, n, r, t.B, t.status), cols = 0, s = 0;
+    if (i >= 0) {
+      s = src[i];
+      const int L = seq_lens[s];
+      if (!length_ok(t, L)) {
+        if (lane == 0) flag(t.status, MLA_DEVERR_SEQ_LEN);
+        i = -1;
+      }
+      cols = (int)(((long long)L + kBT - 1) / kBT);
     }
-    const int was = entry(t, old), now = j < cols ? entry(t, from[j]) : -1;
-    if (was >= 0) atomicSub(t.refs + was, 1);
-    if (now >= 0) atomicAdd(t.refs + now, 1);
-    out[j] = now;
+    if (i < 0 && t.out == t.in) continue;
+    const int32_t* row = t.in + (size_t)r * t.C;
+    const int32_t* from = t.in + (size_t)s * t.C;
+    int32_t* out = t.out + (size_t)r * t.C;
+    for (int j = lane; j < t.C; j += 32) {
+      int32_t now = row[j];
+      if (i >= 0) {
+        const int was = entry(t, now);
+        now = j < cols ? entry(t, from[j]) : -1;
+        if (was != now) {   // (a row cut to its own length keeps most of its blocks)
+          if (was >= 0) atomicSub(t.refs + was, 1);
+          if (now >= 0) atomicAdd(t.refs + now, 1);
+        }
+      }
+      out[j] = now;
+    }
   }
 }
 
 // ------------------------------------------------------------------ trim
-__global__ void __launch_bounds__(256) trim_kernel(Table t, const int32_t* __restrict__ seq_lens, int n_sink,
-                                                   int window) {
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (long long)t.B * t.C) return;
-  const int b = (int)(i / t.C);
-  const long long t0 = (i - (long long)b * t.C) * kBT, L = seq_lens[b];
-  int32_t e = t.in[i];
-  if (!length_ok(t, (int)L)) {
-    flag(t.status, MLA_DEVERR_SEQ_LEN);
-  } else {
-    const bool keep = t0 < min((long long)n_sink, L) || (window > 0 && t0 < L && t0 + kBT > L - window);
-    const int id = entry(t, e);
-    if (!keep) {
-      if (id >= 0) atomicSub(t.refs + id, 1);
-      e = -1;
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+trim_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_lens, int n_sink, int window) {
+  pdl_wait();
+  pdl_trigger();
+  const int thread = blockIdx.x * kThreads + threadIdx.x;
+  copy_ints(t.refs, refs_in, t.n_blocks, thread, kCluster * kThreads);
+  cluster_sync();
+  const int n = t.B * t.C;   // at most 2^30
+  for (int i = thread; i < n; i += kCluster * kThreads) {
+    const int b = i / t.C;
+    const int32_t e = t.in[i];
+    const long long t0 = (long long)(i - b * t.C) * kBT, L = seq_lens[b];
+    if (!length_ok(t, (int)L)) {
+      flag(t.status, MLA_DEVERR_SEQ_LEN);
+    } else {
+      const int id = entry(t, e);
+      const bool keep = t0 < min((long long)n_sink, L) || (window > 0 && t0 < L && t0 + kBT > L - window);
+      if (!keep) {
+        if (id >= 0) atomicSub(t.refs + id, 1);
+        t.out[i] = -1;
+        continue;
+      }
     }
+    if (t.out != t.in) t.out[i] = e;
   }
-  t.out[i] = e;
 }
 
 // ------------------------------------------------------------------ passes over the counts
-// Bit i of the returned word: `pick(id, count)` of id = base + 32 * threadIdx.x + i (false past
+// Bit i of the returned word: `pick(count)` of id = base + 32 * threadIdx.x + i (false past
 // the pool).  Warp w reads its 1024 ids in 32 coalesced loads; lane k keeps the k-th ballot.
 template <typename F>
 __device__ __forceinline__ uint32_t count_word(const int32_t* refs, int n_blocks, int base, F pick) {
   const int lane = threadIdx.x & 31, w0 = base + (threadIdx.x >> 5) * 1024;
   uint32_t word = 0;
-#pragma unroll 8
-  for (int k = 0; k < 32; ++k) {
-    const int id = w0 + 32 * k + lane;
-    const uint32_t m = __ballot_sync(0xffffffffu, id < n_blocks && pick(id, __ldcg(refs + min(id, n_blocks - 1))));
-    if (lane == k) word = m;
+  if (w0 >= n_blocks) return 0;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 32 && w0 + 32 * k0 < n_blocks; k0 += 16) {
+    int32_t c[16];   // 16 loads in flight
+#pragma unroll
+    for (int k = 0; k < 16; ++k) c[k] = __ldcg(refs + min(w0 + 32 * (k0 + k) + lane, n_blocks - 1));
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, w0 + 32 * (k0 + k) + lane < n_blocks && pick(c[k]));
+      if (lane == k0 + k) word = m;
+    }
   }
   return word;
 }
@@ -152,15 +192,18 @@ struct ReserveWs {
   int32_t* need;    // [B] new blocks of earlier rows
   int32_t* copy;    // [B] index of the row's copy in the list, -1: none
   int32_t* writers; // [n_blocks] rows that write into a shared block ...
-  int32_t* last;    // [n_blocks] ... and the last of them (valid at shared blocks only)
+  int32_t* last;    // [n_blocks] ... and the last of them (valid at shared blocks only; more than kThreads rows)
   int32_t* free_ids;  // [n_blocks]
 };
+constexpr int kSharedIds = 4096;   // new ids kept in shared memory (more of them: in the workspace)
 
-// One row's range of columns without a block yet, and the shared block it writes into (-1).
+// One row: its columns [c0, c1) that tokens [L, N) start, and the shared block that they write
+// into (-1: none).  A row with bad lengths is an empty one.
 struct Row {
   int L, c0, c1, shared;
 };
-__device__ __forceinline__ Row row_of(const Table& t, const int32_t* seq_lens, const int32_t* new_lens, int b, bool report) {
+__device__ __forceinline__ Row row_of(const Table& t, const int32_t* refs, const int32_t* seq_lens,
+                                      const int32_t* new_lens, int b, bool report) {
   Row r{seq_lens[b], 0, 0, -1};
   const int N = new_lens[b];
   if (!length_ok(t, r.L) || !length_ok(t, N) || N < r.L) {
@@ -171,57 +214,96 @@ __device__ __forceinline__ Row row_of(const Table& t, const int32_t* seq_lens, c
   r.c0 = (int)(((long long)r.L + kBT - 1) / kBT);
   r.c1 = (int)(((long long)N + kBT - 1) / kBT);
   if (N > r.L && r.L % kBT) {
-    const int32_t e = t.out[(size_t)b * t.C + r.L / kBT];
+    const int32_t e = t.in[(size_t)b * t.C + r.L / kBT];
     if (e < 0 || e >= t.n_blocks) {
       if (report) flag(t.status, MLA_DEVERR_BLOCK);
-    } else if (__ldcg(t.refs + e) > 1) {
+    } else if (refs[e] > 1) {
       r.shared = e;
     }
   }
   return r;
 }
 
-// One CTA; table and counts in place (t.out, t.refs).
-__global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_t* __restrict__ seq_lens,
-                                                           const int32_t* __restrict__ new_lens, ReserveWs ws,
-                                                           int32_t* copies) {
+// CTA 0 decides while the others copy the table and the counts (calls that are not in place);
+// after the cluster's barrier CTA 0 writes what changes.  Decisions read the input only.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_lens,
+               const int32_t* __restrict__ new_lens, ReserveWs ws, int32_t* copies) {
   __shared__ int s_warp[32];
+  __shared__ __align__(16) int32_t s_ids[kSharedIds];   // the writers' shared blocks, then the new ids
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // 1. writers of every shared block: how many, and the last one
-  for (int b = tid; b < t.B; b += kThreads) {
-    const Row r = row_of(t, seq_lens, new_lens, b, true);
-    if (r.shared >= 0) { ws.writers[r.shared] = 0; ws.last[r.shared] = -1; }
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x != 0) {
+    const int thread = (blockIdx.x - 1) * kThreads + tid, threads = (kCluster - 1) * kThreads;
+    copy_ints(t.refs, refs_in, t.n_blocks, thread, threads);
+    copy_ints(t.out, t.in, (long long)t.B * t.C, thread, threads);
+    cluster_sync();
+    return;
+  }
+  // the first kThreads rows stay in registers, one per thread
+  Row mine{0, 0, 0, -1};
+  if (tid < t.B) mine = row_of(t, refs_in, seq_lens, new_lens, tid, true);
+  auto row = [&](int b) { return b == tid ? mine : row_of(t, refs_in, seq_lens, new_lens, b, false); };
+  // 1. A writer of a shared block copies while another holder is left: every writer when there
+  // are other holders, else all but the last one.
+  bool my_copy = false;
+  if (t.B <= kThreads) {   // compared in shared memory
+    s_ids[tid] = mine.shared;
+    __syncthreads();
+    if (mine.shared >= 0) {
+      int writers = 0, later = 0;
+      for (int j = 0; j < t.B; j += 4) {   // entries past B are -1
+        const int4 v = *reinterpret_cast<const int4*>(s_ids + j);
+        const int w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          writers += w[k] == mine.shared;
+          later += w[k] == mine.shared && j + k > tid;
+        }
+      }
+      my_copy = refs_in[mine.shared] > writers || later > 0;
+    }
+  } else {                 // counted in the workspace
+    for (int b = tid; b < t.B; b += kThreads) {
+      const Row r = b == tid ? mine : row_of(t, refs_in, seq_lens, new_lens, b, true);
+      if (r.shared >= 0) { ws.writers[r.shared] = 0; ws.last[r.shared] = -1; }
+    }
+    __syncthreads();
+    for (int b = tid; b < t.B; b += kThreads) {
+      const Row r = row(b);
+      if (r.shared >= 0) { atomicAdd(ws.writers + r.shared, 1); atomicMax(ws.last + r.shared, b); }
+    }
   }
   __syncthreads();
-  for (int b = tid; b < t.B; b += kThreads) {
-    const Row r = row_of(t, seq_lens, new_lens, b, false);
-    if (r.shared >= 0) { atomicAdd(ws.writers + r.shared, 1); atomicMax(ws.last + r.shared, b); }
-  }
-  __syncthreads();
-  // A writer copies while another holder is left: all but the last one when the writers are
-  // all the holders.
   auto copies_block = [&](const Row& r, int b) {
-    return r.shared >= 0 && (__ldcg(t.refs + r.shared) > __ldcg(ws.writers + r.shared) || __ldcg(ws.last + r.shared) != b);
+    if (t.B <= kThreads) return my_copy;
+    return r.shared >= 0 && (refs_in[r.shared] > __ldcg(ws.writers + r.shared) || __ldcg(ws.last + r.shared) != b);
   };
   // 2. new blocks per row (long runs of columns: a warp per row), then their prefix sums
+  bool any_long = false;
   for (int b = tid; b < t.B; b += kThreads) {
-    const Row r = row_of(t, seq_lens, new_lens, b, false);
+    const Row r = row(b);
     int need = copies_block(r, b) ? 1 : 0;
     ws.copy[b] = need;
     if (r.c1 - r.c0 <= kShortRow)
-      for (int j = r.c0; j < r.c1; ++j) need += entry(t, t.out[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+      for (int j = r.c0; j < r.c1; ++j) need += entry(t, t.in[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+    else
+      any_long = true;
     ws.need[b] = need;
   }
-  __syncthreads();
-  for (int b = warp; b < t.B; b += kThreads / 32) {
-    const int c0 = (int)(((long long)seq_lens[b] + kBT - 1) / kBT), c1 = (int)(((long long)new_lens[b] + kBT - 1) / kBT);
-    if (c1 - c0 <= kShortRow || !length_ok(t, seq_lens[b]) || !length_ok(t, new_lens[b])) continue;
-    int n = 0;
-    for (int j = c0 + lane; j < c1; j += 32) n += entry(t, t.out[(size_t)b * t.C + j]) < 0 ? 1 : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) ws.need[b] += n;
+  any_long = __syncthreads_or(any_long);
+  if (any_long) {
+    for (int b = warp; b < t.B; b += kThreads / 32) {
+      const Row r = row_of(t, refs_in, seq_lens, new_lens, b, false);
+      if (r.c1 - r.c0 <= kShortRow) continue;
+      int n = 0;
+      for (int j = r.c0 + lane; j < r.c1; j += 32) n += entry(t, t.in[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) ws.need[b] += n;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   int total = 0, n_copies = 0;
   for (int base = 0; base < t.B; base += kThreads) {
     const int b = base + tid;
@@ -237,12 +319,13 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_
   }
   // 3. the free blocks of lowest id
   const int want = min(total, t.n_blocks);
+  int32_t* ids = want <= kSharedIds ? s_ids : ws.free_ids;
   int n_free = 0;
   for (int base = 0; base < t.n_blocks; base += kTile) {
-    const uint32_t word = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c <= 0; });
+    const uint32_t word = count_word(refs_in, t.n_blocks, base, [](int32_t c) { return c <= 0; });
     int tot;
     const int ex = block_exscan(__popc(word), &tot, s_warp);
-    list_bits(word, base + 32 * tid, ws.free_ids, n_free + ex, want);
+    list_bits(word, base + 32 * tid, ids, n_free + ex, want);
     n_free += tot;
   }
   const bool ok = total <= n_free;
@@ -252,20 +335,21 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_
     t.status[3] = ok ? total : 0;
     if (!ok) flag(t.status, MLA_DEVERR_POOL);
   }
+  cluster_sync();   // the output holds the input's values, and the ids are listed
   if (!ok) return;
-  // 4. counts, table and copy list.  Rows are independent: a row's new ids are free_ids[need[b] ...].
-  __syncthreads();
+  // 4. counts, table and copy list.  Rows are independent: row b's new ids are ids[need[b] ...].
   for (int b = tid; b < t.B; b += kThreads) {
-    // (not row_of: the counts change in this loop; copy[] and need[] carry what was decided)
+    // (not row_of: in place the counts change in this loop; copy[] and need[] carry what was decided)
     int at = ws.need[b];
     const int L = seq_lens[b], N = new_lens[b];
     if (ws.copy[b] >= 0) {
       int32_t* e = t.out + (size_t)b * t.C + L / kBT;
       int32_t* c = copies + 3 * (size_t)ws.copy[b];
-      c[0] = *e; c[1] = ws.free_ids[at]; c[2] = L % kBT;
-      atomicSub(t.refs + *e, 1);
-      *e = ws.free_ids[at++];
-      t.refs[*e] = 1;
+      const int old = *e, id = ids[at++];
+      c[0] = old; c[1] = id; c[2] = L % kBT;
+      atomicSub(t.refs + old, 1);
+      t.refs[id] = 1;
+      *e = id;
     }
     if (!length_ok(t, L) || !length_ok(t, N) || N < L) continue;
     const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
@@ -273,10 +357,12 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_
     for (int j = c0; j < c1; ++j) {
       int32_t* e = t.out + (size_t)b * t.C + j;
       if (*e >= 0 && *e < t.n_blocks) continue;
-      *e = ws.free_ids[at++];
-      t.refs[*e] = 1;
+      const int id = ids[at++];
+      *e = id;
+      t.refs[id] = 1;
     }
   }
+  if (!any_long) return;
   for (int b = warp; b < t.B; b += kThreads / 32) {
     const int L = seq_lens[b], N = new_lens[b];
     const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
@@ -288,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(Table t, const int32_
       const bool none = j < c1 && (*e < 0 || *e >= t.n_blocks);
       const uint32_t m = __ballot_sync(0xffffffffu, none);
       if (none) {
-        const int id = ws.free_ids[at + __popc(m & ((1u << lane) - 1))];
+        const int id = ids[at + __popc(m & ((1u << lane) - 1))];
         *e = id;
         t.refs[id] = 1;
       }
@@ -304,55 +390,66 @@ struct CompactWs {
   int32_t* movers;  // [n_blocks / 2] ids in use from there on, ascending
 };
 
-// One CTA; the counts in place (t.refs).
-__global__ void __launch_bounds__(kThreads) compact_kernel(Table t, CompactWs ws, int32_t* copies) {
+// CTA 0 lists the moves while the others copy the counts (a call that is not in place) and set
+// every other block's new id; after the cluster's barrier CTA 0 moves the counts, and after
+// another one the table entries follow their blocks.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+compact_kernel(Table t, const int32_t* refs_in, CompactWs ws, int32_t* copies) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x;
-  int live = 0;
-  for (int base = 0; base < t.n_blocks; base += kTile) {
-    const uint32_t word = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c > 0; });
-    int tot;
-    block_exscan(__popc(word), &tot, s_warp);
-    live += tot;
+  pdl_wait();
+  pdl_trigger();
+  int n_movers = 0;
+  if (blockIdx.x != 0) {
+    const int thread = (blockIdx.x - 1) * kThreads + tid, threads = (kCluster - 1) * kThreads;
+    copy_ints(t.refs, refs_in, t.n_blocks, thread, threads);
+    for (int i = thread; i < t.n_blocks; i += threads) ws.remap[i] = i;
+  } else {
+    auto in_use = [](int32_t c) { return c > 0; };
+    const uint32_t first = count_word(refs_in, t.n_blocks, 0, in_use);
+    int live = 0;
+    for (int base = 0; base < t.n_blocks; base += kTile) {
+      int tot;
+      block_exscan(__popc(base ? count_word(refs_in, t.n_blocks, base, in_use) : first), &tot, s_warp);
+      live += tot;
+    }
+    int n_holes = 0;
+    for (int base = 0; base < t.n_blocks; base += kTile) {
+      const uint32_t used = base ? count_word(refs_in, t.n_blocks, base, in_use) : first;
+      const int id0 = base + 32 * tid;
+      // bits below the border: ids id0 .. live - 1 (all of them in the pool)
+      const int below = max(0, min(32, live - id0));
+      const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
+      const uint32_t hole = ~used & lo, mover = used & ~lo;
+      int tot_h, tot_m;
+      const int ex_h = block_exscan(__popc(hole), &tot_h, s_warp), ex_m = block_exscan(__popc(mover), &tot_m, s_warp);
+      list_bits(hole, id0, ws.holes, n_holes + ex_h, t.n_blocks / 2);
+      list_bits(mover, id0, ws.movers, n_movers + ex_m, t.n_blocks / 2);
+      n_holes += tot_h;
+      n_movers += tot_m;
+    }
+    if (tid == 0) {   // as many blocks in use behind the border as free ones before it
+      t.status[0] = n_movers;
+      t.status[2] = live;
+      t.status[3] = n_movers;
+    }
   }
-  int n_holes = 0, n_movers = 0;
-  for (int base = 0; base < t.n_blocks; base += kTile) {
-    const uint32_t used = count_word(t.refs, t.n_blocks, base, [](int, int32_t c) { return c > 0; });
-    const int id0 = base + 32 * tid;
-    // bits below the border: ids id0 .. live - 1
-    const int below = max(0, min(32, live - id0)), in_pool = max(0, min(32, t.n_blocks - id0));
-    const uint32_t lo = below == 32 ? 0xffffffffu : (1u << below) - 1u;
-    const uint32_t hole = ~used & lo & (in_pool == 32 ? 0xffffffffu : (1u << in_pool) - 1u), mover = used & ~lo;
-    int tot_h, tot_m;
-    const int ex_h = block_exscan(__popc(hole), &tot_h, s_warp), ex_m = block_exscan(__popc(mover), &tot_m, s_warp);
-    list_bits(hole, id0, ws.holes, n_holes + ex_h, t.n_blocks / 2);
-    list_bits(mover, id0, ws.movers, n_movers + ex_m, t.n_blocks / 2);
-    n_holes += tot_h;
-    n_movers += tot_m;
+  cluster_sync();
+  if (blockIdx.x == 0) {
+    for (int k = tid; k < n_movers; k += kThreads) {
+      const int from = ws.movers[k], to = ws.holes[k];
+      ws.remap[from] = to;
+      t.refs[to] = __ldcg(t.refs + from);
+      t.refs[from] = 0;
+      copies[3 * (size_t)k] = from; copies[3 * (size_t)k + 1] = to; copies[3 * (size_t)k + 2] = kBT;
+    }
   }
-  for (int i = tid; i < t.n_blocks; i += kThreads) ws.remap[i] = i < live ? i : -1;
-  __syncthreads();
-  const int n = n_movers;   // as many blocks in use behind the border as free ones before it
-  for (int k = tid; k < n; k += kThreads) {
-    const int from = ws.movers[k], to = ws.holes[k];
-    ws.remap[from] = to;
-    t.refs[to] = __ldcg(t.refs + from);
-    t.refs[from] = 0;
-    copies[3 * (size_t)k] = from; copies[3 * (size_t)k + 1] = to; copies[3 * (size_t)k + 2] = kBT;
+  cluster_sync();
+  const int n = t.B * t.C;   // at most 2^30
+  for (int i = blockIdx.x * kThreads + tid; i < n; i += kCluster * kThreads) {
+    const int id = entry(t, t.in[i]);
+    t.out[i] = id >= 0 ? __ldcg(ws.remap + id) : -1;
   }
-  if (tid == 0) {
-    t.status[0] = n;
-    t.status[2] = live;
-    t.status[3] = n;
-  }
-}
-
-// Entries follow their blocks; one that names a free block behind the border becomes -1.
-__global__ void __launch_bounds__(256) remap_kernel(Table t, const int32_t* __restrict__ remap) {
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (long long)t.B * t.C) return;
-  const int id = entry(t, t.in[i]);
-  t.out[i] = id >= 0 ? remap[id] : -1;
 }
 
 // ------------------------------------------------------------------ copies
@@ -363,12 +460,15 @@ struct CopyArgs {
   char* base[3];        // c_kv, c_scales, k_rope (null: none)
   uint32_t row[3];      // bytes per token row
 };
-constexpr int kCopyThreads = 256;
-constexpr uint32_t kChunk = 16384;   // bytes per CTA step
+constexpr int kCopyThreads = 256, kCopyCtas = 4;             // threads, CTAs per SM
+constexpr int kCopyVec = 8;                                  // 16-byte loads a thread has in flight
+constexpr uint32_t kChunk = kCopyThreads * kCopyVec * 16;    // bytes per CTA step: 32 KB
 
-// Work items: (copy, array, 16 KB chunk); a block's rows are contiguous in each array.
+// Work items: (copy, array, chunk); a block's rows are contiguous in each array.  Bound by HBM.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
-  const int n = min(a.status[0], a.max_copies);
+  pdl_wait();
+  pdl_trigger();
+  const int n = min(__ldcg(a.status), a.max_copies);
   uint32_t chunks[3], per = 0;
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -387,23 +487,38 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
       continue;
     }
     const size_t block = (size_t)a.row[k] * kBT;
-    const uint32_t bytes = a.row[k] * rows, o0 = chunk * kChunk, o1 = min(bytes, o0 + kChunk);
+    const uint32_t bytes = a.row[k] * rows, o0 = chunk * kChunk;
+    if (o0 >= bytes) continue;
+    const uint32_t o1 = min(bytes, o0 + kChunk), v1 = o1 & ~15u;
     const char* s = a.base[k] + block * src;
     char* d = a.base[k] + block * dst;
-    const uint32_t v1 = o1 & ~15u;
-    for (uint32_t o = o0 + 16 * threadIdx.x; o < v1; o += 16 * kCopyThreads)
-      *reinterpret_cast<uint4*>(d + o) = *reinterpret_cast<const uint4*>(s + o);
-    // the end of the last row, where rows are not whole 16-byte units
-    for (uint32_t o = max(o0, v1) + threadIdx.x; o < o1; o += kCopyThreads) d[o] = s[o];
+    const uint32_t o = o0 + 16 * threadIdx.x;
+    uint4 v[kCopyVec];
+#pragma unroll
+    for (int j = 0; j < kCopyVec; ++j)
+      if (o + j * 16 * kCopyThreads < v1) v[j] = __ldcs(reinterpret_cast<const uint4*>(s + o + j * 16 * kCopyThreads));
+#pragma unroll
+    for (int j = 0; j < kCopyVec; ++j)
+      if (o + j * 16 * kCopyThreads < v1) __stcs(reinterpret_cast<uint4*>(d + o + j * 16 * kCopyThreads), v[j]);
+    // the end of the last row, where rows are not whole 16-byte units (fewer than 16 bytes)
+    if (v1 + threadIdx.x < o1) d[v1 + threadIdx.x] = s[v1 + threadIdx.x];
   }
 }
 
 // ------------------------------------------------------------------ residual ring
 __global__ void __launch_bounds__(256) ring_kernel(mla_cache_t c, uint32_t row_bytes, const int32_t* __restrict__ src,
                                                    const int32_t* __restrict__ dst, int n, int32_t* status) {
+  pdl_wait();
+  pdl_trigger();
   const int r = blockIdx.x;
-  if (r == 0) check_rows(dst, n, c.B, status);
-  const int i = pair_of(src, dst, n, r, c.B, status);
+  if (r == 0) check_rows(dst, n, c.B, status, threadIdx.x, blockDim.x);
+  __shared__ int s_pair;
+  if (threadIdx.x < 32) {
+    const int i = pair_of(src, dst, n, r, c.B, status);
+    if (threadIdx.x == 0) s_pair = i;
+  }
+  __syncthreads();
+  const int i = s_pair;
   if (i < 0 || src[i] == r) return;
   const size_t bytes = (size_t)row_bytes * MLA_RESID_WINDOW;   // a multiple of 16: 128 rows
   const uint4* s = reinterpret_cast<const uint4*>((const char*)c.c_resid + bytes * src[i]);
@@ -438,10 +553,6 @@ mla_status_t check_table(const int32_t* table, const int32_t* refs, int32_t B, i
 
 mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
-cudaError_t copy_ints(int32_t* to, const int32_t* from, size_t n, cudaStream_t s) {
-  return to == from ? cudaSuccess : cudaMemcpyAsync(to, from, n * 4, cudaMemcpyDeviceToDevice, s);
-}
-
 // Workspace: two ints per row and three per block (reserve), two per block (compact).
 size_t workspace_ints(int32_t B, int32_t n_blocks) { return 2 * (size_t)B + 3 * (size_t)n_blocks; }
 
@@ -464,10 +575,8 @@ mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, int32_t 
   if (!src || !dst || !seq_lens || n <= 0) return MLA_ERR_INVALID_ARG;
   if (!aligned4(src) || !aligned4(dst) || !aligned4(seq_lens)) return MLA_ERR_ALIGNMENT;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = copy_ints(refs_out, refs, n_blocks, s);
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
-  fork_kernel<<<B, 128, 0, s>>>(Table{table, table_out, refs_out, B, n_cols, n_blocks, status}, src, dst, n, seq_lens);
-  return cuda_status(cudaGetLastError());
+  const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
+  return cuda_status(mla_launch_kernel(fork_kernel, dim3(kCluster), dim3(kThreads), 0, s, true, t, refs, src, dst, n, seq_lens));
 }
 
 mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
@@ -480,16 +589,13 @@ mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* refs, int32
   if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(copies) || ((uintptr_t)workspace & 15)) return MLA_ERR_ALIGNMENT;
   if (ws_bytes < mla_blocks_workspace_bytes(B, n_cols, n_blocks)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = copy_ints(refs_out, refs, n_blocks, s);
-  if (e == cudaSuccess) e = copy_ints(table_out, table, (size_t)B * n_cols, s);
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
   int32_t* w = (int32_t*)workspace;
   ReserveWs ws;
   ws.need = w; ws.copy = w + B;
   ws.writers = w + 2 * (size_t)B; ws.last = ws.writers + n_blocks; ws.free_ids = ws.last + n_blocks;
-  reserve_kernel<<<1, kThreads, 0, s>>>(Table{table_out, table_out, refs_out, B, n_cols, n_blocks, status}, seq_lens,
-                                        new_lens, ws, copies);
-  return cuda_status(cudaGetLastError());
+  const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
+  return cuda_status(mla_launch_kernel(reserve_kernel, dim3(kCluster), dim3(kThreads), 0, s, true, t, refs, seq_lens,
+                                       new_lens, ws, copies));
 }
 
 mla_status_t mla_blocks_trim(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
@@ -500,10 +606,8 @@ mla_status_t mla_blocks_trim(const int32_t* table, const int32_t* refs, int32_t 
   if (!seq_lens || n_sink < 0 || window < 0) return MLA_ERR_INVALID_ARG;
   if (!aligned4(seq_lens)) return MLA_ERR_ALIGNMENT;
   const cudaStream_t s = (cudaStream_t)stream;
-  if (copy_ints(refs_out, refs, n_blocks, s) != cudaSuccess) return MLA_ERR_CUDA;
-  const unsigned grid = (unsigned)(((long long)B * n_cols + 255) / 256);
-  trim_kernel<<<grid, 256, 0, s>>>(Table{table, table_out, refs_out, B, n_cols, n_blocks, status}, seq_lens, n_sink, window);
-  return cuda_status(cudaGetLastError());
+  const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
+  return cuda_status(mla_launch_kernel(trim_kernel, dim3(kCluster), dim3(kThreads), 0, s, true, t, refs, seq_lens, n_sink, window));
 }
 
 mla_status_t mla_blocks_compact(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols, int32_t n_blocks,
@@ -515,15 +619,10 @@ mla_status_t mla_blocks_compact(const int32_t* table, const int32_t* refs, int32
   if (!aligned4(copies) || ((uintptr_t)workspace & 15)) return MLA_ERR_ALIGNMENT;
   if (ws_bytes < mla_blocks_workspace_bytes(B, n_cols, n_blocks)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = (cudaStream_t)stream;
-  if (copy_ints(refs_out, refs, n_blocks, s) != cudaSuccess) return MLA_ERR_CUDA;
   int32_t* w = (int32_t*)workspace;
   CompactWs ws{w, w + n_blocks, w + n_blocks + n_blocks / 2};
   const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
-  compact_kernel<<<1, kThreads, 0, s>>>(t, ws, copies);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return MLA_ERR_CUDA;
-  remap_kernel<<<(unsigned)(((long long)B * n_cols + 255) / 256), 256, 0, s>>>(t, ws.remap);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(mla_launch_kernel(compact_kernel, dim3(kCluster), dim3(kThreads), 0, s, true, t, refs, ws, copies));
 }
 
 mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* copies,
@@ -546,8 +645,7 @@ mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
-  copy_kernel<<<4 * sms, kCopyThreads, 0, (cudaStream_t)stream>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(mla_launch_kernel(copy_kernel, dim3(kCopyCtas * sms), dim3(kCopyThreads), 0, (cudaStream_t)stream, true, a));
 }
 
 mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src, const int32_t* dst,
@@ -557,8 +655,8 @@ mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, co
   if ((st = mla_validate_cache(*cfg, cache)) != MLA_OK) return st;
   if (!cache->c_resid || !src || !dst || !status || n <= 0) return MLA_ERR_INVALID_ARG;
   if (!aligned4(src) || !aligned4(dst) || !aligned4(status)) return MLA_ERR_ALIGNMENT;
-  ring_kernel<<<cache->B, 256, 0, (cudaStream_t)stream>>>(*cache, (uint32_t)cfg->d_c * 2, src, dst, n, status);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(mla_launch_kernel(ring_kernel, dim3(cache->B), dim3(256), 0, (cudaStream_t)stream, true, *cache,
+                                       (uint32_t)cfg->d_c * 2, src, dst, n, status));
 }
 
 }  // extern "C"
