@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -35,6 +36,29 @@ mla_status_t validate_config(const mla_config_t* c) {
 }
 
 }  // namespace
+
+cudaError_t mla_smem_limit(const void* kern, size_t bytes) {
+  struct Entry {
+    const void* kern;
+    int device;
+    size_t bytes;
+  };
+  static std::mutex mutex;
+  static Entry known[256];
+  static int n = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mutex);
+  int i = 0;
+  while (i < n && !(known[i].kern == kern && known[i].device == dev)) ++i;
+  if (i < n && known[i].bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  if (i == n && n < 256) known[n++] = Entry{kern, dev, 0};
+  if (i < n) known[i].bytes = bytes;
+  return cudaSuccess;
+}
 
 mla_status_t mla_validate_config(const mla_config_t* c) { return validate_config(c); }
 
@@ -434,8 +458,10 @@ mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* 
   if (!mla_chunk_supported(*plan, *cache) || plan->opt_kernel == 1 || plan->opt_kernel == 2) return MLA_ERR_UNSUPPORTED;
   DecodeLayout L = mla_chunk_layout(*plan, B, Q);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  return cuda_status(mla_launch_chunk(*plan, *cache, seq_lens, q, B, Q, out, workspace, L, (cudaStream_t)stream,
-                                      window_of(*cache, n_sink, window)));
+  const MlaWindow win = window_of(*cache, n_sink, window);
+  if (plan->opt_kernel == 0 && mla_window_fused_capable(*plan))
+    return cuda_status(mla_launch_window_fused(*plan, *cache, seq_lens, q, B, Q, out, win, (cudaStream_t)stream));
+  return cuda_status(mla_launch_chunk(*plan, *cache, seq_lens, q, B, Q, out, workspace, L, (cudaStream_t)stream, win));
 }
 
 size_t mla_decode_chunk_workspace_bytes(const mla_plan_t* plan, int32_t B, int32_t Q) {

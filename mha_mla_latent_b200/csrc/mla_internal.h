@@ -105,6 +105,10 @@ inline cudaError_t mla_launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 blo
   return cudaLaunchKernelEx(&lc, kern, std::forward<Args>(args)...);
 }
 
+// Allows `kern` `bytes` of dynamic shared memory on the current device (mla_api.cpp).  The
+// largest size set so far is remembered per kernel and device, so a call sets it at most once.
+cudaError_t mla_smem_limit(const void* kern, size_t bytes);
+
 // Kernels of a call that the profiling options can bracket with events.
 enum MlaProfKernel { kProfAppend = 0, kProfAbsorb = 1, kProfAttention = 2, kProfCombine = 3 };
 
@@ -179,6 +183,11 @@ mla_status_t mla_pick_window_kernel(const mla_plan& p, const mla_cache_t& c, int
 cudaError_t mla_launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
                              int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s,
                              MlaWindow win = MlaWindow());
+
+// The windowed attention in one launch (window_fused.cu): any number of queries per sequence.
+bool mla_window_fused_capable(const mla_plan& p);
+cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
+                                    int B, int Q, void* out, MlaWindow win, cudaStream_t s);
 
 cudaError_t mla_launch_select_pairs(const mla_config_t& cfg, const void* q, const void* k, int T,
                                     int32_t* pair_idx, float* contrib, cudaStream_t s);

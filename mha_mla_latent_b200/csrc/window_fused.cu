@@ -1,0 +1,580 @@
+// Windowed latent attention in one launch: each CTA takes a unit of up to 128 rows (the query
+// heads of a few KV heads x a block of consecutive queries of one sequence) from the raw
+// queries to the finished output.
+//
+// Paper notes "MHA2MLA" (ACL 2025), §关键设计: W_uk is absorbed into the query, the partial-RoPE
+// term is scored apart, the probability-weighted latent goes through W_uv.  Per unit, rows
+// r = (KV head, query head of its group, query), in tiles of 128 tokens:
+//     Q_lat[r][c]  = scale sum_d q[r][d] W_ukF[g(r)][d][c]               K = d_h
+//     S[r][t]      = sum_c Q_lat[r][c] C[t][c] + sum_j Q_rope[r][j] KR[t][j]   K = d_c + 16 per 2 KV heads
+//     O[r][c]     += sum_t P[r][t] C[t][c],  P = 2^(S - m) on the visible tokens
+//     out[r][d]    = sum_c O[r][c] / l[r] W_uv[g(r)][c][d]               K = d_c
+// all on the 5th-generation tensor cores with M = 128.  Rows of few KV heads keep the RoPE
+// product short (its query operand is block-diagonal over the unit's KV heads), make each
+// weight slice serve many rows, and leave nothing to merge: no partials go through memory.
+// The price is that every unit of a sequence reads the window again, which the L2 serves.
+//
+// Operands that the CTA itself makes stay in tensor memory: the queries, the probabilities
+// (over the scores they came from) and the merged latent are A operands of their products
+// there, so shared memory holds Q_lat, the RoPE queries and the ring of tiles only.
+// Tensor memory columns: [0, 256) O, also the absorption's accumulator; [256, 384) and
+// [384, 512) S of even and odd tiles, also q, the merged latent's high halves and the output.
+//
+// Roles: warp 0 TMA producer (W_uk slices, tiles, W_uv slices through one ring), warp 1 MMA
+// issuer, warps 4-7 a row per thread (queries, softmax, epilogue).  Every wait is bounded.
+#include <cuda.h>
+
+#include "decode_common.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace fused {
+
+using namespace sm100;
+
+constexpr int kT = 128;               // tokens per tile
+constexpr int kRows = 128;            // rows per unit
+constexpr uint32_t kBox = kT * 128;   // bytes of 128 rows x 64 bf16 columns
+constexpr uint32_t kKrTile = kT * 64; // RoPE keys of a tile: 32 columns (4 KV heads)
+constexpr int kMaxG = 4;              // KV heads per unit
+constexpr float kTau = 8.0f;          // lazy-rescale threshold, log2 units
+constexpr uint32_t kCols = 512, kOCol = 0, kSCol = 256;
+constexpr uint32_t kSmemMax = 232448;
+
+struct Args {
+  int Q, H, n_kv, G, d_h, d_c, dcp, dhp;   // dcp, dhp: padded to whole 64-column boxes
+  int gb, qb, n_gblk, n_qblk;              // KV heads and queries per unit, units per sequence
+  int T_cap, NST;
+  float scale;                             // softmax scale x log2(e)
+  MlaWindow win;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  const int32_t* seq_lens;
+  const int32_t* rope_pair;
+  const double* theta;
+  mla_cache_t cache;
+  int32_t* err;
+  uint64_t wait_ns;
+  uint32_t stage, off_qr, off_ring, off_bar;
+};
+
+enum { kBarFull = 0, kBarEmpty = 4, kBarQ = 8, kBarAccFull, kBarAccEmpty, kBarQlat, kBarS, kBarP = kBarS + 2,
+       kBarO = kBarP + 2, kBarA = kBarO + 2, kBarDone, kBars };
+
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: A holds row r in lane r, two bf16 of K per 32-bit column.
+__device__ __forceinline__ void mma_a_tmem(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+
+template <bool PAGED>
+__global__ void __launch_bounds__(256, 1)
+window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
+                    const __grid_constant__ CUtensorMap tm_uk, const __grid_constant__ CUtensorMap tm_uv,
+                    const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sb - smem_u32(smem_raw));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto bar = [&](int i) { return sb + a.off_bar + 8u * (uint32_t)i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + a.off_bar + 8 * kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const uint64_t lim = a.wait_ns;
+  const int NST = a.NST;
+
+  // unit -> sequence, KV heads, queries
+  const int u = blockIdx.x;
+  const int qblk = u % a.n_qblk, gblk = (u / a.n_qblk) % a.n_gblk, b = u / (a.n_qblk * a.n_gblk);
+  const int g0 = gblk * a.gb, ng = min(a.gb, a.n_kv - g0);
+  const int q0 = qblk * a.qb, nq = min(a.qb, a.Q - q0);
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < NST; ++s) { mbar_init(bar(kBarFull + s), 1); mbar_init(bar(kBarEmpty + s), 1); }
+    const int four[] = {kBarQ, kBarAccEmpty, kBarQlat, kBarP, kBarP + 1, kBarA};
+    const int one[] = {kBarAccFull, kBarS, kBarS + 1, kBarO, kBarO + 1, kBarDone};
+    for (int i : four) mbar_init(bar(i), 4);
+    for (int i : one) mbar_init(bar(i), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int n_cbox = a.dcp / 64, n_hbox = a.dhp / 64;
+  const uint32_t uk_bytes = (uint32_t)n_cbox * a.d_h * 128u, uv_bytes = (uint32_t)n_hbox * a.d_c * 128u;
+  auto stage_at = [&](int i) { return sb + a.off_ring + (uint32_t)(i % NST) * a.stage; };
+
+  // The first W_uk slices belong to the plan: they may load before the kernels ahead are done.
+  int loaded = 0;   // ring items issued (producer)
+  auto load_uk = [&](int gi) {
+    const int s = loaded % NST;
+    mbar_expect_tx(bar(kBarFull + s), uk_bytes);
+    for (int k = 0; k < n_cbox; ++k)
+      tma_load_2d(stage_at(loaded) + k * a.d_h * 128, &tm_uk, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_h);
+    ++loaded;
+  };
+  if (warp == 0 && lane == 0)
+    while (loaded < min(ng, NST)) load_uk(loaded);
+  pdl_wait();   // queries, lengths and the cache come from earlier kernels
+  pdl_trigger();
+
+  // what the unit reads
+  int L = __ldg(a.seq_lens + b);
+  if (L < 0 || L > a.T_cap || (a.Q > 1 && L < a.Q)) {
+    if (threadIdx.x == 0) raise_error(a.err, MLA_DEVERR_SEQ_LEN);
+    L = 0;
+  }
+  const int p0 = L - a.Q + q0;                      // position of the unit's first query
+  const Span span = L > 0 ? unit_span(p0 + nq, nq, kT, a.win) : Span();
+  const int T = (span.len + kT - 1) / kT;           // tiles
+  auto tile_token = [&](int n) { return span.token(n * kT); };
+
+  if (warp == 0) {
+    // ============================================================ TMA producer (lane 0)
+    if (lane == 0) {
+      const int items = T > 0 ? 2 * ng + T : 0;
+      bool ok = true;
+      while (ok && loaded < items) {
+        const int i = loaded, s = i % NST;
+        if (i >= NST) ok = mbar_wait(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
+        if (!ok) break;
+        if (i < ng) { load_uk(i); continue; }
+        if (i < ng + T) {
+          const int t = tile_token(i - ng);
+          const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
+          const int row = lc.pb * lc.cap + lc.pt;
+          mbar_expect_tx(bar(kBarFull + s), (uint32_t)n_cbox * kBox + kKrTile);
+          for (int k = 0; k < n_cbox; ++k) tma_load_2d(stage_at(i) + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
+          tma_load_2d(stage_at(i) + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
+        } else {
+          const int gi = i - ng - T;
+          mbar_expect_tx(bar(kBarFull + s), uv_bytes);
+          for (int k = 0; k < n_hbox; ++k)
+            tma_load_2d(stage_at(i) + k * a.d_c * 128, &tm_uv, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_c);
+        }
+        ++loaded;
+      }
+      volatile int never = 0;   // every copy lands before the CTA exits
+      for (int i = max(0, loaded - NST); i < loaded; ++i) mbar_wait(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
+    }
+  } else if (warp == 1) {
+    // ============================================================ MMA issuer (lane 0)
+    if (lane == 0 && T > 0) {
+      auto full = [&](int i) { return mbar_wait(bar(kBarFull + i % NST), (i / NST) & 1, abort_flag, lim); };
+      bool ok = mbar_wait(bar(kBarQ), 0, abort_flag, lim);
+      // absorption: q (tensor memory) x W_ukF[g], once per KV head over all rows
+      const uint32_t id_abs = idesc_bf16_f32(kRows, a.dcp, false, true);
+      for (int gi = 0; ok && gi < ng; ++gi) {
+        ok = full(gi) && (gi == 0 || mbar_wait(bar(kBarAccEmpty), (gi - 1) & 1, abort_flag, lim));
+        if (!ok) break;
+        tc_fence_after();
+        for (int k = 0; k < a.d_h / 16; ++k)
+          mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, smem_desc(stage_at(gi) + k * 2048, a.d_h * 128, 1024, kLayoutSW128),
+                     id_abs, k > 0);
+        tc_commit(bar(kBarEmpty + gi % NST));
+        tc_commit(bar(kBarAccFull));
+      }
+      ok = ok && mbar_wait(bar(kBarQlat), 0, abort_flag, lim);
+      tc_fence_after();
+      // tiles: S(n) needs its tile and the buffer of tile n - 2, whose P was read by O(n - 2)
+      // issued before it; O(n) needs P(n).  Whichever can go next is issued.
+      const uint32_t id_s = idesc_bf16_f32(kRows, kT, false, false), id_o = idesc_bf16_f32(kRows, a.dcp, false, true);
+      const int kr_steps = (ng * 8 + 15) / 16;
+      int n1 = 0, n2 = 0;
+      uint64_t idle = 0;
+      while (ok && n2 < T) {
+        const int i1 = ng + n1, i2 = ng + n2;
+        if (n1 < T && n1 <= n2 + 1 && mbar_test(bar(kBarFull + i1 % NST), (i1 / NST) & 1)) {
+          tc_fence_after();
+          const uint32_t c0 = stage_at(i1), k0 = c0 + n_cbox * kBox, d = tmem + kSCol + (n1 & 1) * kT;
+          for (int k = 0; k < a.dcp / 16; ++k)
+            tc_mma_bf16(d, smem_desc(sb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kLayoutSW128),
+                        smem_desc(c0 + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kLayoutSW128), id_s, k > 0);
+          for (int k = 0; k < kr_steps; ++k)
+            tc_mma_bf16(d, smem_desc(sb + a.off_qr + k * 32, 16, 512, kLayoutSW64),
+                        smem_desc(k0 + k * 32, 16, 512, kLayoutSW64), id_s, 1);
+          tc_commit(bar(kBarS + (n1 & 1)));
+          ++n1;
+          idle = 0;
+        } else if (n2 < n1 && mbar_test(bar(kBarP + (n2 & 1)), (n2 >> 1) & 1)) {
+          tc_fence_after();
+          const uint32_t c0 = stage_at(i2), p = tmem + kSCol + (n2 & 1) * kT;
+          for (int k = 0; k < kT / 16; ++k)
+            mma_a_tmem(tmem + kOCol, p + 8 * k, smem_desc(c0 + k * 2048, kBox, 1024, kLayoutSW128), id_o, n2 > 0 || k > 0);
+          tc_commit(bar(kBarEmpty + i2 % NST));
+          tc_commit(bar(kBarO + (n2 & 1)));
+          ++n2;
+          idle = 0;
+        } else {
+          const uint64_t now = globaltimer();
+          if (!idle) idle = now;
+          if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+        }
+      }
+      // output: merged latent (tensor memory, high and low halves) x W_uv[g]
+      const uint32_t id_out = idesc_bf16_f32(kRows, a.dhp, false, true);
+      ok = ok && mbar_wait(bar(kBarA), 0, abort_flag, lim);
+      for (int gi = 0; ok && gi < ng; ++gi) {
+        const int i = ng + T + gi;
+        ok = full(i) && (gi == 0 || mbar_wait(bar(kBarAccEmpty), (ng + gi - 1) & 1, abort_flag, lim));
+        if (!ok) break;
+        tc_fence_after();
+        for (int half = 0; half < 2; ++half)
+          for (int k = 0; k < a.d_c / 16; ++k)
+            mma_a_tmem(tmem + kSCol + kT, tmem + (half ? kOCol : kSCol) + 8 * k,
+                       smem_desc(stage_at(i) + k * 2048, a.d_c * 128, 1024, kLayoutSW128), id_out, half > 0 || k > 0);
+        tc_commit(bar(kBarEmpty + i % NST));
+        tc_commit(bar(kBarAccFull));
+      }
+      tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
+      volatile int never = 0;
+      mbar_wait(bar(kBarDone), 0, &never, lim);
+    }
+  } else if (warp >= 4) {
+    // ============================================================ rows
+    const int w = warp - 4, r = 32 * w + lane;          // tensor memory lane = row
+    const int per_g = a.G * a.qb;
+    const int gi = r / per_g, hi = (r / a.qb) % a.G, qi = r % a.qb;
+    const bool valid = gi < ng && qi < nq;
+    const int g = g0 + gi, h = g * a.G + hi;
+    const size_t row = ((size_t)b * a.Q + q0 + qi) * a.H + h;
+    const uint32_t lane0 = tmem + ((uint32_t)(32 * w) << 16);
+    auto wwait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, lim)); };
+    auto arrive = [&](int i) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(i));
+    };
+    if (T == 0) {   // an empty sequence: zero rows
+      if (valid)
+        for (int c = 0; c < a.d_h / 8; ++c) reinterpret_cast<uint4*>(a.out + row * a.d_h)[c] = make_uint4(0, 0, 0, 0);
+    } else {
+      // q row into tensor memory; the rotated kept pairs, scaled, into this row's KV head chunk
+      // of the block-diagonal RoPE operand
+      const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + row * a.d_h);
+      for (int c0 = 0; c0 < a.d_h / 2; c0 += 32) {   // 32 columns = 64 values
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 x = valid && c0 + 4 * j < a.d_h / 2 ? __ldg(qsrc + c0 / 4 + j) : make_uint4(0, 0, 0, 0);
+          v[4 * j] = x.x; v[4 * j + 1] = x.y; v[4 * j + 2] = x.z; v[4 * j + 3] = x.w;
+        }
+        tmem_st32(lane0 + kSCol + c0, v);
+      }
+      {
+        uint32_t rot[4] = {0, 0, 0, 0};
+        if (valid) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = __ldg(a.rope_pair + g * 4 + j);
+            const uint32_t xy = __ldg(reinterpret_cast<const uint32_t*>(a.q + row * a.d_h) + k);
+            float sn, cs;
+            rope_sincos(p0 + qi, __ldg(a.theta + k), &sn, &cs);
+            rot[j] = pack2((lo_f(xy) * cs - hi_f(xy) * sn) * a.scale, (lo_f(xy) * sn + hi_f(xy) * cs) * a.scale);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kMaxG; ++c)
+          *reinterpret_cast<uint4*>(smem + a.off_qr + r * 64 + ((c ^ (r >> 1)) & 3) * 16) =
+              c == gi ? make_uint4(rot[0], rot[1], rot[2], rot[3]) : make_uint4(0, 0, 0, 0);
+      }
+      tmem_wait_st();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive(kBarQ);
+      // Q_lat: the accumulator's rows of each KV head, scaled, rounded to bf16 (the product's
+      // operand type)
+      bool ok = true;
+      for (int k = 0; ok && k < ng; ++k) {
+        ok = wwait(kBarAccFull, k & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c0 = 0; c0 < a.dcp; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(lane0 + kOCol + c0, v);
+          tmem_wait_ld();
+          if (gi != k && !(gi >= ng && k == 0)) continue;   // rows of no KV head: once, whatever they hold
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack2(__uint_as_float(v[8 * j + 2 * e]) * a.scale, __uint_as_float(v[8 * j + 2 * e + 1]) * a.scale);
+            const int ch = c0 / 8 + j;
+            *reinterpret_cast<uint4*>(smem + (ch >> 3) * kBox + sw128(r, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc_fence_before();
+        arrive(kBarAccEmpty);
+      }
+      fence_proxy_async_smem();
+      if (ok) arrive(kBarQlat);
+      // tiles
+      const int p_row = valid ? p0 + qi : -1;
+      float m = -INFINITY, l = 0.f;
+      for (int n = 0; ok && n < T; ++n) {
+        const int t0 = tile_token(n), nvalid = min(kT, span.len - n * kT);
+        ok = wwait(kBarS + (n & 1), (n >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t scol = lane0 + kSCol + (n & 1) * kT;
+        float s[kT];
+        {
+          uint32_t raw[4][32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32(scol + 32 * k, raw[k]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < kT; ++e) {
+            asm volatile("" : "+r"(raw[e / 32][e % 32]));   // the values exist only after the wait
+            s[e] = __uint_as_float(raw[e / 32][e % 32]);
+          }
+        }
+        // tiles whose tokens every query of the unit sees need no mask
+        const bool whole = nvalid == kT && t0 + kT - 1 <= p0 && (t0 > p0 + nq - 1 - a.win.window || t0 + kT <= a.win.n_sink);
+        if (!whole) {
+          const int lim_t = min(nvalid, p_row + 1 - t0);
+          const int sink_t = a.win.n_sink - t0, win_t = p_row + 1 - a.win.window - t0;
+#pragma unroll
+          for (int t = 0; t < kT; ++t) s[t] = t < lim_t && (t >= win_t || t < sink_t) ? s[t] : -INFINITY;
+          // rows that no query of the unit sees (stale or hidden, possibly not finite) are
+          // zeroed before O's product multiplies them by P = 0; S of this tile has been read
+          if (r >= nvalid || (t0 + r >= a.win.n_sink && t0 + r < span.lo)) {
+            uint8_t* C = smem + a.off_ring + (uint32_t)((ng + n) % NST) * a.stage;
+            for (int k = 0; k < n_cbox; ++k)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(C + k * kBox + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < kT; ++t) mx[t & 3] = fmaxf(mx[t & 3], s[t]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // The running max is raised when a row outgrew it by more than kTau (P stays below
+        // 2^kTau, in range for bf16 and the float32 sums); the loads and stores of O are
+        // warp-collective, so the other rows multiply by 1.
+        const bool raise = top > m + kTau;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float al = raise ? exp2f(m - top) : 1.f;   // m = -inf: 0
+          if (n > 0) {
+            ok = wwait(kBarO + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            for (int c0 = 0; c0 < a.dcp; c0 += 32) {
+              uint32_t o[32];
+              tmem_ld32(lane0 + kOCol + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+              tmem_st32(lane0 + kOCol + c0, o);
+            }
+            tmem_wait_st();
+          }
+          if (raise) {
+            l *= al;
+            m = top;
+          }
+        }
+        const float mb = m == -INFINITY ? 0.f : m;   // masked scores are -inf: 2^(-inf) = 0
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {   // P, rounded to bf16 (the product's operand type), over S
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = ex2_approx(s[64 * k + 2 * e] - mb), y = ex2_approx(s[64 * k + 2 * e + 1] - mb);
+            sum[(2 * e) & 3] += x;
+            sum[(2 * e + 1) & 3] += y;
+            pk[e] = pack2(x, y);
+          }
+          tmem_st32(scol + 32 * k, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(kBarP + (n & 1));
+      }
+      // merged latent, normalised, in two bf16 halves (so that this rounding does not count):
+      // the high ones over S, the low ones over the columns of O already read
+      if (ok) ok = wwait(kBarO + ((T - 1) & 1), ((T - 1) >> 1) & 1);
+      if (ok) {
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        for (int c0 = 0; c0 < a.d_c; c0 += 32) {
+          uint32_t v[32], hi2[16], lo2[16];
+          tmem_ld32(lane0 + kOCol + c0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = __uint_as_float(v[2 * e]) * inv, y = __uint_as_float(v[2 * e + 1]) * inv;
+            hi2[e] = pack2(x, y);
+            lo2[e] = pack2(x - lo_f(hi2[e]), y - hi_f(hi2[e]));
+          }
+          tmem_st16(lane0 + kSCol + c0 / 2, hi2);
+          tmem_st16(lane0 + kOCol + c0 / 2, lo2);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(kBarA);
+      }
+      for (int k = 0; ok && k < ng; ++k) {
+        ok = wwait(kBarAccFull, (ng + k) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c0 = 0; c0 < a.d_h; c0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(lane0 + kSCol + kT + c0, v);
+          tmem_wait_ld();
+          if (!valid || gi != k) continue;
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * a.d_h + c0);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack2(__uint_as_float(v[8 * j + 2 * e]), __uint_as_float(v[8 * j + 2 * e + 1]));
+            dst[j] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc_fence_before();
+        arrive(kBarAccEmpty);
+      }
+    }
+  }
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) raise_error(a.err, MLA_DEVERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = []() -> EncodeTiledFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      return (EncodeTiledFn)p;
+    return nullptr;
+  }();
+  return fn;
+}
+
+static bool map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[2] = {cols, rows};
+  cuuint64_t gstride[1] = {cols * 2};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstride, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout {
+  int NST;
+  uint32_t stage, off_qr, off_ring, off_bar, total;
+};
+// [Q_lat boxes][RoPE queries][ring of 2 to 4 stages][barriers]
+static Layout layout(int dcp) {
+  Layout L{};
+  const uint32_t n_cbox = dcp / 64;
+  L.stage = n_cbox * kBox + kKrTile;
+  L.off_qr = n_cbox * kBox;
+  L.off_ring = L.off_qr + kRows * 64;
+  const uint32_t tail = 8 * kBars + 16;
+  L.NST = (int)std::min<uint32_t>(4, (kSmemMax - 1024 - L.off_ring - tail) / L.stage);
+  L.off_bar = L.off_ring + L.NST * L.stage;
+  L.total = L.off_bar + tail + 1024;
+  return L;
+}
+
+// KV heads per unit: few of them re-read the window more often but fill the machine and its
+// rows' products; the candidate with the least (rounds of CTAs) x (time of a unit) is taken.
+// Times in units of a tile's products at d_c = 256; see the launch comment for the measurement.
+static int pick_gb(int B, int Q, int G, int n_kv, int tiles, int sms) {
+  int best = 1;
+  double best_cost = 1e30;
+  for (int gb = 1; gb <= kMaxG && gb <= n_kv && gb * G <= kRows; gb *= 2) {
+    const int qb = std::min(Q, kRows / (gb * G));
+    const long long units = (long long)B * ((n_kv + gb - 1) / gb) * ((Q + qb - 1) / qb);
+    const double cost = (double)((units + sms - 1) / sms) * (tiles + 2.0 + 2.0 * gb);
+    if (cost < best_cost) { best_cost = cost; best = gb; }
+  }
+  return best;
+}
+
+}  // namespace fused
+}  // namespace mla
+
+// Shapes: bf16 cache and weights, r = 4 kept pairs, d_c a multiple of 32 up to 256, head dim a
+// multiple of 16 up to 128, at most 128 query heads per KV head, RoPE rows of whole 16 bytes.
+bool mla_window_fused_capable(const mla_plan& p) {
+  const mla_config_t& c = p.cfg;
+  return c.dtype == MLA_BF16 && c.cache_kind == MLA_CACHE_SAME && c.r_pairs == 4 && c.d_c % 32 == 0 && c.d_c <= 256 &&
+         c.head_dim % 16 == 0 && c.head_dim <= 128 && c.n_heads / c.n_kv_heads <= 128;
+}
+
+cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
+                                    int B, int Q, void* out, MlaWindow win, cudaStream_t s) {
+  using namespace mla::fused;
+  const mla_config_t& cfg = p.cfg;
+  Args a;
+  a.Q = Q; a.H = cfg.n_heads; a.n_kv = cfg.n_kv_heads; a.G = a.H / a.n_kv; a.d_h = cfg.head_dim; a.d_c = cfg.d_c;
+  a.dcp = (a.d_c + 63) / 64 * 64; a.dhp = (a.d_h + 63) / 64 * 64;
+  const int tiles = (int)std::min<long long>((long long)c.T_cap, (long long)win.n_sink + win.window + Q) / kT + 1;
+  a.gb = pick_gb(B, Q, a.G, a.n_kv, tiles, p.num_sms);
+  a.qb = std::min(Q, kRows / (a.gb * a.G));
+  a.n_gblk = (a.n_kv + a.gb - 1) / a.gb;
+  a.n_qblk = (Q + a.qb - 1) / a.qb;
+  const long long units = (long long)B * a.n_gblk * a.n_qblk;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  a.T_cap = c.T_cap;
+  a.scale = mla::kLog2e * (cfg.softmax_scale > 0.0f ? cfg.softmax_scale : (float)(1.0 / sqrt((double)cfg.head_dim)));
+  a.win = win;
+  a.q = (const __nv_bfloat16*)q; a.out = (__nv_bfloat16*)out; a.seq_lens = seq_lens;
+  a.rope_pair = p.rope_pair; a.theta = p.theta; a.cache = c; a.err = p.err;
+  a.wait_ns = (uint64_t)p.opt_wait_us * 1000u;
+  const Layout L = layout(a.dcp);
+  a.NST = L.NST; a.stage = L.stage; a.off_qr = L.off_qr; a.off_ring = L.off_ring; a.off_bar = L.off_bar;
+  const uint64_t rows = mla_cache_rows(c);
+  CUtensorMap tm_c, tm_kr, tm_uk, tm_uv;
+  if (!map_2d(&tm_c, c.c_kv, a.d_c, rows, 64, kT) || !map_2d(&tm_kr, c.k_rope, p.R, rows, 32, kT) ||
+      !map_2d(&tm_uk, p.W_ukF, a.d_c, (uint64_t)a.n_kv * a.d_h, 64, a.d_h) ||
+      !map_2d(&tm_uv, p.W_uv, a.d_h, (uint64_t)a.n_kv * a.d_c, 64, a.d_c))
+    return cudaErrorInvalidValue;
+  auto kern = c.block_table ? window_fused_kernel<true> : window_fused_kernel<false>;
+  cudaError_t e = mla_smem_limit((const void*)kern, L.total);
+  if (e != cudaSuccess) return e;
+  if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
+  e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(256), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);
+  if (e != cudaSuccess) return e;
+  return mla_profile_event(p, kProfAttention, true, s);
+}
