@@ -21,7 +21,9 @@
 // [384, 512) S of even and odd tiles, also q, the merged latent's high halves and the output.
 //
 // Roles: warp 0 TMA producer (W_uk slices, tiles, W_uv slices through one ring), warp 1 MMA
-// issuer, warps 4-7 a row per thread (queries, softmax, epilogue).  Every wait is bounded.
+// issuer, warps 4-11 the rows, two threads per row (queries, softmax, epilogue).  Every wait is
+// bounded; waits poll without the suspended form, whose wake-up costs more than it frees here
+// (each scheduler holds two row warps and at most one of the others).
 #include <cuda.h>
 
 #include "decode_common.cuh"
@@ -34,6 +36,7 @@ using namespace sm100;
 
 constexpr int kT = 128;               // tokens per tile
 constexpr int kRows = 128;            // rows per unit
+constexpr int kThreads = 384;         // 12 warps
 constexpr uint32_t kBox = kT * 128;   // bytes of 128 rows x 64 bf16 columns
 constexpr uint32_t kKrTile = kT * 64; // RoPE keys of a tile: 32 columns (4 KV heads)
 constexpr int kMaxG = 4;              // KV heads per unit
@@ -55,11 +58,11 @@ struct Args {
   mla_cache_t cache;
   int32_t* err;
   uint64_t wait_ns;
-  uint32_t stage, off_qr, off_ring, off_bar;
+  uint32_t stage, off_qr, off_ring, off_xchg, off_bar;
 };
 
 enum { kBarFull = 0, kBarEmpty = 4, kBarQ = 8, kBarAccFull, kBarAccEmpty, kBarQlat, kBarS, kBarP = kBarS + 2,
-       kBarO = kBarP + 2, kBarA = kBarO + 2, kBarDone, kBars };
+       kBarO = kBarP + 2, kBarA = kBarO + 2, kBarDone, kBarX, kBars = kBarX + 4 };
 
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -79,8 +82,44 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d, uint32_t a, uint64_t b_de
       : "memory");
 }
 
+// Waits for the phase of the given parity without suspending; false when the wait exceeds
+// `limit_ns` or another role gave up.
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_test(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > limit_ns) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+// 32 lanes x 8 consecutive columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Bits 0 .. n-1 of 64 (n outside [0, 64] cut to it).
+__device__ __forceinline__ uint64_t below64(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 template <bool PAGED>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
                     const __grid_constant__ CUtensorMap tm_uk, const __grid_constant__ CUtensorMap tm_uv,
                     const __grid_constant__ Args a) {
@@ -103,10 +142,11 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < NST; ++s) { mbar_init(bar(kBarFull + s), 1); mbar_init(bar(kBarEmpty + s), 1); }
-    const int four[] = {kBarQ, kBarAccEmpty, kBarQlat, kBarP, kBarP + 1, kBarA};
+    const int rows[] = {kBarQ, kBarAccEmpty, kBarQlat, kBarP, kBarP + 1, kBarA};
     const int one[] = {kBarAccFull, kBarS, kBarS + 1, kBarO, kBarO + 1, kBarDone};
-    for (int i : four) mbar_init(bar(i), 4);
+    for (int i : rows) mbar_init(bar(i), 8);   // the row warps
     for (int i : one) mbar_init(bar(i), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(kBarX + i), 2);   // the two warps of the same rows
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -132,9 +172,39 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   };
   if (warp == 0 && lane == 0)
     while (loaded < min(ng, NST)) load_uk(loaded);
+  // rows (warps 4-11): thread -> row r of the unit, half hf of its tokens and columns
+  const int w = warp & 3, hf = warp >= 8, r = 32 * w + lane;   // tensor memory lane = row
+  const int per_g = a.G * a.qb;
+  const int gi = r / per_g, hi = (r / a.qb) % a.G, qi = r % a.qb;
+  const bool valid = warp >= 4 && gi < ng && qi < nq;
+  const int g = g0 + gi;
+  const size_t row = ((size_t)b * a.Q + q0 + qi) * a.H + g * a.G + hi;
+  const uint32_t lane0 = tmem + ((uint32_t)(32 * w) << 16);
+  float* xchg = reinterpret_cast<float*>(smem + a.off_xchg);   // [2][2 halves][rows]
+  auto wwait = [&](int i, int parity) { return __all_sync(0xffffffffu, spin_wait(bar(i), parity, abort_flag, lim)); };
+  int pair[2] = {0, 0};
+  double theta[2] = {0, 0};
+  if (valid) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) pair[j] = __ldg(a.rope_pair + g * 4 + 2 * hf + j);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) theta[j] = __ldg(a.theta + pair[j]);
+  }
   pdl_wait();   // queries, lengths and the cache come from earlier kernels
   pdl_trigger();
 
+  // this thread's part of the q row: blocks hf, hf + 2, .. of 16 values, and two kept pairs
+  uint4 qv[8];
+  uint32_t xy[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = 2 * (hf + 2 * (j / 2)) + j % 2;
+    qv[j] = valid && c < a.d_h / 8 ? __ldg(reinterpret_cast<const uint4*>(a.q + row * a.d_h) + c) : make_uint4(0, 0, 0, 0);
+  }
+  if (valid) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) xy[j] = __ldg(reinterpret_cast<const uint32_t*>(a.q + row * a.d_h) + pair[j]);
+  }
   // what the unit reads
   int L = __ldg(a.seq_lens + b);
   if (L < 0 || L > a.T_cap || (a.Q > 1 && L < a.Q)) {
@@ -153,7 +223,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       bool ok = true;
       while (ok && loaded < items) {
         const int i = loaded, s = i % NST;
-        if (i >= NST) ok = mbar_wait(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
+        if (i >= NST) ok = spin_wait(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
         if (!ok) break;
         if (i < ng) { load_uk(i); continue; }
         if (i < ng + T) {
@@ -172,127 +242,157 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         ++loaded;
       }
       volatile int never = 0;   // every copy lands before the CTA exits
-      for (int i = max(0, loaded - NST); i < loaded; ++i) mbar_wait(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
+      for (int i = max(0, loaded - NST); i < loaded; ++i) spin_wait(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
     }
   } else if (warp == 1) {
-    // ============================================================ MMA issuer (lane 0)
-    if (lane == 0 && T > 0) {
-      auto full = [&](int i) { return mbar_wait(bar(kBarFull + i % NST), (i / NST) & 1, abort_flag, lim); };
-      bool ok = mbar_wait(bar(kBarQ), 0, abort_flag, lim);
+    // ============================================================ MMA issuer
+    // The whole warp walks the same path, with every condition the same in all lanes, and one
+    // elected lane issues: the compiler then keeps descriptors in uniform registers.  (Issued
+    // from a branch of lane 0 a product took 110 to 190 cycles, more than most of them compute.)
+    if (T > 0) {
+      auto wait_all = [&](int i, int parity) {
+        return __all_sync(0xffffffffu, spin_wait(bar(i), parity, abort_flag, lim)) != 0;
+      };
+      auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
+      auto full = [&](int i) { return wait_all(kBarFull + i % NST, (i / NST) & 1); };
+      bool ok = wait_all(kBarQ, 0);
       // absorption: q (tensor memory) x W_ukF[g], once per KV head over all rows
       const uint32_t id_abs = idesc_bf16_f32(kRows, a.dcp, false, true);
       for (int gi = 0; ok && gi < ng; ++gi) {
-        ok = full(gi) && (gi == 0 || mbar_wait(bar(kBarAccEmpty), (gi - 1) & 1, abort_flag, lim));
+        ok = full(gi) && (gi == 0 || wait_all(kBarAccEmpty, (gi - 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        for (int k = 0; k < a.d_h / 16; ++k)
-          mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, smem_desc(stage_at(gi) + k * 2048, a.d_h * 128, 1024, kLayoutSW128),
-                     id_abs, k > 0);
-        tc_commit(bar(kBarEmpty + gi % NST));
-        tc_commit(bar(kBarAccFull));
+        if (elect_one()) {
+          const uint64_t w0 = smem_desc(stage_at(gi), a.d_h * 128, 1024, kLayoutSW128);
+          for (int k = 0; k < a.d_h / 16; ++k) mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, w0 + 128u * k, id_abs, k > 0);
+          tc_commit(bar(kBarEmpty + gi % NST));
+          tc_commit(bar(kBarAccFull));
+        }
+        __syncwarp();
       }
-      ok = ok && mbar_wait(bar(kBarQlat), 0, abort_flag, lim);
+      ok = ok && wait_all(kBarQlat, 0);
       tc_fence_after();
       // tiles: S(n) needs its tile and the buffer of tile n - 2, whose P was read by O(n - 2)
       // issued before it; O(n) needs P(n).  Whichever can go next is issued.
       const uint32_t id_s = idesc_bf16_f32(kRows, kT, false, false), id_o = idesc_bf16_f32(kRows, a.dcp, false, true);
-      const int kr_steps = (ng * 8 + 15) / 16;
+      // descriptors are made once; a step along K adds its bytes / 16 to the address field
+      const uint64_t desc_q = smem_desc(sb, 16, 1024, kLayoutSW128), desc_qr = smem_desc(sb + a.off_qr, 16, 512, kLayoutSW64);
       int n1 = 0, n2 = 0;
-      uint64_t idle = 0;
+      uint64_t idle = 0;   // when nothing could be issued: since when (read every 64th look only)
+      int looks = 0;
       while (ok && n2 < T) {
         const int i1 = ng + n1, i2 = ng + n2;
-        if (n1 < T && n1 <= n2 + 1 && mbar_test(bar(kBarFull + i1 % NST), (i1 / NST) & 1)) {
+        if (n1 < T && n1 <= n2 + 1 && ready(kBarFull + i1 % NST, (i1 / NST) & 1)) {
           tc_fence_after();
-          const uint32_t c0 = stage_at(i1), k0 = c0 + n_cbox * kBox, d = tmem + kSCol + (n1 & 1) * kT;
-          for (int k = 0; k < a.dcp / 16; ++k)
-            tc_mma_bf16(d, smem_desc(sb + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kLayoutSW128),
-                        smem_desc(c0 + (k >> 2) * kBox + (k & 3) * 32, 16, 1024, kLayoutSW128), id_s, k > 0);
-          for (int k = 0; k < kr_steps; ++k)
-            tc_mma_bf16(d, smem_desc(sb + a.off_qr + k * 32, 16, 512, kLayoutSW64),
-                        smem_desc(k0 + k * 32, 16, 512, kLayoutSW64), id_s, 1);
-          tc_commit(bar(kBarS + (n1 & 1)));
+          if (elect_one()) {
+            const uint32_t c0 = stage_at(i1), d = tmem + kSCol + (n1 & 1) * kT;
+            uint64_t da = desc_q, db = smem_desc(c0, 16, 1024, kLayoutSW128);
+            const uint64_t dk = smem_desc(c0 + n_cbox * kBox, 16, 512, kLayoutSW64);
+            tc_mma_bf16(d, desc_qr, dk, id_s, 0);
+            if (ng > 2) tc_mma_bf16(d, desc_qr + 2, dk + 2, id_s, 1);
+            for (int k = 0; k < n_cbox; ++k) {   // a box: four steps of 16 columns
+              tc_mma_bf16(d, da, db, id_s, 1);
+              tc_mma_bf16(d, da + 2, db + 2, id_s, 1);
+              tc_mma_bf16(d, da + 4, db + 4, id_s, 1);
+              tc_mma_bf16(d, da + 6, db + 6, id_s, 1);
+              da += kBox >> 4;
+              db += kBox >> 4;
+            }
+            tc_commit(bar(kBarS + (n1 & 1)));
+          }
+          __syncwarp();
           ++n1;
-          idle = 0;
-        } else if (n2 < n1 && mbar_test(bar(kBarP + (n2 & 1)), (n2 >> 1) & 1)) {
+          looks = 0;
+        } else if (n2 < n1 && ready(kBarP + (n2 & 1), (n2 >> 1) & 1)) {
           tc_fence_after();
-          const uint32_t c0 = stage_at(i2), p = tmem + kSCol + (n2 & 1) * kT;
-          for (int k = 0; k < kT / 16; ++k)
-            mma_a_tmem(tmem + kOCol, p + 8 * k, smem_desc(c0 + k * 2048, kBox, 1024, kLayoutSW128), id_o, n2 > 0 || k > 0);
-          tc_commit(bar(kBarEmpty + i2 % NST));
-          tc_commit(bar(kBarO + (n2 & 1)));
+          if (elect_one()) {
+            const uint32_t p = tmem + kSCol + (n2 & 1) * kT;
+            const uint64_t dv = smem_desc(stage_at(i2), kBox, 1024, kLayoutSW128);
+            mma_a_tmem(tmem + kOCol, p, dv, id_o, n2 > 0);
+#pragma unroll
+            for (int k = 1; k < kT / 16; ++k) mma_a_tmem(tmem + kOCol, p + 8 * k, dv + 128 * k, id_o, 1);
+            tc_commit(bar(kBarEmpty + i2 % NST));
+            tc_commit(bar(kBarO + (n2 & 1)));
+          }
+          __syncwarp();
           ++n2;
-          idle = 0;
-        } else {
+          looks = 0;
+        } else if ((++looks & 63) == 0) {
           const uint64_t now = globaltimer();
-          if (!idle) idle = now;
+          if (looks == 64) idle = now;
           if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+          ok = __all_sync(0xffffffffu, ok) != 0;
         }
       }
       // output: merged latent (tensor memory, high and low halves) x W_uv[g]
       const uint32_t id_out = idesc_bf16_f32(kRows, a.dhp, false, true);
-      ok = ok && mbar_wait(bar(kBarA), 0, abort_flag, lim);
+      ok = ok && wait_all(kBarA, 0);
       for (int gi = 0; ok && gi < ng; ++gi) {
         const int i = ng + T + gi;
-        ok = full(i) && (gi == 0 || mbar_wait(bar(kBarAccEmpty), (ng + gi - 1) & 1, abort_flag, lim));
+        ok = full(i) && (gi == 0 || wait_all(kBarAccEmpty, (ng + gi - 1) & 1));
         if (!ok) break;
         tc_fence_after();
-        for (int half = 0; half < 2; ++half)
-          for (int k = 0; k < a.d_c / 16; ++k)
-            mma_a_tmem(tmem + kSCol + kT, tmem + (half ? kOCol : kSCol) + 8 * k,
-                       smem_desc(stage_at(i) + k * 2048, a.d_c * 128, 1024, kLayoutSW128), id_out, half > 0 || k > 0);
-        tc_commit(bar(kBarEmpty + i % NST));
-        tc_commit(bar(kBarAccFull));
+        if (elect_one()) {
+          const uint64_t w0 = smem_desc(stage_at(i), a.d_c * 128, 1024, kLayoutSW128);
+          for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kSCol + 8 * k, w0 + 128u * k, id_out, k > 0);
+          for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kOCol + 8 * k, w0 + 128u * k, id_out, 1);
+          tc_commit(bar(kBarEmpty + i % NST));
+          tc_commit(bar(kBarAccFull));
+        }
+        __syncwarp();
       }
-      tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
+      if (elect_one()) tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
+      __syncwarp();
       volatile int never = 0;
-      mbar_wait(bar(kBarDone), 0, &never, lim);
+      spin_wait(bar(kBarDone), 0, &never, lim);
     }
   } else if (warp >= 4) {
     // ============================================================ rows
-    const int w = warp - 4, r = 32 * w + lane;          // tensor memory lane = row
-    const int per_g = a.G * a.qb;
-    const int gi = r / per_g, hi = (r / a.qb) % a.G, qi = r % a.qb;
-    const bool valid = gi < ng && qi < nq;
-    const int g = g0 + gi, h = g * a.G + hi;
-    const size_t row = ((size_t)b * a.Q + q0 + qi) * a.H + h;
-    const uint32_t lane0 = tmem + ((uint32_t)(32 * w) << 16);
-    auto wwait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, lim)); };
+    // Two threads per row, in warps w and w + 4 of the same tensor memory lanes: each takes
+    // half of every tile's tokens and of every accumulator's columns.
     auto arrive = [&](int i) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(i));
     };
+    int n_sync = 0;
+    auto pair_sync = [&]() {   // with the other warp of these rows (bounded, unlike a named barrier)
+      tc_fence_before();
+      arrive(kBarX + w);
+      const bool met = wwait(kBarX + w, n_sync++ & 1);
+      tc_fence_after();
+      return met;
+    };
     if (T == 0) {   // an empty sequence: zero rows
       if (valid)
-        for (int c = 0; c < a.d_h / 8; ++c) reinterpret_cast<uint4*>(a.out + row * a.d_h)[c] = make_uint4(0, 0, 0, 0);
+        for (int c = hf; c < a.d_h / 8; c += 2) reinterpret_cast<uint4*>(a.out + row * a.d_h)[c] = make_uint4(0, 0, 0, 0);
     } else {
-      // q row into tensor memory; the rotated kept pairs, scaled, into this row's KV head chunk
-      // of the block-diagonal RoPE operand
-      const uint4* qsrc = reinterpret_cast<const uint4*>(a.q + row * a.d_h);
-      for (int c0 = 0; c0 < a.d_h / 2; c0 += 32) {   // 32 columns = 64 values
-        uint32_t v[32];
+      // q row into tensor memory (blocks of 16 values in turn), the rotated kept pairs, scaled,
+      // into this row's KV head chunk of the block-diagonal RoPE operand
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 x = valid && c0 + 4 * j < a.d_h / 2 ? __ldg(qsrc + c0 / 4 + j) : make_uint4(0, 0, 0, 0);
-          v[4 * j] = x.x; v[4 * j + 1] = x.y; v[4 * j + 2] = x.z; v[4 * j + 3] = x.w;
+      for (int j = 0; j < 4; ++j) {
+        if (8 * (hf + 2 * j) < a.d_h / 2) {
+          const uint32_t v[8] = {qv[2 * j].x, qv[2 * j].y, qv[2 * j].z, qv[2 * j].w,
+                                 qv[2 * j + 1].x, qv[2 * j + 1].y, qv[2 * j + 1].z, qv[2 * j + 1].w};
+          tmem_st8(lane0 + kSCol + 8 * (hf + 2 * j), v);
         }
-        tmem_st32(lane0 + kSCol + c0, v);
       }
       {
-        uint32_t rot[4] = {0, 0, 0, 0};
+        uint32_t rot[2] = {0, 0};
         if (valid) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = __ldg(a.rope_pair + g * 4 + j);
-            const uint32_t xy = __ldg(reinterpret_cast<const uint32_t*>(a.q + row * a.d_h) + k);
+          for (int j = 0; j < 2; ++j) {
+            // the special-function unit's sine and cosine of an angle reduced to [-pi, pi]:
+            // about 5e-7 off, against the 2^-9 of the bf16 rounding that follows
             float sn, cs;
-            rope_sincos(p0 + qi, __ldg(a.theta + k), &sn, &cs);
-            rot[j] = pack2((lo_f(xy) * cs - hi_f(xy) * sn) * a.scale, (lo_f(xy) * sn + hi_f(xy) * cs) * a.scale);
+            __sincosf(rope_angle(p0 + qi, theta[j]), &sn, &cs);
+            const float x = lo_f(xy[j]), y = hi_f(xy[j]);
+            rot[j] = pack2((x * cs - y * sn) * a.scale, (x * sn + y * cs) * a.scale);
           }
         }
+        uint8_t* qr = smem + a.off_qr + r * 64;
 #pragma unroll
         for (int c = 0; c < kMaxG; ++c)
-          *reinterpret_cast<uint4*>(smem + a.off_qr + r * 64 + ((c ^ (r >> 1)) & 3) * 16) =
-              c == gi ? make_uint4(rot[0], rot[1], rot[2], rot[3]) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint2*>(qr + ((c ^ (r >> 1)) & 3) * 16 + 8 * hf) = c == gi ? make_uint2(rot[0], rot[1]) : make_uint2(0, 0);
       }
       tmem_wait_st();
       fence_proxy_async_smem();
@@ -301,11 +401,13 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       // Q_lat: the accumulator's rows of each KV head, scaled, rounded to bf16 (the product's
       // operand type)
       bool ok = true;
+#pragma unroll 1
       for (int k = 0; ok && k < ng; ++k) {
         ok = wwait(kBarAccFull, k & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int c0 = 0; c0 < a.dcp; c0 += 32) {
+#pragma unroll 1
+        for (int c0 = hf * (a.dcp / 2); c0 < (hf + 1) * (a.dcp / 2); c0 += 32) {
           uint32_t v[32];
           tmem_ld32(lane0 + kOCol + c0, v);
           tmem_wait_ld();
@@ -325,23 +427,24 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       }
       fence_proxy_async_smem();
       if (ok) arrive(kBarQlat);
-      // tiles
+      // tiles: this thread's tokens are [64 hf, 64 hf + 64) of each
       const int p_row = valid ? p0 + qi : -1;
       float m = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int n = 0; ok && n < T; ++n) {
         const int t0 = tile_token(n), nvalid = min(kT, span.len - n * kT);
         ok = wwait(kBarS + (n & 1), (n >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t scol = lane0 + kSCol + (n & 1) * kT;
-        float s[kT];
+        float s[64];
         {
-          uint32_t raw[4][32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(scol + 32 * k, raw[k]);
+          uint32_t raw[2][32];
+          tmem_ld32(scol + 64 * hf, raw[0]);
+          tmem_ld32(scol + 64 * hf + 32, raw[1]);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < kT; ++e) {
+          for (int e = 0; e < 64; ++e) {
             asm volatile("" : "+r"(raw[e / 32][e % 32]));   // the values exist only after the wait
             s[e] = __uint_as_float(raw[e / 32][e % 32]);
           }
@@ -349,24 +452,34 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         // tiles whose tokens every query of the unit sees need no mask
         const bool whole = nvalid == kT && t0 + kT - 1 <= p0 && (t0 > p0 + nq - 1 - a.win.window || t0 + kT <= a.win.n_sink);
         if (!whole) {
-          const int lim_t = min(nvalid, p_row + 1 - t0);
-          const int sink_t = a.win.n_sink - t0, win_t = p_row + 1 - a.win.window - t0;
+          const int h0 = t0 + 64 * hf;
+          const int lim_t = min(nvalid - 64 * hf, p_row + 1 - h0);
+          const int sink_t = a.win.n_sink - h0, win_t = p_row + 1 - a.win.window - h0;
+          // bit t: token t of the half is before lim_t, and before sink_t or from win_t on
+          const uint64_t seen = below64(lim_t) & (below64(sink_t) | ~below64(win_t));
 #pragma unroll
-          for (int t = 0; t < kT; ++t) s[t] = t < lim_t && (t >= win_t || t < sink_t) ? s[t] : -INFINITY;
+          for (int t = 0; t < 64; ++t) s[t] = ((uint32_t)(seen >> (t & 32)) >> (t & 31)) & 1u ? s[t] : -INFINITY;
           // rows that no query of the unit sees (stale or hidden, possibly not finite) are
           // zeroed before O's product multiplies them by P = 0; S of this tile has been read
-          if (r >= nvalid || (t0 + r >= a.win.n_sink && t0 + r < span.lo)) {
-            uint8_t* C = smem + a.off_ring + (uint32_t)((ng + n) % NST) * a.stage;
-            for (int k = 0; k < n_cbox; ++k)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(C + k * kBox + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-          }
+          uint8_t* C = smem + a.off_ring + (uint32_t)((ng + n) % NST) * a.stage;
+          auto zero_rows = [&](int from, int to) {   // consecutive threads, consecutive 16-byte chunks
+            for (int i = from * 8 + 128 * hf + r; i < to * 8; i += 256)
+              for (int k = 0; k < n_cbox; ++k) *reinterpret_cast<uint4*>(C + k * kBox + i * 16) = make_uint4(0, 0, 0, 0);
+          };
+          zero_rows(max(0, a.win.n_sink - t0), min(nvalid, span.lo - t0));
+          zero_rows(nvalid, kT);
           fence_proxy_async_smem();
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < kT; ++t) mx[t & 3] = fmaxf(mx[t & 3], s[t]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int t = 0; t < 64; ++t) mx[t & 3] = fmaxf(mx[t & 3], s[t]);
+        // the row's maximum over both halves; past this barrier both have read their S, so P
+        // may go over it
+        float* xm = xchg + (n & 1) * 2 * kRows;
+        xm[hf * kRows + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        ok = pair_sync();
+        if (!ok) break;
+        const float top = fmaxf(xm[r], xm[kRows + r]);
         // The running max is raised when a row outgrew it by more than kTau (P stays below
         // 2^kTau, in range for bf16 and the float32 sums); the loads and stores of O are
         // warp-collective, so the other rows multiply by 1.
@@ -377,7 +490,8 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
             ok = wwait(kBarO + ((n - 1) & 1), ((n - 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            for (int c0 = 0; c0 < a.dcp; c0 += 32) {
+#pragma unroll 1
+            for (int c0 = hf * (a.dcp / 2); c0 < (hf + 1) * (a.dcp / 2); c0 += 32) {
               uint32_t o[32];
               tmem_ld32(lane0 + kOCol + c0, o);
               tmem_wait_ld();
@@ -385,7 +499,6 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
               for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
               tmem_st32(lane0 + kOCol + c0, o);
             }
-            tmem_wait_st();
           }
           if (raise) {
             l *= al;
@@ -394,51 +507,61 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         }
         const float mb = m == -INFINITY ? 0.f : m;   // masked scores are -inf: 2^(-inf) = 0
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];   // P, rounded to bf16 (the product's operand type)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {   // P, rounded to bf16 (the product's operand type), over S
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = ex2_approx(s[64 * k + 2 * e] - mb), y = ex2_approx(s[64 * k + 2 * e + 1] - mb);
-            sum[(2 * e) & 3] += x;
-            sum[(2 * e + 1) & 3] += y;
-            pk[e] = pack2(x, y);
-          }
-          tmem_st32(scol + 32 * k, pk);
+        for (int e = 0; e < 32; ++e) {
+          const float x = ex2_approx(s[2 * e] - mb), y = ex2_approx(s[2 * e + 1] - mb);
+          sum[(2 * e) & 3] += x;
+          sum[(2 * e + 1) & 3] += y;
+          pk[e] = pack2(x, y);
         }
+        tmem_st32(scol + 32 * hf, pk);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
         arrive(kBarP + (n & 1));
       }
       // merged latent, normalised, in two bf16 halves (so that this rounding does not count):
-      // the high ones over S, the low ones over the columns of O already read
+      // the high ones over S, the low ones, once both threads have read their part, over O
       if (ok) ok = wwait(kBarO + ((T - 1) & 1), ((T - 1) >> 1) & 1);
       if (ok) {
-        tc_fence_after();
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        for (int c0 = 0; c0 < a.d_c; c0 += 32) {
-          uint32_t v[32], hi2[16], lo2[16];
-          tmem_ld32(lane0 + kOCol + c0, v);
+        float* xl = xchg + (T & 1) * 2 * kRows;   // (the last tile's maxima may still be read)
+        xl[hf * kRows + r] = l;
+        ok = pair_sync();
+        const float den = xl[r] + xl[kRows + r];
+        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const int half = a.d_c / 2, c_at = hf * half;   // a multiple of 16 up to 128
+        uint32_t lo2[8][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (16 * j >= half) continue;
+          uint32_t v[16], hi2[8];
+          tmem_ld16(lane0 + kOCol + c_at + 16 * j, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 8; ++e) {
+            asm volatile("" : "+r"(v[2 * e]), "+r"(v[2 * e + 1]));
             const float x = __uint_as_float(v[2 * e]) * inv, y = __uint_as_float(v[2 * e + 1]) * inv;
             hi2[e] = pack2(x, y);
-            lo2[e] = pack2(x - lo_f(hi2[e]), y - hi_f(hi2[e]));
+            lo2[j][e] = pack2(x - lo_f(hi2[e]), y - hi_f(hi2[e]));
           }
-          tmem_st16(lane0 + kSCol + c0 / 2, hi2);
-          tmem_st16(lane0 + kOCol + c0 / 2, lo2);
+          tmem_st8(lane0 + kSCol + c_at / 2 + 8 * j, hi2);
         }
+        ok = pair_sync() && ok;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (16 * j < half) tmem_st8(lane0 + kOCol + c_at / 2 + 8 * j, lo2[j]);
         tmem_wait_st();
         tc_fence_before();
         arrive(kBarA);
       }
+#pragma unroll 1
       for (int k = 0; ok && k < ng; ++k) {
         ok = wwait(kBarAccFull, (ng + k) & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int c0 = 0; c0 < a.d_h; c0 += 16) {
+#pragma unroll 1
+        for (int c0 = 16 * hf; c0 < a.d_h; c0 += 32) {
           uint32_t v[16];
           tmem_ld16(lane0 + kSCol + kT + c0, v);
           tmem_wait_ld();
@@ -500,19 +623,20 @@ static bool map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t row
 
 struct Layout {
   int NST;
-  uint32_t stage, off_qr, off_ring, off_bar, total;
+  uint32_t stage, off_qr, off_ring, off_xchg, off_bar, total;
 };
-// [Q_lat boxes][RoPE queries][ring of 2 to 4 stages][barriers]
+// [Q_lat boxes][RoPE queries][ring of 2 to 4 stages][row exchange][barriers]
 static Layout layout(int dcp) {
   Layout L{};
   const uint32_t n_cbox = dcp / 64;
   L.stage = n_cbox * kBox + kKrTile;
   L.off_qr = n_cbox * kBox;
   L.off_ring = L.off_qr + kRows * 64;
-  const uint32_t tail = 8 * kBars + 16;
+  const uint32_t tail = 4 * kRows * 4 + 8 * kBars + 16;
   L.NST = (int)std::min<uint32_t>(4, (kSmemMax - 1024 - L.off_ring - tail) / L.stage);
-  L.off_bar = L.off_ring + L.NST * L.stage;
-  L.total = L.off_bar + tail + 1024;
+  L.off_xchg = L.off_ring + L.NST * L.stage;
+  L.off_bar = L.off_xchg + 4 * kRows * 4;
+  L.total = L.off_xchg + tail + 1024;
   return L;
 }
 
@@ -563,7 +687,7 @@ cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, con
   a.rope_pair = p.rope_pair; a.theta = p.theta; a.cache = c; a.err = p.err;
   a.wait_ns = (uint64_t)p.opt_wait_us * 1000u;
   const Layout L = layout(a.dcp);
-  a.NST = L.NST; a.stage = L.stage; a.off_qr = L.off_qr; a.off_ring = L.off_ring; a.off_bar = L.off_bar;
+  a.NST = L.NST; a.stage = L.stage; a.off_qr = L.off_qr; a.off_ring = L.off_ring; a.off_xchg = L.off_xchg; a.off_bar = L.off_bar;
   const uint64_t rows = mla_cache_rows(c);
   CUtensorMap tm_c, tm_kr, tm_uk, tm_uv;
   if (!map_2d(&tm_c, c.c_kv, a.d_c, rows, 64, kT) || !map_2d(&tm_kr, c.k_rope, p.R, rows, 32, kT) ||
@@ -574,7 +698,7 @@ cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, con
   cudaError_t e = mla_smem_limit((const void*)kern, L.total);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
-  e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(256), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);
+  e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(kThreads), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);
   if (e != cudaSuccess) return e;
   return mla_profile_event(p, kProfAttention, true, s);
 }
