@@ -376,96 +376,102 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
     }
   } else if (warp == GG::MMA) {
     // ============================================================ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc1 = idesc_bf16_f32(GG::M, kCT, false, false);   // S[row][t]
-      const uint32_t idesc2 = idesc_bf16_f32(GG::M, dcp, false, true);    // O[row][d]
-      TileIter<WIN> it;
-      it.init(&a, w);
-      int n = 0, u = 0;
-      bool ok = true;
-      int pend_n = -1, pend_u = 0;
-      bool pend_first = false, pend_last = false;
-      auto do_mma2 = [&](int pn, int pu, bool first, bool lastp) -> bool {
-        const int pb = pn & 1, cs = pn % a.NC;
-        if (!mbar_wait(bars.p_full(pb), (pn >> 1) & 1, abort_flag, lim)) return false;
-        if (first && pu > 0)
-          if (!mbar_wait(bars.o_empty(), (pu - 1) & 1, abort_flag, lim)) return false;
-        tc_fence_after();
-        const uint32_t c0 = sbase_u32 + a.off_c + cs * a.c_stage;
-        const uint32_t p0 = sbase_u32 + a.off_p + pb * kPBytes;
+    // The warp walks one path (every condition the same in all lanes) and an elected lane
+    // issues, so that the descriptors stay in uniform registers; they are made once per operand
+    // and a step along K adds its bytes / 16 to the address field.
+    const uint32_t idesc1 = idesc_bf16_f32(GG::M, kCT, false, false);   // S[row][t]
+    const uint32_t idesc2 = idesc_bf16_f32(GG::M, dcp, false, true);    // O[row][d]
+    const uint64_t desc_q = smem_desc(sbase_u32 + a.off_q, 16, 1024, kLayoutSW128);
+    const uint64_t desc_ar = smem_desc(sbase_u32 + a.off_ar, 16, 1024, kLayoutSW128);
+    auto wait_all = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim)) != 0; };
+    auto ready = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)) != 0; };
+    TileIter<WIN> it;
+    it.init(&a, w);
+    int n = 0, u = 0;
+    bool ok = true;
+    int pend_n = -1, pend_u = 0;
+    bool pend_first = false, pend_last = false;
+    auto do_mma2 = [&](int pn, int pu, bool first, bool lastp) -> bool {
+      const int pb = pn & 1, cs = pn % a.NC;
+      if (!wait_all(bars.p_full(pb), (pn >> 1) & 1)) return false;
+      if (first && pu > 0)
+        if (!wait_all(bars.o_empty(), (pu - 1) & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t ad = smem_desc(sbase_u32 + a.off_p + pb * kPBytes, 16, 1024, kLayoutSW128);
+        const uint64_t bd = smem_desc(sbase_u32 + a.off_c + cs * a.c_stage, kTBox, 1024, kLayoutSW128);
+        tc_mma_bf16(tmem + kOCol, ad, bd, idesc2, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 0; kk < kCT / 16; ++kk) {
-          const uint64_t ad = smem_desc(p0 + kk * 32, 16, 1024, kLayoutSW128);
-          const uint64_t bd = smem_desc(c0 + kk * 2048, kTBox, 1024, kLayoutSW128);
-          tc_mma_bf16(tmem + kOCol, ad, bd, idesc2, (first && kk == 0) ? 0u : 1u);
-        }
+        for (int kk = 1; kk < kCT / 16; ++kk) tc_mma_bf16(tmem + kOCol, ad + 2 * kk, bd + 128 * kk, idesc2, 1u);
         tc_commit(bars.p_empty(pb));
         tc_commit(bars.c_empty(cs));
         if (lastp) tc_commit(bars.o_full());
-        return true;
-      };
-      while (ok && it.valid()) {
-        const int sb = n & 1, cs = n % a.NC, ks = n % a.NK;
-        const bool first = it.first_of_piece();
-        {
-          const uint64_t t_start = globaltimer();
-          while (true) {
-            if (pend_n >= 0 && mbar_test(bars.p_full(pend_n & 1), (pend_n >> 1) & 1)) {
-              ok = do_mma2(pend_n, pend_u, pend_first, pend_last);
-              pend_n = -1;
-              if (!ok) break;
-              continue;
-            }
-            if ((n < 2 || mbar_test(bars.s_empty(sb), ((n >> 1) - 1) & 1)) &&
-                (!first || mbar_test(bars.q_full(), u & 1)) && mbar_test(bars.c_full(cs), (n / a.NC) & 1) &&
-                (!rtc || mbar_test(bars.k_full(ks), (n / a.NK) & 1)))   // MMA1 reads keys only with rtc
-              break;
-            if (*abort_flag || globaltimer() - t_start > lim) {
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-            __nanosleep(32);   // leave the scheduler's issue slots to the other warps
-          }
-        }
-        if (!ok) break;
-        tc_fence_after();
-        {  // MMA1: S = Q_lat C^T (+ Q_rope KR^T)
-          const uint32_t c0 = sbase_u32 + a.off_c + cs * a.c_stage;
-          const uint32_t d = tmem + kSCol + sb * kCT;
-          for (int kk = 0; kk < dcp / 16; ++kk) {
-            const uint64_t ad = smem_desc(sbase_u32 + a.off_q + (kk >> 2) * kQBox + (kk & 3) * 32, 16, 1024,
-                                          kLayoutSW128);
-            const uint64_t bd = smem_desc(c0 + (kk >> 2) * kTBox + (kk & 3) * 32, 16, 1024, kLayoutSW128);
-            tc_mma_bf16(d, ad, bd, idesc1, kk > 0 ? 1u : 0u);
-          }
-          if (rtc) {
-            const uint32_t k0 = sbase_u32 + a.off_k + ks * a.k_stage;
-            for (int kk = 0; kk < kr16; ++kk) {
-              const uint64_t ad = smem_desc(sbase_u32 + a.off_ar + (kk >> 2) * kQBox + (kk & 3) * 32, 16, 1024,
-                                            kLayoutSW128);
-              const uint64_t bd = smem_desc(k0 + (kk >> 2) * kTBox + (kk & 3) * 32, 16, 1024, kLayoutSW128);
-              tc_mma_bf16(d, ad, bd, idesc1, 1u);
-            }
-            tc_commit(bars.k_empty(ks));
-          }
-          tc_commit(bars.s_full(sb));
-          if (it.last_of_piece()) tc_commit(bars.q_empty());
-        }
-        if (pend_n >= 0) {
-          ok = do_mma2(pend_n, pend_u, pend_first, pend_last);
-          if (!ok) break;
-        }
-        pend_n = n; pend_u = u; pend_first = first; pend_last = it.last_of_piece();
-        if (it.last_of_piece()) ++u;
-        it.next();
-        ++n;
       }
-      if (ok && pend_n >= 0) do_mma2(pend_n, pend_u, pend_first, pend_last);
-      tc_commit(bars.mma_done());
-      volatile int never = 0;
-      mbar_wait(bars.mma_done(), 0, &never, lim);
+      __syncwarp();
+      return true;
+    };
+    while (ok && it.valid()) {
+      const int sb = n & 1, cs = n % a.NC, ks = n % a.NK;
+      const bool first = it.first_of_piece();
+      {
+        const uint64_t t_start = globaltimer();
+        while (true) {
+          if (pend_n >= 0 && ready(bars.p_full(pend_n & 1), (pend_n >> 1) & 1)) {
+            ok = do_mma2(pend_n, pend_u, pend_first, pend_last);
+            pend_n = -1;
+            if (!ok) break;
+            continue;
+          }
+          if ((n < 2 || ready(bars.s_empty(sb), ((n >> 1) - 1) & 1)) &&
+              (!first || ready(bars.q_full(), u & 1)) && ready(bars.c_full(cs), (n / a.NC) & 1) &&
+              (!rtc || ready(bars.k_full(ks), (n / a.NK) & 1)))   // MMA1 reads keys only with rtc
+            break;
+          if (__any_sync(0xffffffffu, *abort_flag || globaltimer() - t_start > lim)) {
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          __nanosleep(32);   // leave the scheduler's issue slots to the other warps
+        }
+      }
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {  // MMA1: S = Q_lat C^T (+ Q_rope KR^T), a box of 64 columns is four steps
+        const uint32_t d = tmem + kSCol + sb * kCT;
+        uint64_t ad = desc_q, bd = smem_desc(sbase_u32 + a.off_c + cs * a.c_stage, 16, 1024, kLayoutSW128);
+        for (int kb = 0; kb < n_cbox; ++kb) {
+          tc_mma_bf16(d, ad, bd, idesc1, kb > 0 ? 1u : 0u);
+          tc_mma_bf16(d, ad + 2, bd + 2, idesc1, 1u);
+          tc_mma_bf16(d, ad + 4, bd + 4, idesc1, 1u);
+          tc_mma_bf16(d, ad + 6, bd + 6, idesc1, 1u);
+          ad += kQBox >> 4;
+          bd += kTBox >> 4;
+        }
+        if (rtc) {
+          const uint64_t kd = smem_desc(sbase_u32 + a.off_k + ks * a.k_stage, 16, 1024, kLayoutSW128);
+          for (int kk = 0; kk < kr16; ++kk)
+            tc_mma_bf16(d, desc_ar + (kk >> 2) * (kQBox >> 4) + (kk & 3) * 2, kd + (kk >> 2) * (kTBox >> 4) + (kk & 3) * 2,
+                        idesc1, 1u);
+          tc_commit(bars.k_empty(ks));
+        }
+        tc_commit(bars.s_full(sb));
+        if (it.last_of_piece()) tc_commit(bars.q_empty());
+      }
+      __syncwarp();
+      if (pend_n >= 0) {
+        ok = do_mma2(pend_n, pend_u, pend_first, pend_last);
+        if (!ok) break;
+      }
+      pend_n = n; pend_u = u; pend_first = first; pend_last = it.last_of_piece();
+      if (it.last_of_piece()) ++u;
+      it.next();
+      ++n;
     }
+    if (ok && pend_n >= 0) do_mma2(pend_n, pend_u, pend_first, pend_last);
+    if (elect_one()) tc_commit(bars.mma_done());
+    __syncwarp();
+    volatile int never = 0;
+    mbar_wait(bars.mma_done(), 0, &never, lim);
   } else if (QUANT && Crew<ROWS, QB>::dq_index(warp) >= 0) {
     // ============================================================ dequantisation
     // thread = token row of the tile (with four dequantising warps: a token row and the
