@@ -672,6 +672,10 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
     e = mla_launch_kernel(decode_simt_kernel<T, INT4>, dim3(L.G), dim3(256), smem, s, p.opt_pdl, da);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, true, s)) != cudaSuccess) return e;
+  } else if (L.kernel == 4 && aa.win.window > 0 && p.opt_kernel == 0 && mla_window_decode_capable(p)) {
+    e = mla_launch_window_decode(p, c, seq_lens, B, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
+                                 (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, aa.win, s);
+    if (e != cudaSuccess) return e;
   } else if (L.kernel == 4) {
     e = mla_launch_chunk_tc(p, c, seq_lens, B, 1, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
                             (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, s,

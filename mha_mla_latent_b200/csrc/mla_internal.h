@@ -189,6 +189,12 @@ bool mla_window_fused_capable(const mla_plan& p);
 cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
                                     int B, int Q, void* out, MlaWindow win, cudaStream_t s);
 
+// The windowed decode's split attention for up to 32 heads (window_decode.cu).
+bool mla_window_decode_capable(const mla_plan& p);
+cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, int B,
+                                     const Sched& sched, const void* qlat, const float* qrope, float* opart,
+                                     float* mlpart, int P, int G, MlaWindow win, cudaStream_t s);
+
 cudaError_t mla_launch_select_pairs(const mla_config_t& cfg, const void* q, const void* k, int T,
                                     int32_t* pair_idx, float* contrib, cudaStream_t s);
 cudaError_t mla_launch_append(const mla_plan& p, const void* x, const int32_t* seq_idx,

@@ -82,30 +82,6 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d, uint32_t a, uint64_t b_de
       : "memory");
 }
 
-// Waits for the phase of the given parity without suspending; false when the wait exceeds
-// `limit_ns` or another role gave up.
-__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
-  if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_test(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > limit_ns) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-// 32 lanes x 8 consecutive columns.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 // Bits 0 .. n-1 of 64 (n outside [0, 64] cut to it).
 __device__ __forceinline__ uint64_t below64(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
@@ -174,7 +150,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   const size_t row = ((size_t)b * a.Q + q0 + qi) * a.H + g * a.G + hi;
   const uint32_t lane0 = tmem + ((uint32_t)(32 * w) << 16);
   float* xchg = reinterpret_cast<float*>(smem + a.off_xchg);   // [2][2 halves][rows]
-  auto wwait = [&](int i, int parity) { return __all_sync(0xffffffffu, spin_wait(bar(i), parity, abort_flag, lim)); };
+  auto wwait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)); };
   int pair[2] = {0, 0};
   double theta[2] = {0, 0};
   if (valid) {
@@ -216,7 +192,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       bool ok = true;
       while (ok && loaded < items) {
         const int i = loaded, s = i % NST;
-        if (i >= NST) ok = spin_wait(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
+        if (i >= NST) ok = mbar_spin(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
         if (!ok) break;
         if (i < ng) { load_uk(i); continue; }
         if (i < ng + T) {
@@ -235,7 +211,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         ++loaded;
       }
       volatile int never = 0;   // every copy lands before the CTA exits
-      for (int i = max(0, loaded - NST); i < loaded; ++i) spin_wait(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
+      for (int i = max(0, loaded - NST); i < loaded; ++i) mbar_spin(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer
@@ -244,7 +220,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
     // from a branch of lane 0 a product took 110 to 190 cycles, more than most of them compute.)
     if (T > 0) {
       auto wait_all = [&](int i, int parity) {
-        return __all_sync(0xffffffffu, spin_wait(bar(i), parity, abort_flag, lim)) != 0;
+        return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)) != 0;
       };
       auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
       auto full = [&](int i) { return wait_all(kBarFull + i % NST, (i / NST) & 1); };
@@ -337,7 +313,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       if (elect_one()) tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
       __syncwarp();
       volatile int never = 0;
-      spin_wait(bar(kBarDone), 0, &never, lim);
+      mbar_spin(bar(kBarDone), 0, &never, lim);
     }
   } else if (warp >= 4) {
     // ============================================================ rows
