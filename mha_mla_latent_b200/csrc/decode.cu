@@ -638,7 +638,7 @@ cudaError_t launch_combine(const mla_plan& p, int units, int H, int n_kv, int q_
   const size_t smem_c = (size_t)cfg.d_c * (ca.ncols + RB) * sizeof(float) +
                         (size_t)RBP * (cfg.d_c + 8) * sizeof(__nv_bfloat16);   // + the MMA form's A tiles
   const int n_rbc = (units * G + RB - 1) / RB, n_dc = (cfg.head_dim + ca.ncols - 1) / ca.ncols;
-  cudaError_t e = cudaFuncSetAttribute(combine_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_c);
+  cudaError_t e = mla_smem_limit((const void*)combine_kernel<T>, smem_c);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfCombine, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(combine_kernel<T>, dim3(n_kv * n_rbc * n_dc), dim3(256), smem_c, s, p.opt_pdl, ca);
@@ -665,17 +665,12 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
     size_t smem = sizeof(float) * ((size_t)H * cfg.d_c + H * 2 * cfg.r_pairs +
                                    kSimtTile * (cfg.d_c + 1) + kSimtTile * (p.R + 1) +
                                    kSimtTile * H + 3 * H);
-    e = cudaFuncSetAttribute(decode_simt_kernel<T, INT4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+    e = mla_smem_limit((const void*)decode_simt_kernel<T, INT4>, smem);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
     e = mla_launch_kernel(decode_simt_kernel<T, INT4>, dim3(L.G), dim3(256), smem, s, p.opt_pdl, da);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, true, s)) != cudaSuccess) return e;
-  } else if (L.kernel == 4 && aa.win.window > 0 && p.opt_kernel == 0 && mla_window_decode_capable(p)) {
-    e = mla_launch_window_decode(p, c, seq_lens, B, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
-                                 (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, aa.win, s);
-    if (e != cudaSuccess) return e;
   } else if (L.kernel == 4) {
     e = mla_launch_chunk_tc(p, c, seq_lens, B, 1, sched, base + L.off_qlat, (const float*)(base + L.off_qrope),
                             (float*)(base + L.off_opart), (float*)(base + L.off_mlpart), L.P, L.G, s,
@@ -697,7 +692,7 @@ cudaError_t launch_decode_t(const mla_plan& p, const mla_cache_t& c, const int32
   size_t smem_abs;
   int nblk;
   absorb_setup<T>(p, c, seq_lens, q, B, ws, L, win, &aa, &smem_abs, &nblk);
-  cudaError_t e = cudaFuncSetAttribute(absorb_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_abs);
+  cudaError_t e = mla_smem_limit((const void*)absorb_kernel<T>, smem_abs);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(absorb_kernel<T>, dim3(nblk), dim3(256), smem_abs, s, p.opt_pdl, aa);
@@ -752,7 +747,7 @@ cudaError_t launch_step_t(const mla_plan& p, const mla_cache_t& c, const int32_t
   sp.app_gy = (int)agrid.y;
   const int nblk = nabs + (int)(agrid.x * agrid.y * agrid.z);
   const size_t smem = std::max(smem_app, smem_abs);
-  cudaError_t e = cudaFuncSetAttribute(step_pre_kernel<INT4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = mla_smem_limit((const void*)step_pre_kernel<INT4>, smem);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(step_pre_kernel<INT4>, dim3(nblk), dim3(256), smem, s, p.opt_pdl, sp);
@@ -775,7 +770,7 @@ cudaError_t launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t*
   absorb_setup<bf16>(p, c, seq_lens, q, B * Q, ws, L, win, &aa, &smem_abs, &nblk);
   aa.q_chunk = Q;
   aa.q_block = kQB;
-  cudaError_t e = cudaFuncSetAttribute(absorb_kernel<bf16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_abs);
+  cudaError_t e = mla_smem_limit((const void*)absorb_kernel<bf16>, smem_abs);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(absorb_kernel<bf16>, dim3(nblk), dim3(256), smem_abs, s, p.opt_pdl, aa);
@@ -797,9 +792,9 @@ DecodeLayout mla_decode_layout(const mla_plan& p, int B, int kernel) {
   const mla_config_t& cfg = p.cfg;
   DecodeLayout L;
   L.kernel = kernel;
-  L.tile = kernel == 2 ? 128 : kernel == 4 ? 64 : mla::kSimtTile;
+  L.tile = kernel == 2 ? 128 : kernel >= 4 ? 64 : mla::kSimtTile;
   // the tensor-core kernels hold one CTA per SM (one wave); the CUDA-core kernel two
-  L.G = p.opt_splits > 0 ? p.opt_splits : (kernel == 2 || kernel == 4 ? p.num_sms : 2 * p.num_sms);
+  L.G = p.opt_splits > 0 ? p.opt_splits : (kernel == 1 ? 2 * p.num_sms : p.num_sms);
   L.P = B + L.G;
   L.K = cfg.d_c + p.R;
   const int H = cfg.n_heads;
@@ -811,7 +806,7 @@ DecodeLayout mla_decode_layout(const mla_plan& p, int B, int kernel) {
   L.off_seq_first = take(sizeof(int32_t) * B);
   L.off_seq_np = take(sizeof(int32_t) * B);
   L.off_worker_first = take(sizeof(int32_t) * (L.G + 1));
-  L.off_piece_b = take(sizeof(int32_t) * L.P);
+  L.off_piece_b = take(sizeof(int32_t) * (kernel == 5 ? 4 : 1) * L.P);   // windowed decode: whole pieces
   L.off_piece_t0 = take(sizeof(int32_t) * L.P);
   L.off_piece_t1 = take(sizeof(int32_t) * L.P);
   if (L.kernel == 1)
@@ -880,6 +875,7 @@ cudaError_t mla_launch_decode(const mla_plan& p, const mla_cache_t& c, const int
                               const void* q, int B, void* out, void* ws, const DecodeLayout& L,
                               cudaStream_t s, MlaWindow win) {
   using namespace mla;
+  if (L.kernel == 5) return mla_launch_window_decode(p, c, seq_lens, q, B, out, ws, L, win, s);
   const bool quant = mla_kind_quant(p.cfg.cache_kind);   // int4 or int2 codes
   if (p.cfg.dtype == MLA_BF16)
     return quant ? launch_decode_t<__nv_bfloat16, true>(p, c, seq_lens, q, B, out, ws, L, s, win)

@@ -216,4 +216,31 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
   }
 }
 
+// ------------------------------------------------------------------ windowed decode
+// The windowed decode's split needs no schedule in memory: every CTA sums the sequences' units
+// itself (units of `tile` visible tokens, laid end to end, cut into G equal ranges).  A piece is
+// the part of sequence b in worker w's range, and its partial goes to slot w + (non-empty
+// sequences before b): slots of one sequence are consecutive, and all are below B + G.
+//
+// A sequence counts kSeqCost units more than it has, ahead of its own: beginning a piece costs
+// a worker about that long, so workers with a sequence's end and the next one's start get fewer.
+constexpr int kSeqCost = 2;
+struct SeqUnits {
+  int len = 0, n = 0;   // visible tokens, units with kSeqCost (0 for an empty sequence)
+};
+__device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, MlaWindow win) {
+  SeqUnits s;
+  if (b >= B) return s;
+  const int L = __ldg(seq_lens + b);
+  if (L <= 0 || L > T_cap) return s;
+  s.len = unit_span(L, 1, tile, win).len;
+  s.n = (s.len + tile - 1) / tile + kSeqCost;
+  return s;
+}
+// Workers that get units: no more than there are units, so that none in between is empty.
+__device__ __forceinline__ int busy_workers(int total, int G) { return min(total, G); }
+__device__ __forceinline__ long long worker_begin(int w, int total, int G) { return (long long)w * total / G; }
+// The worker whose range holds unit c of `total` (the last one that starts at or before it).
+__device__ __forceinline__ int worker_of(long long c, int total, int G) { return (int)(((c + 1) * G - 1) / total); }
+
 }  // namespace mla

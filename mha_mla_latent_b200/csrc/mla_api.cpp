@@ -133,7 +133,8 @@ mla_status_t mla_pick_window_kernel(const mla_plan& p, const mla_cache_t& c, int
   *kernel = 1;
   if (p.opt_kernel == 2) return MLA_ERR_UNSUPPORTED;   // the token-row kernel has no window
   if (p.opt_kernel != 1) {
-    if (mla_decode_t_supported(p, c)) *kernel = 4;
+    if (p.opt_kernel == 0 && mla_window_decode_capable(p)) *kernel = 5;
+    else if (mla_decode_t_supported(p, c)) *kernel = 4;
     else if (p.opt_kernel == 3) return MLA_ERR_UNSUPPORTED;
   }
   if (*kernel == 1 && (size_t)p.cfg.n_heads * p.cfg.d_c > 8192) return MLA_ERR_UNSUPPORTED;
@@ -406,6 +407,7 @@ size_t mla_decode_workspace_bytes(const mla_plan_t* plan, int32_t B) {
   size_t n = mla_decode_layout(*plan, B, 1).total;
   if (mla_tc_capable(*plan)) n = std::max(n, mla_decode_layout(*plan, B, 2).total);
   if (mla_decode_t_capable(*plan)) n = std::max(n, mla_decode_layout(*plan, B, 4).total);
+  if (mla_window_decode_capable(*plan)) n = std::max(n, mla_decode_layout(*plan, B, 5).total);
   return host_stage(*plan, B, n).total;
 }
 

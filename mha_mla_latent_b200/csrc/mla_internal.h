@@ -133,7 +133,8 @@ inline cudaError_t mla_profile_event(const mla_plan& p, MlaProfKernel k, bool af
 // Decode workspace layout (byte offsets from the workspace base).
 struct DecodeLayout {
   int kernel = 1;          // 1 CUDA-core, 2 tcgen05 decode (token rows), 3 tcgen05 query
-                           // chunks, 4 tcgen05 decode (head rows: the chunk kernel's form)
+                           // chunks, 4 tcgen05 decode (head rows: the chunk kernel's form),
+                           // 5 tcgen05 windowed decode
   int tile = 32;           // tokens per schedule tile
   int G = 0;               // workers (CTAs of the split-K kernel)
   int P = 0;               // max pieces = B + G
@@ -178,7 +179,7 @@ bool mla_decode_t_capable(const mla_plan& p);
 bool mla_decode_t_supported(const mla_plan& p, const mla_cache_t& c);
 // The decode kernel a call runs (layout kernel id 1, 2 or 4), or the status refusing the call.
 mla_status_t mla_pick_decode_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel);
-// The same for a decode with a sliding window (layout kernel id 1 or 4).
+// The same for a decode with a sliding window (layout kernel id 1, 4 or 5).
 mla_status_t mla_pick_window_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel);
 cudaError_t mla_launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
                              int B, int Q, void* out, void* ws, const DecodeLayout& L, cudaStream_t s,
@@ -189,11 +190,11 @@ bool mla_window_fused_capable(const mla_plan& p);
 cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
                                     int B, int Q, void* out, MlaWindow win, cudaStream_t s);
 
-// The windowed decode's split attention for up to 32 heads (window_decode.cu).
+// The windowed decode for up to 32 heads: absorption, split attention and merge
+// (window_decode.cu; layout kernel id 5).
 bool mla_window_decode_capable(const mla_plan& p);
-cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, int B,
-                                     const Sched& sched, const void* qlat, const float* qrope, float* opart,
-                                     float* mlpart, int P, int G, MlaWindow win, cudaStream_t s);
+cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
+                                     int B, void* out, void* ws, const DecodeLayout& D, MlaWindow win, cudaStream_t s);
 
 cudaError_t mla_launch_select_pairs(const mla_config_t& cfg, const void* q, const void* k, int T,
                                     int32_t* pair_idx, float* contrib, cudaStream_t s);

@@ -130,6 +130,19 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// A place in a ring of `n` stages and the phase parity of its barriers there, advanced without
+// divisions (a remainder and a quotient per poll cost a role more than its work).
+struct RingPos {
+  int slot = 0;
+  uint32_t parity = 0;   // of a full barrier; an empty barrier's last phase has the other one
+  __device__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");

@@ -31,6 +31,7 @@
 
 #include "decode_common.cuh"
 #include "sm100.cuh"
+#include "warp_mma.cuh"
 
 namespace mla {
 namespace wdec {
@@ -41,18 +42,22 @@ constexpr int kUnit = 64;                 // tokens of a schedule tile and of a 
 constexpr int kT = 128;                   // tokens per product tile: two units
 constexpr uint32_t kHalf = kUnit * 128;   // bytes of a box: 64 rows x 128 B
 constexpr uint32_t kSlot = 2 * kHalf;     // ring slot: 128 tokens x 64 columns
-constexpr int kThreads = 384;
+// Threads: four warpgroups with a quantised latent (the last one dequantises), else three.
+template <int QB> constexpr int kThreadsOf = QB ? 512 : 384;
 constexpr float kTau = 8.0f;              // lazy-rescale threshold, log2 units
 constexpr uint32_t kCols = 256, kSCol = 0, kOCol = 64;   // S: 2 x 32 columns, O: 2 streams x 2 blocks x 32
 constexpr uint32_t kSmemMax = 232448;
 constexpr int kMaxC = 4, kMaxK = 8, kMaxRaw = 3;
+constexpr int kPieces = 64;               // pieces of a worker kept in shared memory
 
 struct Args {
   int H, G, d_c, dcp, R, P, T_cap;
   int n_cbox, n_kbox, kr_rows;            // boxes per token row; heads a key box is multiplied with
+  int kpb;                                // key boxes issued together
   int NC, NK, NRAW;                       // latent tiles, key boxes, code tiles in the rings
+  int B, workers;
   MlaWindow win;
-  Sched sched;
+  int4* pieces;                           // [P] by slot: the pieces past the first kPieces of a worker
   const int32_t* seq_lens;
   const float* qrope;                     // [B][H][8], rotated, scaled
   float* opart;                           // [P][H][d_c]
@@ -62,7 +67,7 @@ struct Args {
   mla_cache_t cache;
   int32_t* err;
   uint64_t wait_ns;
-  uint32_t off_q, off_qr, off_p, off_c, off_k, off_raw, raw_stage, off_red, off_bar;
+  uint32_t off_q, off_qr, off_p, off_c, off_k, off_raw, raw_stage, off_red, off_list, off_bar;
 };
 
 enum {
@@ -70,9 +75,10 @@ enum {
   kREmpty = kRFull + kMaxRaw, kSFull = kREmpty + kMaxRaw, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kODone = kPFull + 2,
   kOEmpty = kODone + 2, kQFull, kQEmpty, kMeet, kDone, kBars
 };
-// Exchange area, floats: per group the tile maxima of its warps [2][4][32]; by piece parity the
-// sums of all warps [2][2][4][32] and the groups' maxima [2][2][32].
-constexpr uint32_t kRedBytes = (2 * 4 * 32 + 2 * 2 * 4 * 32 + 2 * 2 * 32) * 4;
+// Exchange area, floats: per group the tile maxima of its warps [2][4][32] (first row also the
+// scores of a stream's first visible token); by piece parity the sums of all warps
+// [2][2][4][32] and the groups' maxima [2][2][32]; per group the merge weights [2][2][32].
+constexpr uint32_t kRedBytes = (2 * 4 * 32 + 2 * 2 * 4 * 32 + 2 * 2 * 32 + 2 * 2 * 32) * 4;
 
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -80,25 +86,30 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// Walk over a worker's pieces in tiles: x is the tile's first token in the sequence's span.
+// Walk over a worker's pieces in tiles: x is the tile's first token in the sequence's span.  A
+// piece is (sequence, first token, end, slot).
 struct Walk {
   const Args* a;
-  int pc, end, b, x, x0, x1;
+  const int4* list;   // the first kPieces pieces; the others at their slots, which are consecutive
+  int pc, end, slot, b, x, x0, x1;
   Span span;
-  __device__ void init(const Args* args, int w) {
+  __device__ void init(const Args* args, const int4* pieces, int n) {
     a = args;
-    pc = a->sched.worker_first[w];
-    end = a->sched.worker_first[w + 1];
+    list = pieces;
+    pc = 0;
+    end = n;
     if (pc < end) load();
   }
   __device__ void load() {
-    b = a->sched.piece_b[pc]; x0 = a->sched.piece_t0[pc]; x1 = a->sched.piece_t1[pc]; x = x0;
+    const int4 p = pc < kPieces ? list[pc] : a->pieces[list[0].w + pc];
+    b = p.x; x0 = p.y; x1 = p.z; slot = p.w; x = x0;
     span = unit_span(__ldg(a->seq_lens + b), 1, kUnit, a->win);
   }
   __device__ bool valid() const { return pc < end; }
   __device__ bool first() const { return x == x0; }
   __device__ bool last() const { return x + kT >= x1; }
   __device__ int rows() const { return min(kT, x1 - x); }
+  __device__ int seq_len() const { return __ldg(a->seq_lens + b); }
   __device__ int units() const { return x1 - x > kUnit ? 2 : 1; }
   __device__ int token(int unit) const { return span.token(x + unit * kUnit); }
   // Every row of the tile holds a visible token.
@@ -151,9 +162,54 @@ template <int N> __device__ __forceinline__ void tmem_ld(uint32_t ta, uint32_t (
 template <> __device__ __forceinline__ void tmem_ld<16>(uint32_t ta, uint32_t (&v)[16]) { tmem_ld16(ta, v); }
 template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t ta, uint32_t (&v)[32]) { tmem_ld32(ta, v); }
 
+// The worker's pieces: list[0 .. min(n, kPieces)), the others in the workspace; returns n.  Whole
+// CTA.  Reads the lengths, which were complete before the kernel ahead of this one started.
+__device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, int* s_warp, int* s_misc) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  if (tid == 0) { s_misc[0] = INT_MAX; s_misc[1] = 0; }
+  int total = 0;
+  SeqUnits mine;
+  int my_ex = 0;
+  for (int base = 0; base < a.B; base += nt) {
+    mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+    int tot;
+    my_ex = block_exscan(mine.n, &tot, s_warp);
+    total += tot;
+  }
+  const int busy = busy_workers(total, a.workers);
+  if (w >= busy) return 0;
+  const int w0 = (int)worker_begin(w, total, busy), w1 = (int)worker_begin(w + 1, total, busy);
+  int c_carry = 0, ne_carry = 0;
+  for (int base = 0; base < a.B; base += nt) {
+    if (a.B > nt) {   // more sequences than threads: their units once more
+      mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+      int tot;
+      my_ex = block_exscan(mine.n, &tot, s_warp);
+      my_ex += c_carry;
+      c_carry += tot;
+    }
+    int tot_ne;
+    const int ne = ne_carry + block_exscan(mine.n > 0 ? 1 : 0, &tot_ne, s_warp);
+    ne_carry += tot_ne;
+    const int first = my_ex + kSeqCost;   // where the sequence's own units begin
+    const bool in = mine.n > 0 && first < w1 && my_ex + mine.n > w0;
+    if (in) atomicMin(s_misc, ne);   // the worker's first sequence
+    __syncthreads();
+    if (in) {
+      const int k = ne - s_misc[0];
+      const int4 p = make_int4(base + tid, max(0, w0 - first) * kUnit, min(mine.len, (w1 - first) * kUnit), w + ne);
+      if (k < kPieces) list[k] = p;
+      else a.pieces[p.w] = p;
+      atomicMax(s_misc + 1, k + 1);
+    }
+  }
+  __syncthreads();
+  return s_misc[1];
+}
+
 // N: heads padded to 16 or 32; QB: code width of a quantised latent (4 or 2), 0 for bf16.
 template <int N, int QB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<QB>, 1)
 window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
                      const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -173,8 +229,8 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
       int n = 1;
-      if (i >= kCFull && i < kCEmpty && QB) n = 2;      // both dequantising warps
-      if (i >= kREmpty && i < kSFull) n = 2;
+      if (i >= kCFull && i < kCEmpty && QB) n = 4;      // the dequantising warps
+      if (i >= kREmpty && i < kSFull) n = 4;
       if (i >= kSEmpty && i < kODone) n = 4;            // a softmax group's warps (S read, P written)
       if (i == kOEmpty || i == kMeet) n = 8;            // both groups
       if (i == kQFull) n = 2;                           // Q_lat bytes, the RoPE rows
@@ -183,7 +239,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     fence_mbar_init();
   }
   // query rows past the last head and the zero blocks of the RoPE operand stay zero
-  for (uint32_t i = threadIdx.x; i < (a.off_p - a.off_q) / 16; i += kThreads)
+  for (uint32_t i = threadIdx.x; i < (a.off_p - a.off_q) / 16; i += kThreadsOf<QB>)
     reinterpret_cast<uint4*>(smem + a.off_q)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 0 && lane == 0) {
@@ -200,85 +256,125 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const uint32_t c_bytes = (uint32_t)a.n_cbox * kSlot;
-  pdl_wait();   // schedule, absorbed queries and the cache come from earlier kernels
-  pdl_trigger();
-  const int w = blockIdx.x;
-
+  // The kernel ahead is this call's absorption, which started once everything before it was
+  // done: lengths and cache can be read now, only the absorbed queries must be waited for.
+  __shared__ int s_warp[32], s_misc[2];
+  int4* list = reinterpret_cast<int4*>(smem + a.off_list);
+  const int n_pieces = worker_pieces(a, blockIdx.x, list, s_warp, s_misc);
+  // Registers with a quantised latent: 512 threads x 128 = 65536 = 128 x (88 + 168 + 168 + 88).
+  if (warp < 4) {
+  if (QB) setmaxnreg_dec<88>();
   if (warp == 0) {
-    // ============================================================ TMA producer (lane 0)
-    if (lane == 0) {
-      // cursors: latent (or code) tiles with the queries, and key boxes, whose slots free up at
-      // different times
-      Walk wc, wk;
-      wc.init(&a, w);
-      wk = wc;
-      int nc = 0, nk = 0, kb = 0, tk = 0, u = 0;
-      int looks = 0;
-      uint64_t idle = 0;
-      auto row_of = [&](const Walk& it, int unit) {
-        const MlaLoc lc = mla_loc(a.cache, it.b, it.token(unit), a.err);   // a unit lies in one block
-        return lc.pb * lc.cap + lc.pt;
-      };
-      while (wc.valid() || wk.valid()) {
-        bool progress = false;
-        if (wc.valid()) {
-          const int s = QB ? nc % NRAW : nc % NC, ring = QB ? NRAW : NC;
-          const bool q_ok = !wc.first() || u == 0 || mbar_test(bar(kQEmpty), (u - 1) & 1);
-          if (q_ok && (nc < ring || mbar_test(bar((QB ? kREmpty : kCEmpty) + s), ((nc / ring) - 1) & 1))) {
-            if (wc.first()) {
-              mbar_expect_tx(bar(kQFull), (uint32_t)a.n_cbox * a.H * 128u);
-              for (int k = 0; k < a.n_cbox; ++k)
-                tma_load_2d(sb + a.off_q + k * N * 128, &tm_q, bar(kQFull), k * 64, wc.b * a.H);
-              ++u;
-            }
-            const int units = wc.units();
-            if (QB) mbar_expect_tx(bar(kRFull + s), (uint32_t)units * kUnit * a.code_row);
-            else mbar_expect_tx(bar(kCFull + s), (uint32_t)units * a.n_cbox * kHalf);
-            for (int j = 0; j < units; ++j) {
-              const int row = row_of(wc, j);
-              if (QB) {
-                tma_load_2d(sb + a.off_raw + s * a.raw_stage + j * kUnit * a.code_row, &tm_c, bar(kRFull + s), 0, row);
-              } else {
-                for (int k = 0; k < a.n_cbox; ++k)
-                  tma_load_2d(sb + a.off_c + s * c_bytes + k * kSlot + j * kHalf, &tm_c, bar(kCFull + s), k * 64, row);
+    // ============================================================ TMA producer (converged warp, elected lane)
+    // Cursors: latent (or code) tiles, key boxes, queries, whose places free up at different
+    // times; the queries of the first piece wait for the absorption.  The cache rows of a
+    // tile's units are looked up when the cursor reaches it, not when its place is free.
+    auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
+    auto row_of = [&](const Walk& it, int unit) {
+      const MlaLoc lc = mla_loc(a.cache, it.b, it.token(unit), a.err);   // a unit lies in one block
+      return lc.pb * lc.cap + lc.pt;
+    };
+    Walk wc, wk, wq;
+    wc.init(&a, list, n_pieces);
+    wk = wc;
+    wq = wc;
+    int c_row[2] = {0, 0}, k_row[2] = {0, 0};
+    auto rows_at = [&](const Walk& it, int (&row)[2]) {
+      row[0] = row_of(it, 0);
+      row[1] = it.units() > 1 ? row_of(it, 1) : row[0];
+    };
+    if (wc.valid()) rows_at(wc, c_row);
+    k_row[0] = c_row[0]; k_row[1] = c_row[1];
+    int nc = 0, nk = 0, kb = 0, tk = 0, u = 0;   // u: query loads issued
+    RingPos rc, rk;
+    const int c_ring = QB ? NRAW : NC;
+    int looks = 0;
+    uint64_t idle = 0;
+    auto load_q = [&]() {
+      if (elect_one()) {
+        mbar_expect_tx(bar(kQFull), (uint32_t)a.n_cbox * a.H * 128u);
+        for (int k = 0; k < a.n_cbox; ++k) tma_load_2d(sb + a.off_q + k * N * 128, &tm_q, bar(kQFull), k * 64, wq.b * a.H);
+      }
+      __syncwarp();
+      ++u;
+      if (++wq.pc < wq.end) wq.load();
+    };
+    bool ok = true;
+    while (ok && (wc.valid() || wk.valid() || wq.valid())) {
+      bool progress = false;
+      if (wc.valid()) {
+        const int s = rc.slot;
+        if (nc < c_ring || ready((QB ? kREmpty : kCEmpty) + s, rc.parity ^ 1)) {
+          const int units = wc.units();
+          if (elect_one()) {
+            if (QB) {
+              const uint32_t dst = sb + a.off_raw + s * a.raw_stage;
+              mbar_expect_tx(bar(kRFull + s), (uint32_t)units * kUnit * a.code_row);
+              tma_load_2d(dst, &tm_c, bar(kRFull + s), 0, c_row[0]);
+              if (units > 1) tma_load_2d(dst + kUnit * a.code_row, &tm_c, bar(kRFull + s), 0, c_row[1]);
+            } else {
+              const uint32_t dst = sb + a.off_c + s * c_bytes;
+              mbar_expect_tx(bar(kCFull + s), (uint32_t)units * a.n_cbox * kHalf);
+              for (int k = 0; k < a.n_cbox; ++k) {
+                tma_load_2d(dst + k * kSlot, &tm_c, bar(kCFull + s), k * 64, c_row[0]);
+                if (units > 1) tma_load_2d(dst + k * kSlot + kHalf, &tm_c, bar(kCFull + s), k * 64, c_row[1]);
               }
             }
-            wc.next();
-            ++nc;
-            progress = true;
           }
-        }
-        if (wk.valid() && tk < nc) {   // keys never run ahead of their tile's latent copy
-          const int s = nk % NK;
-          if (nk < NK || mbar_test(bar(kKEmpty + s), ((nk / NK) - 1) & 1)) {
-            const int units = wk.units();
-            mbar_expect_tx(bar(kKFull + s), (uint32_t)units * kHalf);
-            for (int j = 0; j < units; ++j)
-              tma_load_2d(sb + a.off_k + s * kSlot + j * kHalf, &tm_kr, bar(kKFull + s), kb * 64, row_of(wk, j));
-            ++nk;
-            if (++kb == a.n_kbox) { kb = 0; ++tk; wk.next(); }
-            progress = true;
-          }
-        }
-        if (progress) {
-          looks = 0;
-        } else if ((++looks & 63) == 0) {
-          const uint64_t now = globaltimer();
-          if (looks == 64) idle = now;
-          if (*abort_flag || now - idle > lim) { *abort_flag = 1; break; }
+          __syncwarp();
+          wc.next();
+          rc.next(c_ring);
+          ++nc;
+          if (wc.valid()) rows_at(wc, c_row);
+          progress = true;
         }
       }
-      // every issued copy lands before the CTA exits
-      volatile int never = 0;
-      auto drain = [&](int first, int ring, int issued) {
-        for (int i = max(0, issued - ring); i < issued; ++i) mbar_spin(bar(first + i % ring), (i / ring) & 1, &never, lim);
-      };
-      drain(QB ? kRFull : kCFull, QB ? NRAW : NC, nc);
-      drain(kKFull, NK, nk);
-      if (*abort_flag && u > 0) {   // the queries' copy (its barrier may still miss the RoPE rows: wait a moment instead)
-        const uint64_t t0 = globaltimer();
-        while (!mbar_test(bar(kQFull), (u - 1) & 1) && globaltimer() - t0 < 1000000ull) {}
+      while (wk.valid() && tk < nc) {   // keys never run ahead of their tile's latent copy
+        const int s = rk.slot;
+        if (!(nk < NK || ready(kKEmpty + s, rk.parity ^ 1))) break;
+        const int units = wk.units();
+        if (elect_one()) {
+          mbar_expect_tx(bar(kKFull + s), (uint32_t)units * kHalf);
+          tma_load_2d(sb + a.off_k + s * kSlot, &tm_kr, bar(kKFull + s), kb * 64, k_row[0]);
+          if (units > 1) tma_load_2d(sb + a.off_k + s * kSlot + kHalf, &tm_kr, bar(kKFull + s), kb * 64, k_row[1]);
+        }
+        __syncwarp();
+        rk.next(NK);
+        ++nk;
+        if (++kb == a.n_kbox) {
+          kb = 0;
+          ++tk;
+          wk.next();
+          if (wk.valid()) rows_at(wk, k_row);
+        }
+        progress = true;
       }
+      if (wq.valid() && u > 0 && ready(kQEmpty, (u - 1) & 1)) {
+        load_q();
+        progress = true;
+      }
+      if (progress) {
+        looks = 0;
+      } else if (u == 0) {   // the rings are full
+        pdl_wait();
+        load_q();
+      } else if ((++looks & 63) == 0) {
+        const uint64_t now = globaltimer();
+        if (looks == 64) idle = now;
+        if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+        ok = __all_sync(0xffffffffu, ok) != 0;
+      }
+    }
+    // every issued copy lands before the CTA exits
+    volatile int never = 0;
+    auto drain = [&](int first, int ring, int issued) {
+      for (int i = max(0, issued - ring); i < issued; ++i) mbar_spin(bar(first + i % ring), (i / ring) & 1, &never, lim);
+    };
+    drain(QB ? kRFull : kCFull, QB ? NRAW : NC, nc);
+    drain(kKFull, NK, nk);
+    if (*abort_flag && u > 0) {   // the queries' copy (its barrier may still miss the RoPE rows: wait a moment instead)
+      const uint64_t t0 = globaltimer();
+      while (!mbar_test(bar(kQFull), (u - 1) & 1) && globaltimer() - t0 < 1000000ull) {}
     }
   } else if (warp == 1) {
     // ============================================================ MMA issuer (converged warp, elected lane)
@@ -289,59 +385,68 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
     const int n_blk = (a.dcp + 127) / 128;   // blocks of 128 latent columns
     Walk i1, i2;                             // tiles whose S, and whose O, is issued next
-    i1.init(&a, w);
+    i1.init(&a, list, n_pieces);
     i2 = i1;
-    int n1 = 0, j1 = 0, nk = 0, n2 = 0, u1 = 0, u2 = 0;   // j1: parts of S(n1) issued (latent, then key boxes)
+    // S(n1) is issued in batches, the latent product with the first kpb key boxes, then kpb key
+    // boxes at a time (all of them in one batch where the ring holds them): a batch costs about
+    // 200 cycles before its first product starts
+    int n1 = 0, kb1 = 0, n2 = 0, u1 = 0, u2 = 0;   // kb1: key boxes of S(n1) issued
+    RingPos r1, r2, rk;                            // latent tiles of S and of O, key boxes
     bool ok = true;
     int looks = 0;
     uint64_t idle = 0;
     while (ok && i2.valid()) {
       bool progress = false;
       if (i1.valid()) {
-        const int s = n1 & 1;
-        if (j1 == 0) {
-          if ((n1 < 2 || ready(kSEmpty + s, ((n1 >> 1) - 1) & 1)) && (!i1.first() || ready(kQFull, u1 & 1)) &&
-              ready(kCFull + n1 % NC, (n1 / NC) & 1)) {
-            tc_fence_after();
-            if (elect_one()) {
-              uint64_t da = smem_desc(sb + a.off_c + (n1 % NC) * c_bytes, 16, 1024, kLayoutSW128), db = desc_q;
-              const uint32_t d = tmem + kSCol + s * 32;
+        const int s = n1 & 1, take = min(a.kpb, a.n_kbox - kb1);
+        bool go = kb1 > 0 || ((n1 < 2 || ready(kSEmpty + s, ((n1 >> 1) - 1) & 1)) &&
+                              ready(kCFull + r1.slot, r1.parity) && (!i1.first() || ready(kQFull, u1 & 1)));
+        RingPos rt = rk;
+        for (int k = 0; go && k < take; ++k) {
+          go = ready(kKFull + rt.slot, rt.parity);
+          rt.next(NK);
+        }
+        if (go) {
+          tc_fence_after();
+          const bool done = kb1 + take == a.n_kbox;
+          if (elect_one()) {
+            const uint32_t d0 = tmem + kSCol + s * 32;
+            if (kb1 == 0) {
+              uint64_t da = smem_desc(sb + a.off_c + r1.slot * c_bytes, 16, 1024, kLayoutSW128), db = desc_q;
               for (int k = 0; k < a.n_cbox; ++k) {   // a box of 64 columns is four steps
-                tc_mma_bf16(d, da, db, id_s, k > 0);
-                tc_mma_bf16(d, da + 2, db + 2, id_s, 1);
-                tc_mma_bf16(d, da + 4, db + 4, id_s, 1);
-                tc_mma_bf16(d, da + 6, db + 6, id_s, 1);
+                tc_mma_bf16(d0, da, db, id_s, k > 0);
+                tc_mma_bf16(d0, da + 2, db + 2, id_s, 1);
+                tc_mma_bf16(d0, da + 4, db + 4, id_s, 1);
+                tc_mma_bf16(d0, da + 6, db + 6, id_s, 1);
                 da += kSlot >> 4;
                 db += (N * 128) >> 4;
               }
             }
-            __syncwarp();
-            j1 = 1;
-            progress = true;
-          }
-        } else if (ready(kKFull + nk % NK, (nk / NK) & 1)) {
-          tc_fence_after();
-          const int kb = j1 - 1;
-          const bool done = j1 == a.n_kbox;
-          if (elect_one()) {
-            // KV heads 8 kb .. 8 kb + 7: query heads from col on
-            const int col = a.kr_rows == N ? 0 : (kb * 8 * a.G) & ~15;
-            const uint32_t d = tmem + kSCol + s * 32 + col;
-            const uint64_t da = smem_desc(sb + a.off_k + (nk % NK) * kSlot, 16, 1024, kLayoutSW128);
-            const uint64_t db = desc_qr + (uint32_t)kb * (a.kr_rows * 128u >> 4);
-            const int steps = min(4, (a.R - kb * 64 + 15) / 16);
-            for (int k = 0; k < steps; ++k) tc_mma_bf16(d, da + 2 * k, db + 2 * k, id_k, 1);
-            tc_commit(bar(kKEmpty + nk % NK));
+            for (int j = 0; j < take; ++j) {
+              // KV heads 8 kb .. 8 kb + 7: query heads from col on
+              const int kb = kb1 + j, slot = rk.slot;
+              const uint32_t d = d0 + (a.kr_rows == N ? 0 : (kb * 8 * a.G) & ~15);
+              const uint64_t da = smem_desc(sb + a.off_k + slot * kSlot, 16, 1024, kLayoutSW128);
+              const uint64_t db = desc_qr + (uint32_t)kb * (a.kr_rows * 128u >> 4);
+              const int steps = min(4, (a.R - kb * 64 + 15) / 16);
+              tc_mma_bf16(d, da, db, id_k, 1);
+              if (steps > 1) tc_mma_bf16(d, da + 2, db + 2, id_k, 1);
+              if (steps > 2) tc_mma_bf16(d, da + 4, db + 4, id_k, 1);
+              if (steps > 3) tc_mma_bf16(d, da + 6, db + 6, id_k, 1);
+              tc_commit(bar(kKEmpty + slot));
+              rk.next(NK);
+            }
             if (done) {
               tc_commit(bar(kSFull + s));
               if (i1.last()) tc_commit(bar(kQEmpty));
             }
           }
           __syncwarp();
-          ++nk;
-          ++j1;
+          rk = rt;
+          kb1 += take;
           if (done) {
-            j1 = 0;
+            kb1 = 0;
+            r1.next(NC);
             if (i1.last()) ++u1;
             i1.next();
             ++n1;
@@ -357,18 +462,27 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           const int s = n2 & 1;
           if (elect_one()) {
             const uint64_t dp = smem_desc(sb + a.off_p + s * kPBytes, 16, 8 * kPRow, kPLayout);
-            const uint64_t dc = smem_desc(sb + a.off_c + (n2 % NC) * c_bytes, kSlot, 1024, kLayoutSW128);
+            const uint64_t dc = smem_desc(sb + a.off_c + r2.slot * c_bytes, kSlot, 1024, kLayoutSW128);
             const int steps = (i2.rows() + 15) / 16;
-            for (int m = 0; m < n_blk; ++m)
-              for (int k = 0; k < steps; ++k)
-                tc_mma_bf16(tmem + kOCol + s * 64 + m * 32, dc + (uint32_t)m * (2 * kSlot >> 4) + 128u * k,
-                            dp + (uint32_t)k * (16 * kPRow >> 4), id_o, !fresh || k > 0);
-            tc_commit(bar(kCEmpty + n2 % NC));
+            for (int m = 0; m < n_blk; ++m) {
+              const uint32_t d = tmem + kOCol + s * 64 + m * 32;
+              const uint64_t dm = dc + (uint32_t)m * (2 * kSlot >> 4);
+              if (steps == kT / 16) {
+                tc_mma_bf16(d, dm, dp, id_o, !fresh);
+#pragma unroll
+                for (int k = 1; k < kT / 16; ++k) tc_mma_bf16(d, dm + 128 * k, dp + k * (16 * kPRow >> 4), id_o, 1);
+              } else {
+                for (int k = 0; k < steps; ++k)
+                  tc_mma_bf16(d, dm + 128u * k, dp + (uint32_t)k * (16 * kPRow >> 4), id_o, !fresh || k > 0);
+              }
+            }
+            tc_commit(bar(kCEmpty + r2.slot));
             tc_commit(bar(kODone + s));
           }
           __syncwarp();
           if (i2.last()) ++u2;
           i2.next();
+          r2.next(NC);
           ++n2;
           progress = true;
         }
@@ -386,115 +500,131 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     __syncwarp();
     volatile int never = 0;
     mbar_spin(bar(kDone), 0, &never, lim);
-  } else if (warp < 4) {
-    // ============================================================ dequantisation (two token rows per thread)
-    if (QB != 0) {
-      const int t = (warp - 2) * 32 + lane;   // rows t and t + 64 of each tile
-      Walk it;
-      it.init(&a, w);
-      bool ok = true;
-      for (int n = 0; ok && it.valid(); ++n, it.next()) {
-        const int rs = n % NRAW, cs = n % NC;
-        const int L = __ldg(a.seq_lens + it.b);
-        // where the rows' scales (and ring rows) come from, asked for ahead of the waits
-        const __half* sp[2];
-        bool live[2], ring[2];
-        size_t slot[2];
+  }   // (warps 2 and 3 idle)
+  } else if (QB != 0 && warp >= 12) {
+    // ============================================================ dequantisation (a token row per thread)
+    if (QB) setmaxnreg_dec<88>();
+    const int r = (warp - 12) * 32 + lane;
+    Walk it;
+    it.init(&a, list, n_pieces);
+    // Where a row's values come from is asked for ahead of its tile, so that no load is waited
+    // for in the loop: the cache row (a look into the block table) two tiles, the group scales
+    // and the ring tag a tile ahead.
+    struct Src {
+      bool live = false;
+      int tag = -1, pos = 0;            // ring: the position its slot holds, the token's own
+      size_t slot = 0;
+      unsigned short sc[8];             // fp16 scales
+    };
+    Walk w1 = it, w2 = it;              // one and two tiles ahead
+    auto cache_row = [&](const Walk& t) -> long long {
+      if (!t.valid() || !t.visible(r)) return -1;
+      const MlaLoc lc = mla_loc(a.cache, t.b, t.token(r >> 6), a.err);
+      return (long long)lc.pb * lc.cap + lc.pt + (r & 63);
+    };
+    auto source = [&](const Walk& t, long long row, Src& o) {
+      o.live = row >= 0;
+      o.tag = -1;
+      if (!o.live) return;
+      const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.scales) + (size_t)row * (a.d_c / 32);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = t + 64 * j;
-          live[j] = it.visible(r);
-          ring[j] = false;
-          sp[j] = a.scales;
-          slot[j] = 0;
-          if (live[j]) {
-            const int tp = it.token(j) + t;
-            const MlaLoc lc = mla_loc(a.cache, it.b, it.token(j), a.err);
-            sp[j] = a.scales + ((size_t)lc.pb * lc.cap + lc.pt + t) * (a.d_c / 32);
-            if (a.cache.c_resid && tp >= L - MLA_RESID_WINDOW) {
-              slot[j] = (size_t)it.b * MLA_RESID_WINDOW + (tp & (MLA_RESID_WINDOW - 1));
-              ring[j] = __ldg(a.cache.resid_pos + slot[j]) == tp;
-            }
-          }
-        }
-        __half sc[2][8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sc[j][k] = k < a.d_c / 32 && live[j] ? __ldg(sp[j] + k) : __float2half(0.f);
-        ok = __all_sync(0xffffffffu, mbar_spin(bar(kRFull + rs), (n / NRAW) & 1, abort_flag, lim));
-        if (ok && n >= NC) ok = __all_sync(0xffffffffu, mbar_spin(bar(kCEmpty + cs), ((n / NC) - 1) & 1, abort_flag, lim));
-        if (!ok) break;
-        uint8_t* C = smem + a.off_c + cs * c_bytes;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = t + 64 * j;
-          auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4*>(C + (chunk >> 3) * kSlot + sw128(r, chunk)) = v; };
-          if (ring[j]) {   // one of the window's unquantised tokens
-            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) + slot[j] * a.d_c);
-            for (int c = 0; c < a.d_c / 8; ++c) put(c, __ldg(src + c));
-          } else if (live[j]) {
-            const uint8_t* codes = smem + a.off_raw + rs * a.raw_stage + r * a.code_row;
-#pragma unroll 1
-            for (int g = 0; g < a.d_c / 32; ++g) {
-              __half hs = sc[j][0];
-#pragma unroll
-              for (int k = 1; k < 8; ++k) hs = g == k ? sc[j][k] : hs;
-              const float sv = __half2float(hs);
-              uint32_t wd[4];
-              if (QB == 4) {
-                const uint4 cw = *reinterpret_cast<const uint4*>(codes + g * 16);
-                wd[0] = cw.x; wd[1] = cw.y; wd[2] = cw.z; wd[3] = cw.w;
-              } else {
-                const uint2 cw = *reinterpret_cast<const uint2*>(codes + g * 8);
-                wd[0] = cw.x; wd[1] = cw.x >> 16; wd[2] = cw.y; wd[3] = cw.y >> 16;
-              }
-#pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                // offset codes in the mantissa of 2^23: the float exceeds the base by the code;
-                // code x scale is rounded to bf16, the products' operand type
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t f = wd[ch] >> (2 * QB * e);
-                  constexpr uint32_t top = 1u << (QB ? QB - 1 : 0), mask = 2 * top - 1;
-                  const float base = 8388608.0f + (float)top;
-                  const float lo = __uint_as_float(0x4B000000u | ((f ^ top) & mask)) - base;
-                  const float hi = __uint_as_float(0x4B000000u | (((f >> QB) ^ top) & mask)) - base;
-                  o[e] = pack2(lo * sv, hi * sv);
-                }
-                put(4 * g + ch, make_uint4(o[0], o[1], o[2], o[3]));
-              }
-            }
-          } else {
-            for (int c = 0; c < a.d_c / 8; ++c) put(c, make_uint4(0, 0, 0, 0));
-          }
-          for (int c = a.d_c / 8; c < a.dcp / 8; ++c) put(c, make_uint4(0, 0, 0, 0));   // padding columns
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(kREmpty + rs));
-          mbar_arrive(bar(kCFull + cs));
+      for (int k = 0; k < 8; ++k)
+        if (k < a.d_c / 32) o.sc[k] = __ldg(sp + k);
+      if (a.cache.c_resid) {
+        o.pos = t.token(r >> 6) + (r & 63);
+        if (o.pos >= t.seq_len() - MLA_RESID_WINDOW) {
+          o.slot = (size_t)t.b * MLA_RESID_WINDOW + (o.pos & (MLA_RESID_WINDOW - 1));
+          o.tag = __ldg(a.cache.resid_pos + o.slot);
         }
       }
+    };
+    Src cur, nxt;
+    source(it, cache_row(it), cur);
+    if (w1.valid()) w1.next();
+    long long row1 = cache_row(w1);
+    w2 = w1;
+    bool ok = true;
+    RingPos rr, rc;   // code tiles, latent tiles
+    for (int n = 0; ok && it.valid(); ++n, it.next(), rr.next(NRAW), rc.next(NC)) {
+      const int rs = rr.slot, cs = rc.slot;
+      source(w1, row1, nxt);
+      if (w2.valid()) w2.next();
+      const long long row2 = cache_row(w2);
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kRFull + rs), rr.parity, abort_flag, lim));
+      if (ok && n >= NC) ok = __all_sync(0xffffffffu, mbar_wait(bar(kCEmpty + cs), rc.parity ^ 1, abort_flag, lim));
+      if (!ok) break;
+      uint8_t* C = smem + a.off_c + cs * c_bytes;
+      auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4*>(C + (chunk >> 3) * kSlot + sw128(r, chunk)) = v; };
+      if (cur.live && cur.tag >= 0 && cur.tag == cur.pos) {   // one of the window's unquantised tokens
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) + cur.slot * a.d_c);
+        for (int c = 0; c < a.d_c / 8; ++c) put(c, __ldg(src + c));
+      } else if (cur.live) {
+        const uint8_t* codes = smem + a.off_raw + rs * a.raw_stage + r * a.code_row;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          if (g >= a.d_c / 32) break;
+          // An offset code u = code + top sits in the mantissa of 1.0 from bit 23 - QB on: the
+          // float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at
+          // most QB + 11 bits), rounded once to bf16, the products' operand type.
+          constexpr uint32_t kTop = 1u << (QB ? QB - 1 : 0), kMask = (2 * kTop - 1) << (23 - QB);
+          constexpr uint32_t kOne = 0x3F800000u ^ (kTop << (23 - QB));
+          const float sv = __half2float(__ushort_as_half(cur.sc[g]));
+          const float mul = sv * (float)(2 * kTop), add = -sv * (float)(3 * kTop);
+          uint32_t wd[4];
+          if (QB == 4) {
+            const uint4 cw = *reinterpret_cast<const uint4*>(codes + g * 16);
+            wd[0] = cw.x; wd[1] = cw.y; wd[2] = cw.z; wd[3] = cw.w;
+          } else {
+            const uint2 cw = *reinterpret_cast<const uint2*>(codes + g * 8);
+            wd[0] = cw.x; wd[1] = cw.x >> 16; wd[2] = cw.y; wd[3] = cw.y >> 16;
+          }
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int sh = 23 - QB - QB * e;
+              const uint32_t at = sh >= 0 ? wd[ch] << (sh & 31) : wd[ch] >> (-sh & 31);
+              f[e] = fmaf(__uint_as_float((at & kMask) ^ kOne), mul, add);
+            }
+            put(4 * g + ch, make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
+          }
+        }
+      } else {
+        for (int c = 0; c < a.d_c / 8; ++c) put(c, make_uint4(0, 0, 0, 0));
+      }
+      for (int c = a.d_c / 8; c < a.dcp / 8; ++c) put(c, make_uint4(0, 0, 0, 0));   // padding columns
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kREmpty + rs));
+        mbar_arrive(bar(kCFull + cs));
+      }
+      cur = nxt;
+      w1 = w2;
+      row1 = row2;
     }
   } else {
     // ============================================================ softmax groups
+    if (QB) setmaxnreg_inc<168>();
     const int s = warp >= 8;                 // stream
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lane0 = tmem + ((uint32_t)(32 * q) << 16);
     float* red = reinterpret_cast<float*>(smem + a.off_red) + s * 4 * 32;
     float* sums = reinterpret_cast<float*>(smem + a.off_red) + 2 * 4 * 32;   // [parity][stream][warp][32]
     float* tops = sums + 2 * 2 * 4 * 32;                                     // [parity][stream][32]
-    auto warp_wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)) != 0; };
+    float* wts = tops + 2 * 2 * 32 + s * 2 * 32;                             // merge weights [stream][32]
+    pdl_wait();   // the RoPE queries, and the partials this kernel writes
+    pdl_trigger();
+    auto warp_wait = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, lim)) != 0; };
     auto arrive = [&](int i) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(i));
     };
     Walk it;
-    it.init(&a, w);
+    it.init(&a, list, n_pieces);
     int n = 0, u = 0;                        // tiles and pieces of the CTA
+    RingPos rc;                              // latent tiles
     float m[N], l[N];
     bool some = false;                       // this stream had a tile in the piece
     bool fail = false;
@@ -536,7 +666,22 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         }
         tc_fence_before();
         arrive(kSEmpty + s);
-        bool raise = !some;
+        if (!some) {
+          // the stream starts from the scores of its first visible token plus kTau: a raise (a
+          // reduction over the tile, microseconds with its code cold) is then needed only for
+          // scores 2 kTau above that token's, and the sums stay as exact with a maximum that is
+          // up to kTau too high
+          const int t0 = it.token(0);
+          const int first = t0 >= it.span.lo || t0 < a.win.n_sink ? 0 : it.span.lo - t0;
+          if (r == first) {
+#pragma unroll
+            for (int h = 0; h < N; ++h) red[h] = x[h];
+          }
+          (void)group_or(1 + s, false);
+#pragma unroll
+          for (int h = 0; h < N; ++h) m[h] = red[h] + kTau;
+        }
+        bool raise = false;
 #pragma unroll
         for (int h = 0; h < N; ++h) raise |= x[h] > m[h] + kTau;
         // P's buffer and the accumulator are free once the stream's previous tile is in O
@@ -553,10 +698,10 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
 #pragma unroll
           for (int h = 0; h < N; ++h) {
             const float t = fmaxf(fmaxf(red[h], red[32 + h]), fmaxf(red[64 + h], red[96 + h]));
-            const bool up = t > m[h] + (some ? kTau : 0.f) || !some;
-            al[h] = up ? exp2f(m[h] - t) : 1.f;   // m = -inf: 0
+            const bool up = t > m[h] + kTau;
+            al[h] = up ? ex2_approx(m[h] - t) : 1.f;   // m = -inf: 0
             m[h] = up ? t : m[h];
-            l[h] = some ? l[h] * al[h] : 0.f;
+            l[h] *= al[h];
           }
           if (some) {
             for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk) {
@@ -593,7 +738,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         if (!QB && !it.whole()) {
           // rows without a visible token (stale or hidden, possibly not finite) are zeroed
           // before O's product multiplies them by P = 0; S of this tile has been read
-          uint8_t* C = smem + a.off_c + (n % NC) * c_bytes;
+          uint8_t* C = smem + a.off_c + rc.slot * c_bytes;
           auto zero_rows = [&](int from, int to) {   // consecutive threads, consecutive 16-byte chunks
             for (int i = from * 8 + r; i < to * 8; i += 128)
               for (int b = 0; b < a.n_cbox; ++b) *reinterpret_cast<uint4*>(C + b * kSlot + i * 16) = make_uint4(0, 0, 0, 0);
@@ -627,12 +772,17 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         const int done0 = (n + 2) >> 1, done1 = (n + 1) >> 1;   // tiles of each stream so far
         arrive(kMeet);
         if (!fail) fail = !warp_wait(kMeet, u & 1);
+        const float* t0 = tops + par * 2 * 32;
+        if (r < N) {   // a stream without a tile in this piece weighs nothing
+          const float m0 = t0[r], m1 = t0[32 + r], M = fmaxf(m0, m1);
+          wts[r] = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M);
+          wts[32 + r] = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
+        }
         if (!fail && done0 > 0) fail = !warp_wait(kODone, (done0 - 1) & 1);
         if (!fail && done1 > 0) fail = !warp_wait(kODone + 1, (done1 - 1) & 1);
         if (group_or(1 + s, fail)) break;
         tc_fence_after();
         // this group writes heads [N/2 s, N/2 s + N/2): lane = latent column
-        const float* t0 = tops + par * 2 * 32;
         const float* l0 = sums + par * 2 * 4 * 32;
         constexpr int HN = N / 2;
         for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk) {
@@ -646,31 +796,28 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
             for (int e = 0; e < 8; ++e) {
               asm volatile("" : "+r"(o0[e]), "+r"(o1[e]));
               const int h = HN * s + h0 + e;
-              const float m0 = t0[h], m1 = t0[32 + h], M = fmaxf(m0, m1);
-              // a stream without a tile in this piece holds nothing (its columns are stale)
-              const float v0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M) * __uint_as_float(o0[e]);
-              const float v1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M) * __uint_as_float(o1[e]);
-              if (h < a.H && c < a.d_c) a.opart[((size_t)it.pc * a.H + h) * a.d_c + c] = v0 + v1;
+              const float w0 = wts[h], w1 = wts[32 + h];   // weight 0: the columns may be stale
+              const float v = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
+              if (h < a.H && c < a.d_c) a.opart[((size_t)it.slot * a.H + h) * a.d_c + c] = v;
             }
           }
         }
         if (s == 0 && r < a.H) {
-          const float m0 = t0[r], m1 = t0[32 + r], M = fmaxf(m0, m1);
+          const float M = fmaxf(t0[r], t0[32 + r]);
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             sum0 += l0[k * 32 + r];
             sum1 += l0[(4 + k) * 32 + r];
           }
-          a.mlpart[((size_t)r * a.P + it.pc) * 2] = M;
-          a.mlpart[((size_t)r * a.P + it.pc) * 2 + 1] =
-              (m0 == -INFINITY ? 0.f : exp2f(m0 - M) * sum0) + (m1 == -INFINITY ? 0.f : exp2f(m1 - M) * sum1);
+          *reinterpret_cast<float2*>(a.mlpart + ((size_t)r * a.P + it.slot) * 2) = make_float2(M, wts[r] * sum0 + wts[32 + r] * sum1);
         }
         tc_fence_before();
         arrive(kOEmpty);
         ++u;
       }
       it.next();
+      rc.next(NC);
       ++n;
     }
   }
@@ -683,6 +830,250 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     tmem_dealloc(tmem, kCols);
   }
   if (threadIdx.x == 0 && *abort_flag) raise_error(a.err, MLA_DEVERR_TIMEOUT);
+}
+
+// ------------------------------------------------------------------ absorption
+// q_lat[row][c] = scale x log2(e) x sum_d q[row][d] W_ukF[g][d][c] (bf16, the attention's operand
+// type) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
+// kept pairs of the rows, rotated at L - 1.  Latency bound: the W_uk slice and the frequencies
+// come from the plan and are fetched before the kernel ahead is waited for; what follows the
+// wait is one round trip for queries and lengths.
+constexpr int kARows = 32, kACols = 64, kAThreads = 256;
+struct AbsorbArgs {
+  int B, H, G, n_kv, d_h, d_c, T_cap;
+  float scale;
+  const __nv_bfloat16* q;       // [B][H][d_h]
+  const __nv_bfloat16* W_ukF;   // [n_kv][d_h][d_c]
+  const int32_t* seq_lens;
+  const int32_t* rope_pair;     // [n_kv][4]
+  const double* theta;
+  __nv_bfloat16* qlat;          // [B][H][d_c]
+  float* qrope;                 // [B][H][8]
+};
+
+__global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  using bf16 = __nv_bfloat16;
+  constexpr int WLD = kACols + 8;
+  const int KP = (a.d_h + 15) & ~15, QLD = KP + 8;
+  bf16* sw = reinterpret_cast<bf16*>(smem);   // [KP][WLD]
+  bf16* sq = sw + KP * WLD;                   // [32][QLD]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rows_g = a.B * a.G, n_rb = (rows_g + kARows - 1) / kARows;
+  const int g = blockIdx.x % a.n_kv, rb = (blockIdx.x / a.n_kv) % n_rb, cc = blockIdx.x / (a.n_kv * n_rb);
+  const int row0 = rb * kARows, c0 = cc * kACols;
+  const bf16* W = a.W_ukF + (size_t)g * a.d_h * a.d_c;
+  auto index = [&](int row) { return (size_t)(row / a.G) * a.H + g * a.G + row % a.G; };
+  for (int v = tid; v < KP * (kACols / 8); v += kAThreads) {   // zeros past the matrix edges
+    const int d = v / (kACols / 8), c = (v % (kACols / 8)) * 8;
+    const bool ok = d < a.d_h && c0 + c < a.d_c;   // whole chunks: d_c is a multiple of 32
+    cp_async16(smem_u32(sw + d * WLD + c), ok ? (const void*)(W + (size_t)d * a.d_c + c0 + c) : a.W_ukF, ok ? 16u : 0u);
+  }
+  // RoPE (first column chunk): a thread per row and kept pair
+  const int rr = row0 + tid / 4;
+  const bool rot = cc == 0 && tid < 4 * kARows && rr < rows_g;
+  const int pair = rot ? __ldg(a.rope_pair + g * 4 + (tid & 3)) : 0;
+  const double th = rot ? __ldg(a.theta + pair) : 0.0;
+  pdl_wait();
+  pdl_trigger();
+  for (int v = tid; v < kARows * (KP / 8); v += kAThreads) {
+    const int r = v / (KP / 8), d = (v % (KP / 8)) * 8;
+    const bool ok = row0 + r < rows_g && d < a.d_h;   // whole chunks: d_h is a multiple of 8
+    cp_async16(smem_u32(sq + r * QLD + d), ok ? (const void*)(a.q + index(row0 + r) * a.d_h + d) : a.q, ok ? 16u : 0u);
+  }
+  cp_async_commit();
+  if (rot) {
+    const size_t o = index(rr);
+    const int L = __ldg(a.seq_lens + rr / a.G);
+    const uint32_t xy = __ldg(reinterpret_cast<const uint32_t*>(a.q + o * a.d_h) + pair);
+    const float x = __uint_as_float(xy << 16), y = __uint_as_float(xy & 0xFFFF0000u);
+    // the special-function unit's sine and cosine of an angle reduced to [-pi, pi]: about 5e-7
+    // off, against the 2^-9 of the rounding to bf16 that the attention applies
+    float sn, cs;
+    __sincosf(rope_angle(L >= 1 && L <= a.T_cap ? L - 1 : 0, th), &sn, &cs);
+    *reinterpret_cast<float2*>(a.qrope + o * 8 + 2 * (tid & 3)) = make_float2((x * cs - y * sn) * a.scale, (x * sn + y * cs) * a.scale);
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  const int m0 = 16 * (warp & 1), n0 = 16 * (warp >> 1);
+  if (row0 + m0 >= rows_g) return;
+  float acc[2][4] = {};
+#pragma unroll 4
+  for (int k0 = 0; k0 < KP; k0 += 16) {
+    uint32_t fa[4], fb[4];
+    wmma16::load_a(fa, sq, QLD, m0, k0, lane);
+    wmma16::load_b2(fb, sw, WLD, k0, n0, lane);
+    wmma16::mma_16816(acc[0], fa, fb[0], fb[1]);
+    wmma16::mma_16816(acc[1], fa, fb[2], fb[3]);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = row0 + m0 + (lane >> 2) + 8 * j;
+    if (row >= rows_g) continue;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int c = c0 + n0 + 8 * nt + 2 * (lane & 3);
+      if (c < a.d_c)
+        *reinterpret_cast<__nv_bfloat162*>(a.qlat + index(row) * a.d_c + c) =
+            __floats2bfloat162_rn(acc[nt][2 * j] * a.scale, acc[nt][2 * j + 1] * a.scale);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ merge of the pieces, W_uv
+// out[row][d] = sum_c (sum_j 2^(m_j - M) O_j[c] / sum_j 2^(m_j - M) l_j) W_uv[g][c][d] for 16 rows
+// (sequence, query head of KV head g) and 64 columns per CTA.  Latency bound: the W_uv chunk and
+// the pieces' slots are fetched and counted before the attention kernel is waited for, and a
+// warp has the partials of up to four pieces in flight.  The merged latent goes into the warp
+// products as two bf16 halves, so its rounding does not count.
+constexpr int kMRows = 16, kMCols = 64, kMThreads = 256;
+struct MergeArgs {
+  int B, H, G, n_kv, d_c, d_h, P, workers, T_cap;
+  MlaWindow win;
+  const int32_t* seq_lens;
+  const float* opart;
+  const float* mlpart;
+  const __nv_bfloat16* W_uv;   // [n_kv][d_c][d_h]
+  __nv_bfloat16* out;          // [B][H][d_h]
+  int32_t* err;
+};
+
+__global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_warp[32];
+  __shared__ int3 s_seq[kMRows];   // first unit, units, non-empty sequences before it
+  using bf16 = __nv_bfloat16;
+  constexpr int WLD = kMCols + 8;
+  const int ALD = a.d_c + 8;
+  bf16* sw = reinterpret_cast<bf16*>(smem);            // [d_c][WLD]
+  bf16* shi = sw + a.d_c * WLD;                        // [16][ALD]
+  bf16* slo = shi + kMRows * ALD;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rows_g = a.B * a.G, n_rb = (rows_g + kMRows - 1) / kMRows;
+  const int g = blockIdx.x % a.n_kv, rb = (blockIdx.x / a.n_kv) % n_rb, cc = blockIdx.x / (a.n_kv * n_rb);
+  const int row0 = rb * kMRows, d0 = cc * kMCols;
+  const bf16* W = a.W_uv + (size_t)g * a.d_c * a.d_h;
+  for (int v = tid; v < a.d_c * (kMCols / 8); v += kMThreads) {
+    const int c = v / (kMCols / 8), d = (v % (kMCols / 8)) * 8;
+    const bool ok = d0 + d < a.d_h;   // whole chunks: d_h is a multiple of 8
+    cp_async16(smem_u32(sw + c * WLD + d), ok ? (const void*)(W + (size_t)c * a.d_h + d0 + d) : a.W_uv, ok ? 16u : 0u);
+  }
+  cp_async_commit();
+  const int b_first = row0 / a.G;
+  int total = 0, ne = 0;
+  for (int base = 0; base < a.B; base += kMThreads) {
+    const SeqUnits u = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+    int tot_u, tot_ne;
+    const int ex_u = block_exscan(u.n, &tot_u, s_warp), ex_ne = block_exscan(u.n > 0 ? 1 : 0, &tot_ne, s_warp);
+    if (blockIdx.x == 0 && base + tid < a.B && (unsigned)__ldg(a.seq_lens + base + tid) > (unsigned)a.T_cap)
+      raise_error(a.err, MLA_DEVERR_SEQ_LEN);   // treated as empty
+    const int k = base + tid - b_first;
+    if (k >= 0 && k < kMRows && base + tid < a.B) s_seq[k] = make_int3(total + ex_u, u.n, ne + ex_ne);
+    total += tot_u;
+    ne += tot_ne;
+  }
+  __syncthreads();
+  const int busy = busy_workers(total, a.workers);
+  pdl_wait();   // the partials
+  pdl_trigger();
+#pragma unroll 1
+  for (int j = 0; j < kMRows / 8; ++j) {
+    const int r = warp + 8 * j, row = row0 + r;
+    float acc[8] = {};   // columns 4 lane + 0..3 and 128 + 4 lane + 0..3
+    if (row < rows_g) {
+      const int b = row / a.G, h = g * a.G + row % a.G;
+      const int3 sq = s_seq[b - b_first];
+      int first = 0, np = 0;
+      if (sq.y > 0) {
+        const int w0 = worker_of(sq.x + kSeqCost, total, busy), w1 = worker_of(sq.x + sq.y - 1, total, busy);
+        first = w0 + sq.z;
+        np = w1 - w0 + 1;
+      }
+      const float2* ml = reinterpret_cast<const float2*>(a.mlpart) + (size_t)h * a.P + first;
+      const float* op = a.opart + ((size_t)first * a.H + h) * a.d_c + 4 * lane;
+      const size_t step = (size_t)a.H * a.d_c;
+      const bool c0 = 4 * lane < a.d_c, c1 = 128 + 4 * lane < a.d_c;
+      float2 mine = lane < np ? __ldg(ml + lane) : make_float2(-INFINITY, 0.f);
+      float M = mine.x;
+      for (int k = lane + 32; k < np; k += 32) M = fmaxf(M, __ldg(ml + k).x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float den = 0.f;
+#pragma unroll 1
+      for (int k0 = 0; k0 < np; k0 += 32) {
+        if (k0 > 0) mine = k0 + lane < np ? __ldg(ml + k0 + lane) : make_float2(-INFINITY, 0.f);
+        const float wt = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
+        den += wt * mine.y;
+        const int n = min(32, np - k0);
+#pragma unroll 1
+        for (int k = 0; k < n; k += 4) {
+          float4 v[4][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k + i < n) {
+              const float* p = op + (size_t)(k0 + k + i) * step;
+              if (c0) v[i][0] = __ldg(reinterpret_cast<const float4*>(p));
+              if (c1) v[i][1] = __ldg(reinterpret_cast<const float4*>(p + 128));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float wk = __shfl_sync(0xffffffffu, wt, (k + i) & 31);
+            if (k + i < n) {
+              acc[0] += wk * v[i][0].x; acc[1] += wk * v[i][0].y; acc[2] += wk * v[i][0].z; acc[3] += wk * v[i][0].w;
+              acc[4] += wk * v[i][1].x; acc[5] += wk * v[i][1].y; acc[6] += wk * v[i][1].z; acc[7] += wk * v[i][1].w;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+      const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] *= inv;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = 128 * k + 4 * lane;
+      if (c >= a.d_c) continue;
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float x = acc[4 * k + 2 * e], y = acc[4 * k + 2 * e + 1];
+        hi[e] = pack2(x, y);
+        lo[e] = pack2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
+      }
+      *reinterpret_cast<uint2*>(shi + r * ALD + c) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(slo + r * ALD + c) = make_uint2(lo[0], lo[1]);
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  const int n0 = 8 * warp;   // this warp's columns
+  float ahi[4] = {}, alo[4] = {};
+#pragma unroll 2
+  for (int k0 = 0; k0 < a.d_c; k0 += 32) {
+    uint32_t bw[4], fh[4], fl[4];
+    // four 8 x 8 blocks down the columns: B fragments of two steps of 16
+    wmma16::ldsm_x4_t(smem_u32(sw + (k0 + lane) * WLD + n0), bw[0], bw[1], bw[2], bw[3]);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      wmma16::load_a(fh, shi, ALD, 0, k0 + 16 * st, lane);
+      wmma16::load_a(fl, slo, ALD, 0, k0 + 16 * st, lane);
+      wmma16::mma_16816(ahi, fh, bw[2 * st], bw[2 * st + 1]);
+      wmma16::mma_16816(alo, fl, bw[2 * st], bw[2 * st + 1]);
+    }
+  }
+  const int d = d0 + n0 + 2 * (lane & 3);
+  if (d >= a.d_h) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = row0 + (lane >> 2) + 8 * j;
+    if (row >= rows_g) continue;
+    const size_t o = ((size_t)(row / a.G) * a.H + g * a.G + row % a.G) * a.d_h + d;
+    *reinterpret_cast<__nv_bfloat162*>(a.out + o) = __floats2bfloat162_rn(ahi[2 * j] + alo[2 * j], ahi[2 * j + 1] + alo[2 * j + 1]);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -718,12 +1109,12 @@ static bool map_2d(CUtensorMap* m, bool bytes, const void* base, uint64_t cols, 
 
 struct Layout {
   int N, NC, NK, NRAW, n_cbox, n_kbox, kr_rows;
-  uint32_t off_q, off_qr, off_p, off_c, off_k, off_raw, raw_stage, off_red, off_bar, total;
+  uint32_t off_q, off_qr, off_p, off_c, off_k, off_raw, raw_stage, off_red, off_list, off_bar, total;
 };
 
 // [Q_lat boxes][RoPE query boxes][P of two streams][latent ring][key-box ring][code ring]
-// [exchange][barriers].  The slots left (16 KB: 128 tokens x 64 columns) go to latent tiles and
-// key boxes in the proportion a tile needs them, at least two latent tiles (one per stream).
+// [exchange][pieces][barriers].  Of the slots left (16 KB: 128 tokens x 64 columns) a tile's key boxes
+// come first, the others hold latent tiles, at least two (one per stream).
 static bool layout(const mla_config_t& c, int R, Layout* out) {
   Layout L{};
   const int G = c.n_heads / c.n_kv_heads, qbits = mla_kind_quant(c.cache_kind) ? mla_quant_bits(c.cache_kind) : 0;
@@ -736,22 +1127,18 @@ static bool layout(const mla_config_t& c, int R, Layout* out) {
   L.off_qr = (uint32_t)(L.n_cbox * L.N) * 128;
   L.off_p = L.off_qr + (uint32_t)(L.n_kbox * L.kr_rows) * 128;
   L.off_c = L.off_p + 2u * kT * L.N * 2;
-  const uint32_t tail = kRedBytes + 8 * kBars + 16 + 1024;
+  const uint32_t tail = kRedBytes + kPieces * 16 + 8 * kBars + 16 + 1024 + 1024;   // alignment, static part
   const uint32_t fixed = L.off_c + L.NRAW * L.raw_stage + tail;
   if (fixed > kSmemMax) return false;
   const int slots = (int)((kSmemMax - fixed) / kSlot);
-  const int per = L.n_cbox + L.n_kbox;
-  L.NC = std::max(2, std::min(kMaxC, (slots + per - 1) / per));
+  L.NC = std::max(2, std::min(kMaxC, (slots - L.n_kbox) / L.n_cbox));
   L.NK = std::min(kMaxK, slots - L.NC * L.n_cbox);
-  if (L.NK < 1 && L.NC > 2) {
-    L.NC = 2;
-    L.NK = std::min(kMaxK, slots - L.NC * L.n_cbox);
-  }
   if (L.NK < 1) return false;
   L.off_k = L.off_c + (uint32_t)(L.NC * L.n_cbox) * kSlot;
   L.off_raw = L.off_k + (uint32_t)L.NK * kSlot;
   L.off_red = L.off_raw + L.NRAW * L.raw_stage;
-  L.off_bar = L.off_red + kRedBytes;
+  L.off_list = L.off_red + kRedBytes;
+  L.off_bar = L.off_list + kPieces * 16;
   L.total = L.off_bar + 8 * kBars + 16 + 1024;
   *out = L;
   return true;
@@ -761,36 +1148,40 @@ static bool layout(const mla_config_t& c, int R, Layout* out) {
 }  // namespace mla
 
 // Shapes: bf16 with r = 4 kept pairs per KV head, up to 32 query heads and 32 KV heads, d_c a
-// multiple of 32 up to 256, code rows of whole 16 bytes, key rows of whole 16 bytes.
+// multiple of 32 up to 256, head dim a multiple of 8, code rows of whole 16 bytes.
 bool mla_window_decode_capable(const mla_plan& p) {
   const mla_config_t& c = p.cfg;
-  if (c.dtype != MLA_BF16 || c.r_pairs != 4 || c.n_heads > 32 || c.d_c % 32 != 0 || c.d_c > 256) return false;
+  if (c.dtype != MLA_BF16 || c.r_pairs != 4 || c.n_heads > 32 || c.head_dim % 8 != 0 || c.d_c % 32 != 0 || c.d_c > 256) return false;
   if (mla_kind_quant(c.cache_kind) && c.d_c * mla_quant_bits(c.cache_kind) / 8 % 16 != 0) return false;
   mla::wdec::Layout L;
   return mla::wdec::layout(c, p.R, &L);
 }
 
-cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, int B,
-                                     const Sched& sched, const void* qlat, const float* qrope, float* opart,
-                                     float* mlpart, int P, int G, MlaWindow win, cudaStream_t s) {
+cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
+                                     int B, void* out, void* ws, const DecodeLayout& D, MlaWindow win, cudaStream_t s) {
   using namespace mla::wdec;
   const mla_config_t& cfg = p.cfg;
+  char* base = (char*)ws;
   const int qbits = mla_kind_quant(cfg.cache_kind) ? mla_quant_bits(cfg.cache_kind) : 0;
   Layout L;
   if (!layout(cfg, p.R, &L)) return cudaErrorInvalidValue;
   Args a;
-  a.H = cfg.n_heads; a.G = a.H / cfg.n_kv_heads; a.d_c = cfg.d_c; a.dcp = L.n_cbox * 64; a.R = p.R; a.P = P;
+  a.H = cfg.n_heads; a.G = a.H / cfg.n_kv_heads; a.d_c = cfg.d_c; a.dcp = L.n_cbox * 64; a.R = p.R; a.P = D.P;
   a.T_cap = c.T_cap; a.n_cbox = L.n_cbox; a.n_kbox = L.n_kbox; a.kr_rows = L.kr_rows;
   a.NC = L.NC; a.NK = L.NK; a.NRAW = L.NRAW;
-  a.win = win; a.sched = sched; a.seq_lens = seq_lens; a.qrope = qrope; a.opart = opart; a.mlpart = mlpart;
+  a.kpb = L.NK >= L.n_kbox ? L.n_kbox : std::max(1, L.NK - 1);
+  a.B = B; a.workers = D.G; a.win = win;
+  a.pieces = (int4*)(base + D.off_piece_b);
+  a.seq_lens = seq_lens; a.qrope = (const float*)(base + D.off_qrope);
+  a.opart = (float*)(base + D.off_opart); a.mlpart = (float*)(base + D.off_mlpart);
   a.scales = (const __half*)c.c_scales; a.code_row = (uint32_t)(cfg.d_c * qbits / 8); a.cache = c; a.err = p.err;
   a.wait_ns = (uint64_t)p.opt_wait_us * 1000u;
   a.off_q = L.off_q; a.off_qr = L.off_qr; a.off_p = L.off_p; a.off_c = L.off_c; a.off_k = L.off_k; a.off_raw = L.off_raw;
-  a.raw_stage = L.raw_stage; a.off_red = L.off_red; a.off_bar = L.off_bar;
+  a.raw_stage = L.raw_stage; a.off_red = L.off_red; a.off_list = L.off_list; a.off_bar = L.off_bar;
   const uint64_t rows = mla_cache_rows(c);
   CUtensorMap tm_c, tm_kr, tm_q;
   bool ok = map_2d(&tm_kr, false, c.k_rope, p.R, rows, 64, kUnit) &&
-            map_2d(&tm_q, false, qlat, cfg.d_c, (uint64_t)B * a.H, 64, a.H);
+            map_2d(&tm_q, false, base + D.off_qlat, cfg.d_c, (uint64_t)B * a.H, 64, a.H);
   ok = ok && (qbits ? map_2d(&tm_c, true, c.c_kv, a.code_row, rows, a.code_row, kUnit)
                     : map_2d(&tm_c, false, c.c_kv, cfg.d_c, rows, 64, kUnit));
   if (!ok) return cudaErrorInvalidValue;
@@ -799,10 +1190,36 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
     return qbits == 4 ? window_decode_kernel<N, 4> : qbits == 2 ? window_decode_kernel<N, 2> : window_decode_kernel<N, 0>;
   };
   const auto kern = L.N == 16 ? pick(std::integral_constant<int, 16>()) : pick(std::integral_constant<int, 32>());
-  cudaError_t e = mla_smem_limit((const void*)kern, L.total);
+  AbsorbArgs b;
+  b.B = B; b.H = a.H; b.G = a.G; b.n_kv = cfg.n_kv_heads; b.d_h = cfg.head_dim; b.d_c = cfg.d_c; b.T_cap = c.T_cap;
+  b.scale = mla::kLog2e * (cfg.softmax_scale > 0.0f ? cfg.softmax_scale : (float)(1.0 / sqrt((double)cfg.head_dim)));
+  b.q = (const __nv_bfloat16*)q; b.W_ukF = (const __nv_bfloat16*)p.W_ukF; b.seq_lens = seq_lens;
+  b.rope_pair = p.rope_pair; b.theta = p.theta;
+  b.qlat = (__nv_bfloat16*)(base + D.off_qlat); b.qrope = (float*)(base + D.off_qrope);
+  const int KP = (cfg.head_dim + 15) & ~15;
+  const size_t smem_b = sizeof(__nv_bfloat16) * ((size_t)KP * (kACols + 8) + (size_t)kARows * (KP + 8));
+  const int n_rba = (B * a.G + kARows - 1) / kARows, n_cca = (cfg.d_c + kACols - 1) / kACols;
+  cudaError_t e = mla_smem_limit((const void*)window_absorb_kernel, smem_b);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfAbsorb, false, s);
+  if (e == cudaSuccess)
+    e = mla_launch_kernel(window_absorb_kernel, dim3(cfg.n_kv_heads * n_rba * n_cca), dim3(kAThreads), smem_b, s, p.opt_pdl, b);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfAbsorb, true, s);
+  if (e == cudaSuccess) e = mla_smem_limit((const void*)kern, L.total);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfAttention, false, s);
+  if (e == cudaSuccess)
+    e = mla_launch_kernel(kern, dim3(D.G), dim3(qbits ? kThreadsOf<4> : kThreadsOf<0>), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_q, a);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfAttention, true, s);
   if (e != cudaSuccess) return e;
-  if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
-  e = mla_launch_kernel(kern, dim3(G), dim3(kThreads), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_q, a);
-  if (e != cudaSuccess) return e;
-  return mla_profile_event(p, kProfAttention, true, s);
+  MergeArgs m;
+  m.B = B; m.H = a.H; m.G = a.G; m.n_kv = cfg.n_kv_heads; m.d_c = cfg.d_c; m.d_h = cfg.head_dim; m.P = D.P;
+  m.workers = D.G; m.T_cap = c.T_cap; m.win = win; m.seq_lens = seq_lens; m.opart = a.opart; m.mlpart = a.mlpart;
+  m.W_uv = (const __nv_bfloat16*)p.W_uv; m.out = (__nv_bfloat16*)out; m.err = p.err;
+  const size_t smem = sizeof(__nv_bfloat16) * ((size_t)cfg.d_c * (kMCols + 8) + 2 * (size_t)kMRows * (cfg.d_c + 8));
+  const int n_rb = (B * a.G + kMRows - 1) / kMRows, n_cc = (cfg.head_dim + kMCols - 1) / kMCols;
+  e = mla_smem_limit((const void*)window_merge_kernel, smem);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfCombine, false, s);
+  if (e == cudaSuccess)
+    e = mla_launch_kernel(window_merge_kernel, dim3(cfg.n_kv_heads * n_rb * n_cc), dim3(kMThreads), smem, s, p.opt_pdl, m);
+  if (e == cudaSuccess) e = mla_profile_event(p, kProfCombine, true, s);
+  return e;
 }

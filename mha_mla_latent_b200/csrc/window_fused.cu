@@ -128,19 +128,17 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   const uint32_t tmem = *s_tmem;
   const int n_cbox = a.dcp / 64, n_hbox = a.dhp / 64;
   const uint32_t uk_bytes = (uint32_t)n_cbox * a.d_h * 128u, uv_bytes = (uint32_t)n_hbox * a.d_c * 128u;
-  auto stage_at = [&](int i) { return sb + a.off_ring + (uint32_t)(i % NST) * a.stage; };
 
   // The first W_uk slices belong to the plan: they may load before the kernels ahead are done.
   int loaded = 0;   // ring items issued (producer)
-  auto load_uk = [&](int gi) {
-    const int s = loaded % NST;
+  auto load_uk = [&](int gi, int s) {
     mbar_expect_tx(bar(kBarFull + s), uk_bytes);
     for (int k = 0; k < n_cbox; ++k)
-      tma_load_2d(stage_at(loaded) + k * a.d_h * 128, &tm_uk, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_h);
+      tma_load_2d(sb + a.off_ring + (uint32_t)s * a.stage + k * a.d_h * 128, &tm_uk, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_h);
     ++loaded;
   };
   if (warp == 0 && lane == 0)
-    while (loaded < min(ng, NST)) load_uk(loaded);
+    while (loaded < min(ng, NST)) load_uk(loaded, loaded);
   // rows (warps 4-11): thread -> row r of the unit, half hf of its tokens and columns
   const int w = warp & 3, hf = warp >= 8, r = 32 * w + lane;   // tensor memory lane = row
   const int per_g = a.G * a.qb;
@@ -190,23 +188,27 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
     if (lane == 0) {
       const int items = T > 0 ? 2 * ng + T : 0;
       bool ok = true;
+      RingPos rp;
+      for (int i = 0; i < loaded; ++i) rp.next(NST);
       while (ok && loaded < items) {
-        const int i = loaded, s = i % NST;
-        if (i >= NST) ok = mbar_spin(bar(kBarEmpty + s), ((i / NST) - 1) & 1, abort_flag, lim);
+        const int i = loaded, s = rp.slot;
+        if (i >= NST) ok = mbar_spin(bar(kBarEmpty + s), rp.parity ^ 1, abort_flag, lim);
         if (!ok) break;
-        if (i < ng) { load_uk(i); continue; }
+        rp.next(NST);
+        if (i < ng) { load_uk(i, s); continue; }
+        const uint32_t at = sb + a.off_ring + (uint32_t)s * a.stage;
         if (i < ng + T) {
           const int t = tile_token(i - ng);
           const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
           const int row = lc.pb * lc.cap + lc.pt;
           mbar_expect_tx(bar(kBarFull + s), (uint32_t)n_cbox * kBox + kKrTile);
-          for (int k = 0; k < n_cbox; ++k) tma_load_2d(stage_at(i) + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
-          tma_load_2d(stage_at(i) + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
+          for (int k = 0; k < n_cbox; ++k) tma_load_2d(at + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
+          tma_load_2d(at + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
         } else {
           const int gi = i - ng - T;
           mbar_expect_tx(bar(kBarFull + s), uv_bytes);
           for (int k = 0; k < n_hbox; ++k)
-            tma_load_2d(stage_at(i) + k * a.d_c * 128, &tm_uv, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_c);
+            tma_load_2d(at + k * a.d_c * 128, &tm_uv, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_c);
         }
         ++loaded;
       }
@@ -223,21 +225,23 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)) != 0;
       };
       auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
-      auto full = [&](int i) { return wait_all(kBarFull + i % NST, (i / NST) & 1); };
+      auto stage_at = [&](const RingPos& p) { return sb + a.off_ring + (uint32_t)p.slot * a.stage; };
+      RingPos r1;   // ring items: weights, then tiles (S), then weights
       bool ok = wait_all(kBarQ, 0);
       // absorption: q (tensor memory) x W_ukF[g], once per KV head over all rows
       const uint32_t id_abs = idesc_bf16_f32(kRows, a.dcp, false, true);
       for (int gi = 0; ok && gi < ng; ++gi) {
-        ok = full(gi) && (gi == 0 || wait_all(kBarAccEmpty, (gi - 1) & 1));
+        ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (gi - 1) & 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t w0 = smem_desc(stage_at(gi), a.d_h * 128, 1024, kLayoutSW128);
+          const uint64_t w0 = smem_desc(stage_at(r1), a.d_h * 128, 1024, kLayoutSW128);
           for (int k = 0; k < a.d_h / 16; ++k) mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, w0 + 128u * k, id_abs, k > 0);
-          tc_commit(bar(kBarEmpty + gi % NST));
+          tc_commit(bar(kBarEmpty + r1.slot));
           tc_commit(bar(kBarAccFull));
         }
         __syncwarp();
+        r1.next(NST);
       }
       ok = ok && wait_all(kBarQlat, 0);
       tc_fence_after();
@@ -247,14 +251,14 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       // descriptors are made once; a step along K adds its bytes / 16 to the address field
       const uint64_t desc_q = smem_desc(sb, 16, 1024, kLayoutSW128), desc_qr = smem_desc(sb + a.off_qr, 16, 512, kLayoutSW64);
       int n1 = 0, n2 = 0;
+      RingPos r2 = r1;     // tiles of O
       uint64_t idle = 0;   // when nothing could be issued: since when (read every 64th look only)
       int looks = 0;
       while (ok && n2 < T) {
-        const int i1 = ng + n1, i2 = ng + n2;
-        if (n1 < T && n1 <= n2 + 1 && ready(kBarFull + i1 % NST, (i1 / NST) & 1)) {
+        if (n1 < T && n1 <= n2 + 1 && ready(kBarFull + r1.slot, r1.parity)) {
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t c0 = stage_at(i1), d = tmem + kSCol + (n1 & 1) * kT;
+            const uint32_t c0 = stage_at(r1), d = tmem + kSCol + (n1 & 1) * kT;
             uint64_t da = desc_q, db = smem_desc(c0, 16, 1024, kLayoutSW128);
             const uint64_t dk = smem_desc(c0 + n_cbox * kBox, 16, 512, kLayoutSW64);
             tc_mma_bf16(d, desc_qr, dk, id_s, 0);
@@ -270,20 +274,22 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
             tc_commit(bar(kBarS + (n1 & 1)));
           }
           __syncwarp();
+          r1.next(NST);
           ++n1;
           looks = 0;
         } else if (n2 < n1 && ready(kBarP + (n2 & 1), (n2 >> 1) & 1)) {
           tc_fence_after();
           if (elect_one()) {
             const uint32_t p = tmem + kSCol + (n2 & 1) * kT;
-            const uint64_t dv = smem_desc(stage_at(i2), kBox, 1024, kLayoutSW128);
+            const uint64_t dv = smem_desc(stage_at(r2), kBox, 1024, kLayoutSW128);
             mma_a_tmem(tmem + kOCol, p, dv, id_o, n2 > 0);
 #pragma unroll
             for (int k = 1; k < kT / 16; ++k) mma_a_tmem(tmem + kOCol, p + 8 * k, dv + 128 * k, id_o, 1);
-            tc_commit(bar(kBarEmpty + i2 % NST));
+            tc_commit(bar(kBarEmpty + r2.slot));
             tc_commit(bar(kBarO + (n2 & 1)));
           }
           __syncwarp();
+          r2.next(NST);
           ++n2;
           looks = 0;
         } else if ((++looks & 63) == 0) {
@@ -297,18 +303,18 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       const uint32_t id_out = idesc_bf16_f32(kRows, a.dhp, false, true);
       ok = ok && wait_all(kBarA, 0);
       for (int gi = 0; ok && gi < ng; ++gi) {
-        const int i = ng + T + gi;
-        ok = full(i) && (gi == 0 || wait_all(kBarAccEmpty, (ng + gi - 1) & 1));
+        ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (ng + gi - 1) & 1));
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t w0 = smem_desc(stage_at(i), a.d_c * 128, 1024, kLayoutSW128);
+          const uint64_t w0 = smem_desc(stage_at(r1), a.d_c * 128, 1024, kLayoutSW128);
           for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kSCol + 8 * k, w0 + 128u * k, id_out, k > 0);
           for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kOCol + 8 * k, w0 + 128u * k, id_out, 1);
-          tc_commit(bar(kBarEmpty + i % NST));
+          tc_commit(bar(kBarEmpty + r1.slot));
           tc_commit(bar(kBarAccFull));
         }
         __syncwarp();
+        r1.next(NST);
       }
       if (elect_one()) tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
       __syncwarp();
@@ -399,8 +405,10 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       // tiles: this thread's tokens are [64 hf, 64 hf + 64) of each
       const int p_row = valid ? p0 + qi : -1;
       float m = -INFINITY, l = 0.f;
+      RingPos rt;
+      for (int i = 0; i < ng; ++i) rt.next(NST);
 #pragma unroll 1
-      for (int n = 0; ok && n < T; ++n) {
+      for (int n = 0; ok && n < T; ++n, rt.next(NST)) {
         const int t0 = tile_token(n), nvalid = min(kT, span.len - n * kT);
         ok = wwait(kBarS + (n & 1), (n >> 1) & 1);
         if (!ok) break;
@@ -430,7 +438,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
           for (int t = 0; t < 64; ++t) s[t] = ((uint32_t)(seen >> (t & 32)) >> (t & 31)) & 1u ? s[t] : -INFINITY;
           // rows that no query of the unit sees (stale or hidden, possibly not finite) are
           // zeroed before O's product multiplies them by P = 0; S of this tile has been read
-          uint8_t* C = smem + a.off_ring + (uint32_t)((ng + n) % NST) * a.stage;
+          uint8_t* C = smem + a.off_ring + (uint32_t)rt.slot * a.stage;
           auto zero_rows = [&](int from, int to) {   // consecutive threads, consecutive 16-byte chunks
             for (int i = from * 8 + 128 * hf + r; i < to * 8; i += 256)
               for (int k = 0; k < n_cbox; ++k) *reinterpret_cast<uint4*>(C + k * kBox + i * 16) = make_uint4(0, 0, 0, 0);
