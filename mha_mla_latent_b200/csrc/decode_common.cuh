@@ -222,19 +222,19 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
 // the part of sequence b in worker w's range, and its partial goes to slot w + (non-empty
 // sequences before b): slots of one sequence are consecutive, and all are below B + G.
 //
-// A sequence counts kSeqCost units more than it has, ahead of its own: beginning a piece costs
-// a worker about that long, so workers with a sequence's end and the next one's start get fewer.
-constexpr int kSeqCost = 2;
+// A sequence counts `cost` units more than it has, ahead of its own: ending a piece and beginning
+// another costs a worker about that long, so workers with a sequence's end and the next one's
+// start get fewer.
 struct SeqUnits {
-  int len = 0, n = 0;   // visible tokens, units with kSeqCost (0 for an empty sequence)
+  int len = 0, n = 0;   // visible tokens, units with the cost (0 for an empty sequence)
 };
-__device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, MlaWindow win) {
+__device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, int cost, MlaWindow win) {
   SeqUnits s;
   if (b >= B) return s;
   const int L = __ldg(seq_lens + b);
   if (L <= 0 || L > T_cap) return s;
   s.len = unit_span(L, 1, tile, win).len;
-  s.n = (s.len + tile - 1) / tile + kSeqCost;
+  s.n = (s.len + tile - 1) / tile + cost;
   return s;
 }
 // Workers that get units: no more than there are units, so that none in between is empty.

@@ -55,7 +55,7 @@ struct Args {
   int n_cbox, n_kbox, kr_rows;            // boxes per token row; heads a key box is multiplied with
   int kpb;                                // key boxes issued together
   int NC, NK, NRAW;                       // latent tiles, key boxes, code tiles in the rings
-  int B, workers;
+  int B, workers, cost;                   // cost of a piece, in units (see seq_units)
   MlaWindow win;
   int4* pieces;                           // [P] by slot: the pieces past the first kPieces of a worker
   const int32_t* seq_lens;
@@ -171,7 +171,7 @@ __device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, i
   SeqUnits mine;
   int my_ex = 0;
   for (int base = 0; base < a.B; base += nt) {
-    mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+    mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.cost, a.win);
     int tot;
     my_ex = block_exscan(mine.n, &tot, s_warp);
     total += tot;
@@ -182,7 +182,7 @@ __device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, i
   int c_carry = 0, ne_carry = 0;
   for (int base = 0; base < a.B; base += nt) {
     if (a.B > nt) {   // more sequences than threads: their units once more
-      mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+      mine = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.cost, a.win);
       int tot;
       my_ex = block_exscan(mine.n, &tot, s_warp);
       my_ex += c_carry;
@@ -191,7 +191,7 @@ __device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, i
     int tot_ne;
     const int ne = ne_carry + block_exscan(mine.n > 0 ? 1 : 0, &tot_ne, s_warp);
     ne_carry += tot_ne;
-    const int first = my_ex + kSeqCost;   // where the sequence's own units begin
+    const int first = my_ex + a.cost;   // where the sequence's own units begin
     const bool in = mine.n > 0 && first < w1 && my_ex + mine.n > w0;
     if (in) atomicMin(s_misc, ne);   // the worker's first sequence
     __syncthreads();
@@ -560,16 +560,21 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         for (int c = 0; c < a.d_c / 8; ++c) put(c, __ldg(src + c));
       } else if (cur.live) {
         const uint8_t* codes = smem + a.off_raw + rs * a.raw_stage + r * a.code_row;
+        // (a rolled loop: unrolled, the roles' code no longer fits the instruction caches)
+        uint32_t scw[4];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          if (g >= a.d_c / 32) break;
+        for (int k = 0; k < 4; ++k) scw[k] = cur.sc[2 * k] | (uint32_t)cur.sc[2 * k + 1] << 16;
+#pragma unroll 1
+        for (int g = 0; g < a.d_c / 32; ++g) {
           // An offset code u = code + top sits in the mantissa of 1.0 from bit 23 - QB on: the
           // float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at
           // most QB + 11 bits), rounded once to bf16, the products' operand type.
           constexpr uint32_t kTop = 1u << (QB ? QB - 1 : 0), kMask = (2 * kTop - 1) << (23 - QB);
           constexpr uint32_t kOne = 0x3F800000u ^ (kTop << (23 - QB));
-          const float sv = __half2float(__ushort_as_half(cur.sc[g]));
+          const float sv = __half2float(__ushort_as_half((unsigned short)scw[0]));
           const float mul = sv * (float)(2 * kTop), add = -sv * (float)(3 * kTop);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) scw[k] = __funnelshift_r(scw[k], k < 3 ? scw[k + 1] : 0u, 16);   // the next group's scale
           uint32_t wd[4];
           if (QB == 4) {
             const uint4 cw = *reinterpret_cast<const uint4*>(codes + g * 16);
@@ -785,21 +790,24 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         // this group writes heads [N/2 s, N/2 s + N/2): lane = latent column
         const float* l0 = sums + par * 2 * 4 * 32;
         constexpr int HN = N / 2;
-        for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk) {
-          const int c = blk * 128 + r;
-          for (int h0 = 0; h0 < HN; h0 += 8) {
-            uint32_t o0[8], o1[8];
-            tmem_ld8(lane0 + kOCol + blk * 32 + HN * s + h0, o0);
-            tmem_ld8(lane0 + kOCol + 64 + blk * 32 + HN * s + h0, o1);
-            tmem_wait_ld();
+        float w0[HN], w1[HN];   // weight 0: the stream's columns may be stale
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              asm volatile("" : "+r"(o0[e]), "+r"(o1[e]));
-              const int h = HN * s + h0 + e;
-              const float w0 = wts[h], w1 = wts[32 + h];   // weight 0: the columns may be stale
-              const float v = (w0 > 0.f ? w0 * __uint_as_float(o0[e]) : 0.f) + (w1 > 0.f ? w1 * __uint_as_float(o1[e]) : 0.f);
-              if (h < a.H && c < a.d_c) a.opart[((size_t)it.slot * a.H + h) * a.d_c + c] = v;
-            }
+        for (int e = 0; e < HN; ++e) { w0[e] = wts[HN * s + e]; w1[e] = wts[32 + HN * s + e]; }
+        float* dst = a.opart + ((size_t)it.slot * a.H + HN * s) * a.d_c + r;
+#pragma unroll 1
+        for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk, dst += 128) {
+          uint32_t o0[HN], o1[HN];
+#pragma unroll
+          for (int e = 0; e < HN; e += 8) {
+            tmem_ld8(lane0 + kOCol + blk * 32 + HN * s + e, *reinterpret_cast<uint32_t(*)[8]>(o0 + e));
+            tmem_ld8(lane0 + kOCol + 64 + blk * 32 + HN * s + e, *reinterpret_cast<uint32_t(*)[8]>(o1 + e));
+          }
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < HN; ++e) {
+            asm volatile("" : "+r"(o0[e]), "+r"(o1[e]));
+            const float v = (w0[e] > 0.f ? w0[e] * __uint_as_float(o0[e]) : 0.f) + (w1[e] > 0.f ? w1[e] * __uint_as_float(o1[e]) : 0.f);
+            if (HN * s + e < a.H && blk * 128 + r < a.d_c) dst[(size_t)e * a.d_c] = v;
           }
         }
         if (s == 0 && r < a.H) {
@@ -928,7 +936,7 @@ __global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) 
 // products as two bf16 halves, so its rounding does not count.
 constexpr int kMRows = 16, kMCols = 64, kMThreads = 256;
 struct MergeArgs {
-  int B, H, G, n_kv, d_c, d_h, P, workers, T_cap;
+  int B, H, G, n_kv, d_c, d_h, P, workers, T_cap, cost;
   MlaWindow win;
   const int32_t* seq_lens;
   const float* opart;
@@ -962,7 +970,7 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
   const int b_first = row0 / a.G;
   int total = 0, ne = 0;
   for (int base = 0; base < a.B; base += kMThreads) {
-    const SeqUnits u = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.win);
+    const SeqUnits u = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.cost, a.win);
     int tot_u, tot_ne;
     const int ex_u = block_exscan(u.n, &tot_u, s_warp), ex_ne = block_exscan(u.n > 0 ? 1 : 0, &tot_ne, s_warp);
     if (blockIdx.x == 0 && base + tid < a.B && (unsigned)__ldg(a.seq_lens + base + tid) > (unsigned)a.T_cap)
@@ -985,7 +993,7 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
       const int3 sq = s_seq[b - b_first];
       int first = 0, np = 0;
       if (sq.y > 0) {
-        const int w0 = worker_of(sq.x + kSeqCost, total, busy), w1 = worker_of(sq.x + sq.y - 1, total, busy);
+        const int w0 = worker_of(sq.x + a.cost, total, busy), w1 = worker_of(sq.x + sq.y - 1, total, busy);
         first = w0 + sq.z;
         np = w1 - w0 + 1;
       }
@@ -1171,6 +1179,8 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   a.NC = L.NC; a.NK = L.NK; a.NRAW = L.NRAW;
   a.kpb = L.NK >= L.n_kbox ? L.n_kbox : std::max(1, L.NK - 1);
   a.B = B; a.workers = D.G; a.win = win;
+  // about 5 us, the time a CTA takes for 220 KB; a unit of short rows is bound by latency instead
+  a.cost = std::max(2, std::min(8, (int)(3400 / mla_cache_bytes_per_token(&cfg))));
   a.pieces = (int4*)(base + D.off_piece_b);
   a.seq_lens = seq_lens; a.qrope = (const float*)(base + D.off_qrope);
   a.opart = (float*)(base + D.off_opart); a.mlpart = (float*)(base + D.off_mlpart);
@@ -1212,7 +1222,7 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   if (e != cudaSuccess) return e;
   MergeArgs m;
   m.B = B; m.H = a.H; m.G = a.G; m.n_kv = cfg.n_kv_heads; m.d_c = cfg.d_c; m.d_h = cfg.head_dim; m.P = D.P;
-  m.workers = D.G; m.T_cap = c.T_cap; m.win = win; m.seq_lens = seq_lens; m.opart = a.opart; m.mlpart = a.mlpart;
+  m.workers = D.G; m.cost = a.cost; m.T_cap = c.T_cap; m.win = win; m.seq_lens = seq_lens; m.opart = a.opart; m.mlpart = a.mlpart;
   m.W_uv = (const __nv_bfloat16*)p.W_uv; m.out = (__nv_bfloat16*)out; m.err = p.err;
   const size_t smem = sizeof(__nv_bfloat16) * ((size_t)cfg.d_c * (kMCols + 8) + 2 * (size_t)kMRows * (cfg.d_c + 8));
   const int n_rb = (B * a.G + kMRows - 1) / kMRows, n_cc = (cfg.head_dim + kMCols - 1) / kMCols;
