@@ -15,4 +15,6 @@ __all__ = ["build", "cache", "convert"]
 def __getattr__(name):
     if name.startswith("__") or name in ("build", "cache", "convert", "_lib"):
         return importlib.import_module(f"{__name__}.{name}")
-    return getattr(importlib.import_module(f"{__name__}._lib"), name)
+    value = getattr(importlib.import_module(f"{__name__}._lib"), name)
+    globals()[name] = value   # found at once from now on: this function costs a call 2 us
+    return value

@@ -304,40 +304,40 @@ def mla_blocks_workspace_bytes(B: int, n_cols: int, n_blocks: int) -> int:
 _I32 = torch.int32
 
 
-def _i32(t, name, shape=None):
-    """Device pointer of a contiguous int32 device tensor (of the given shape, where one is given)."""
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be a contiguous int32 device tensor"
-                         + (f" of shape {list(shape)}" if shape is not None else ""))
+def _i32(t, name, n):
+    """Device pointer of a contiguous int32 device tensor of n elements."""
+    if t.dtype is not _I32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 device tensor of {n} elements")
     return t.data_ptr()
 
 
 def _table(table, refs):
-    """Pointers and sizes of a block table [B][n_cols] and its holder counts [n_blocks]."""
-    if table.dim() != 2 or refs.dim() != 1:
-        raise ValueError("table is [B][n_cols], refs is [n_blocks]")
+    """Sizes of a block table [B][n_cols] and its holder counts [n_blocks]."""
     B, C = table.shape
-    return _i32(table, "table"), _i32(refs, "refs"), B, C, refs.shape[0]
+    return B, C, refs.numel()
 
 
 def _block_status(status):
     if status.numel() < MLA_BLOCKS_STATUS_INTS:
         raise ValueError(f"status holds {MLA_BLOCKS_STATUS_INTS} int32")
-    return _i32(status, "status")
+    return _i32(status, "status", status.numel())
 
 
 def _block_copies(copies):
-    if copies.dim() != 2 or copies.shape[1] != 3:
+    n, three = copies.shape
+    if three != 3:
         raise ValueError("copies is [max_copies][3]")
-    return _i32(copies, "copies"), copies.shape[0]
+    return _i32(copies, "copies", 3 * n), n
 
 
 def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status, stream=None, check=True):
     """Row dst[i] of the table shares the blocks of row src[i] (its first seq_lens[src[i]] tokens)."""
-    t, r, B, C, n = _table(table, refs)
-    st = _lib.mla_blocks_fork(t, r, B, C, n, _i32(src, "src"), _i32(dst, "dst", src.shape), src.numel(),
-                              _i32(seq_lens, "seq_lens", (B,)), _i32(table_out, "table_out", (B, C)),
-                              _i32(refs_out, "refs_out", (n,)), _block_status(status), _stream(stream))
+    B, C, n = _table(table, refs)
+    k = src.numel()
+    st = _lib.mla_blocks_fork(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n, _i32(src, "src", k),
+                              _i32(dst, "dst", k), k, _i32(seq_lens, "seq_lens", B),
+                              _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n),
+                              _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_blocks_fork")
     return st
@@ -346,10 +346,11 @@ def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status
 def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, copies, status, workspace, stream=None,
                        check=True):
     """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence, shared partial blocks copied on write."""
-    t, r, B, C, n = _table(table, refs)
+    B, C, n = _table(table, refs)
     cp, n_cp = _block_copies(copies)
-    st = _lib.mla_blocks_reserve(t, r, B, C, n, _i32(seq_lens, "seq_lens", (B,)), _i32(new_lens, "new_lens", (B,)),
-                                 _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)), cp, n_cp,
+    st = _lib.mla_blocks_reserve(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
+                                 _i32(seq_lens, "seq_lens", B), _i32(new_lens, "new_lens", B),
+                                 _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n), cp, n_cp,
                                  _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_blocks_reserve")
@@ -358,10 +359,10 @@ def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, cop
 
 def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, status, stream=None, check=True):
     """Releases the blocks without a token among the first n_sink or the newest `window` ones."""
-    t, r, B, C, n = _table(table, refs)
-    st = _lib.mla_blocks_trim(t, r, B, C, n, _i32(seq_lens, "seq_lens", (B,)), n_sink, window,
-                              _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)),
-                              _block_status(status), _stream(stream))
+    B, C, n = _table(table, refs)
+    st = _lib.mla_blocks_trim(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
+                              _i32(seq_lens, "seq_lens", B), n_sink, window, _i32(table_out, "table_out", B * C),
+                              _i32(refs_out, "refs_out", n), _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_blocks_trim")
     return st
@@ -369,10 +370,11 @@ def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, 
 
 def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspace, stream=None, check=True):
     """Moves the blocks in use to the lowest ids; `copies` lists the moves."""
-    t, r, B, C, n = _table(table, refs)
+    B, C, n = _table(table, refs)
     cp, n_cp = _block_copies(copies)
-    st = _lib.mla_blocks_compact(t, r, B, C, n, _i32(table_out, "table_out", (B, C)), _i32(refs_out, "refs_out", (n,)),
-                                 cp, n_cp, _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
+    st = _lib.mla_blocks_compact(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
+                                 _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n), cp, n_cp,
+                                 _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
     if check:
         _check(st, "mla_blocks_compact")
     return st
@@ -389,8 +391,9 @@ def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None
 
 def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True):
     """Copies the residual windows of sequences src to sequences dst in one layer's cache."""
-    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src"), _i32(dst, "dst", src.shape),
-                            src.numel(), _block_status(status), _stream(stream))
+    n = src.numel()
+    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src", n), _i32(dst, "dst", n), n,
+                            _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_ring_copy")
     return st

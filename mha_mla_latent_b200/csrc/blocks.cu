@@ -138,22 +138,32 @@ trim_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_len
   copy_ints(t.refs, refs_in, t.n_blocks, thread, kCluster * kThreads);
   cluster_sync();
   const int n = t.B * t.C;   // at most 2^30
-  for (int i = thread; i < n; i += kCluster * kThreads) {
-    const int b = i / t.C;
-    const int32_t e = t.in[i];
-    const long long t0 = (long long)(i - b * t.C) * kBT, L = seq_lens[b];
-    if (!length_ok(t, (int)L)) {
-      flag(t.status, MLA_DEVERR_SEQ_LEN);
-    } else {
-      const int id = entry(t, e);
-      const bool keep = t0 < min((long long)n_sink, L) || (window > 0 && t0 < L && t0 + kBT > L - window);
-      if (!keep) {
-        if (id >= 0) atomicSub(t.refs + id, 1);
-        t.out[i] = -1;
-        continue;
-      }
+  constexpr int kBatch = 8;  // entries and lengths in flight
+  for (int i0 = thread; i0 < n; i0 += kBatch * kCluster * kThreads) {
+    int32_t e[kBatch], len[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = min(i0 + k * kCluster * kThreads, n - 1);
+      e[k] = t.in[i];
+      len[k] = __ldg(seq_lens + i / t.C);
     }
-    if (t.out != t.in) t.out[i] = e;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kCluster * kThreads;
+      if (i >= n) break;
+      const long long t0 = (long long)(i % t.C) * kBT, L = len[k];
+      if (!length_ok(t, len[k])) {
+        flag(t.status, MLA_DEVERR_SEQ_LEN);
+      } else {
+        const int id = entry(t, e[k]);
+        const bool keep = t0 < min((long long)n_sink, L) || (window > 0 && t0 < L && t0 + kBT > L - window);
+        if (!keep) {
+          if (id >= 0) atomicSub(t.refs + id, 1);
+          e[k] = -1;
+        }
+      }
+      t.out[i] = e[k];
+    }
   }
 }
 

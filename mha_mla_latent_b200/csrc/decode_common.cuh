@@ -226,13 +226,14 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
 // another costs a worker about that long, so workers with a sequence's end and the next one's
 // start get fewer.
 struct SeqUnits {
-  int len = 0, n = 0;   // visible tokens, units with the cost (0 for an empty sequence)
+  int L = 0, len = 0, n = 0;   // length, visible tokens, units with the cost (0 for an empty sequence)
 };
 __device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, int cost, MlaWindow win) {
   SeqUnits s;
   if (b >= B) return s;
   const int L = __ldg(seq_lens + b);
   if (L <= 0 || L > T_cap) return s;
+  s.L = L;
   s.len = unit_span(L, 1, tile, win).len;
   s.n = (s.len + tile - 1) / tile + cost;
   return s;

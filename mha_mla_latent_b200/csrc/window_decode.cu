@@ -87,29 +87,30 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Walk over a worker's pieces in tiles: x is the tile's first token in the sequence's span.  A
-// piece is (sequence, first token, end, slot).
+// piece is (sequence, first token, end, the sequence's length); its slot is slot0 + its number.
 struct Walk {
   const Args* a;
   const int4* list;   // the first kPieces pieces; the others at their slots, which are consecutive
-  int pc, end, slot, b, x, x0, x1;
+  int pc, end, slot0, b, x, x0, x1, len;
   Span span;
-  __device__ void init(const Args* args, const int4* pieces, int n) {
+  __device__ void init(const Args* args, const int4* pieces, int n, int first_slot) {
     a = args;
     list = pieces;
+    slot0 = first_slot;
     pc = 0;
     end = n;
     if (pc < end) load();
   }
   __device__ void load() {
-    const int4 p = pc < kPieces ? list[pc] : a->pieces[list[0].w + pc];
-    b = p.x; x0 = p.y; x1 = p.z; slot = p.w; x = x0;
-    span = unit_span(__ldg(a->seq_lens + b), 1, kUnit, a->win);
+    const int4 p = pc < kPieces ? list[pc] : a->pieces[slot0 + pc];
+    b = p.x; x0 = p.y; x1 = p.z; len = p.w; x = x0;
+    span = unit_span(len, 1, kUnit, a->win);
   }
   __device__ bool valid() const { return pc < end; }
   __device__ bool first() const { return x == x0; }
   __device__ bool last() const { return x + kT >= x1; }
   __device__ int rows() const { return min(kT, x1 - x); }
-  __device__ int seq_len() const { return __ldg(a->seq_lens + b); }
+  __device__ int slot() const { return slot0 + pc; }
   __device__ int units() const { return x1 - x > kUnit ? 2 : 1; }
   __device__ int token(int unit) const { return span.token(x + unit * kUnit); }
   // Every row of the tile holds a visible token.
@@ -164,7 +165,7 @@ template <> __device__ __forceinline__ void tmem_ld<32>(uint32_t ta, uint32_t (&
 
 // The worker's pieces: list[0 .. min(n, kPieces)), the others in the workspace; returns n.  Whole
 // CTA.  Reads the lengths, which were complete before the kernel ahead of this one started.
-__device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, int* s_warp, int* s_misc) {
+__device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, int* slot0, int* s_warp, int* s_misc) {
   const int tid = threadIdx.x, nt = blockDim.x;
   if (tid == 0) { s_misc[0] = INT_MAX; s_misc[1] = 0; }
   int total = 0;
@@ -197,13 +198,14 @@ __device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, i
     __syncthreads();
     if (in) {
       const int k = ne - s_misc[0];
-      const int4 p = make_int4(base + tid, max(0, w0 - first) * kUnit, min(mine.len, (w1 - first) * kUnit), w + ne);
+      const int4 p = make_int4(base + tid, max(0, w0 - first) * kUnit, min(mine.len, (w1 - first) * kUnit), mine.L);
       if (k < kPieces) list[k] = p;
-      else a.pieces[p.w] = p;
+      else a.pieces[w + ne] = p;
       atomicMax(s_misc + 1, k + 1);
     }
   }
   __syncthreads();
+  *slot0 = w + s_misc[0];
   return s_misc[1];
 }
 
@@ -260,7 +262,8 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
   // done: lengths and cache can be read now, only the absorbed queries must be waited for.
   __shared__ int s_warp[32], s_misc[2];
   int4* list = reinterpret_cast<int4*>(smem + a.off_list);
-  const int n_pieces = worker_pieces(a, blockIdx.x, list, s_warp, s_misc);
+  int slot0 = 0;
+  const int n_pieces = worker_pieces(a, blockIdx.x, list, &slot0, s_warp, s_misc);
   // Registers with a quantised latent: 512 threads x 128 = 65536 = 128 x (88 + 168 + 168 + 88).
   if (warp < 4) {
   if (QB) setmaxnreg_dec<88>();
@@ -275,7 +278,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       return lc.pb * lc.cap + lc.pt;
     };
     Walk wc, wk, wq;
-    wc.init(&a, list, n_pieces);
+    wc.init(&a, list, n_pieces, slot0);
     wk = wc;
     wq = wc;
     int c_row[2] = {0, 0}, k_row[2] = {0, 0};
@@ -385,7 +388,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
     const int n_blk = (a.dcp + 127) / 128;   // blocks of 128 latent columns
     Walk i1, i2;                             // tiles whose S, and whose O, is issued next
-    i1.init(&a, list, n_pieces);
+    i1.init(&a, list, n_pieces, slot0);
     i2 = i1;
     // S(n1) is issued in batches, the latent product with the first kpb key boxes, then kpb key
     // boxes at a time (all of them in one batch where the ring holds them): a batch costs about
@@ -506,7 +509,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
     if (QB) setmaxnreg_dec<88>();
     const int r = (warp - 12) * 32 + lane;
     Walk it;
-    it.init(&a, list, n_pieces);
+    it.init(&a, list, n_pieces, slot0);
     // Where a row's values come from is asked for ahead of its tile, so that no load is waited
     // for in the loop: the cache row (a look into the block table) two tiles, the group scales
     // and the ring tag a tile ahead.
@@ -532,7 +535,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         if (k < a.d_c / 32) o.sc[k] = __ldg(sp + k);
       if (a.cache.c_resid) {
         o.pos = t.token(r >> 6) + (r & 63);
-        if (o.pos >= t.seq_len() - MLA_RESID_WINDOW) {
+        if (o.pos >= t.len - MLA_RESID_WINDOW) {
           o.slot = (size_t)t.b * MLA_RESID_WINDOW + (o.pos & (MLA_RESID_WINDOW - 1));
           o.tag = __ldg(a.cache.resid_pos + o.slot);
         }
@@ -627,7 +630,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       if (lane == 0) mbar_arrive(bar(i));
     };
     Walk it;
-    it.init(&a, list, n_pieces);
+    it.init(&a, list, n_pieces, slot0);
     int n = 0, u = 0;                        // tiles and pieces of the CTA
     RingPos rc;                              // latent tiles
     float m[N], l[N];
@@ -643,7 +646,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           fail = u > 0 && !warp_wait(kQEmpty, (u - 1) & 1);
           if (!fail && lane < a.H) {
             const float4* src = reinterpret_cast<const float4*>(a.qrope + ((size_t)it.b * a.H + lane) * 8);
-            const float4 x = __ldg(src), y = __ldg(src + 1);
+            const float4 x = __ldcg(src), y = __ldcg(src + 1);
             const int g = lane / a.G, kb = g >> 3;
             const int col = a.kr_rows == N ? 0 : (kb * 8 * a.G) & ~15;
             *reinterpret_cast<uint4*>(smem + a.off_qr + kb * a.kr_rows * 128 + sw128(lane - col, g & 7)) =
@@ -793,7 +796,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         float w0[HN], w1[HN];   // weight 0: the stream's columns may be stale
 #pragma unroll
         for (int e = 0; e < HN; ++e) { w0[e] = wts[HN * s + e]; w1[e] = wts[32 + HN * s + e]; }
-        float* dst = a.opart + ((size_t)it.slot * a.H + HN * s) * a.d_c + r;
+        float* dst = a.opart + ((size_t)it.slot() * a.H + HN * s) * a.d_c + r;
 #pragma unroll 1
         for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk, dst += 128) {
           uint32_t o0[HN], o1[HN];
@@ -818,7 +821,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
             sum0 += l0[k * 32 + r];
             sum1 += l0[(4 + k) * 32 + r];
           }
-          *reinterpret_cast<float2*>(a.mlpart + ((size_t)r * a.P + it.slot) * 2) = make_float2(M, wts[r] * sum0 + wts[32 + r] * sum1);
+          *reinterpret_cast<float2*>(a.mlpart + ((size_t)r * a.P + it.slot()) * 2) = make_float2(M, wts[r] * sum0 + wts[32 + r] * sum1);
         }
         tc_fence_before();
         arrive(kOEmpty);
@@ -932,9 +935,9 @@ __global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) 
 // out[row][d] = sum_c (sum_j 2^(m_j - M) O_j[c] / sum_j 2^(m_j - M) l_j) W_uv[g][c][d] for 16 rows
 // (sequence, query head of KV head g) and 64 columns per CTA.  Latency bound: the W_uv chunk and
 // the pieces' slots are fetched and counted before the attention kernel is waited for, and a
-// warp has the partials of up to four pieces in flight.  The merged latent goes into the warp
+// warp, which merges one row, has the partials of four pieces in flight.  The merged latent goes into the warp
 // products as two bf16 halves, so its rounding does not count.
-constexpr int kMRows = 16, kMCols = 64, kMThreads = 256;
+constexpr int kMRows = 16, kMCols = 64, kMThreads = 512, kMBatch = 4;
 struct MergeArgs {
   int B, H, G, n_kv, d_c, d_h, P, workers, T_cap, cost;
   MlaWindow win;
@@ -984,9 +987,8 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
   const int busy = busy_workers(total, a.workers);
   pdl_wait();   // the partials
   pdl_trigger();
-#pragma unroll 1
-  for (int j = 0; j < kMRows / 8; ++j) {
-    const int r = warp + 8 * j, row = row0 + r;
+  {   // a row per warp
+    const int r = warp, row = row0 + r;
     float acc[8] = {};   // columns 4 lane + 0..3 and 128 + 4 lane + 0..3
     if (row < rows_g) {
       const int b = row / a.G, h = g * a.G + row % a.G;
@@ -1001,38 +1003,36 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
       const float* op = a.opart + ((size_t)first * a.H + h) * a.d_c + 4 * lane;
       const size_t step = (size_t)a.H * a.d_c;
       const bool c0 = 4 * lane < a.d_c, c1 = 128 + 4 * lane < a.d_c;
-      float2 mine = lane < np ? __ldg(ml + lane) : make_float2(-INFINITY, 0.f);
+      float4 v[kMBatch][2];
+      auto fetch = [&](int k) {   // pieces k .. k + kMBatch - 1
+#pragma unroll
+        for (int i = 0; i < kMBatch; ++i) {
+          v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float* p = op + (size_t)(k + i) * step;
+          if (k + i < np && c0) v[i][0] = __ldcg(reinterpret_cast<const float4*>(p));
+          if (k + i < np && c1) v[i][1] = __ldcg(reinterpret_cast<const float4*>(p + 128));
+        }
+      };
+      fetch(0);   // in the same round trip as the maxima
+      float2 mine = lane < np ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
       float M = mine.x;
-      for (int k = lane + 32; k < np; k += 32) M = fmaxf(M, __ldg(ml + k).x);
+      for (int k = lane + 32; k < np; k += 32) M = fmaxf(M, __ldcg(ml + k).x);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float den = 0.f;
+      float wt = 0.f, den = 0.f;
 #pragma unroll 1
-      for (int k0 = 0; k0 < np; k0 += 32) {
-        if (k0 > 0) mine = k0 + lane < np ? __ldg(ml + k0 + lane) : make_float2(-INFINITY, 0.f);
-        const float wt = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
-        den += wt * mine.y;
-        const int n = min(32, np - k0);
-#pragma unroll 1
-        for (int k = 0; k < n; k += 4) {
-          float4 v[4][2];
+      for (int k = 0; k < np; k += kMBatch) {
+        if ((k & 31) == 0) {   // the weights of pieces k .. k + 31, one per lane
+          if (k > 0) mine = k + lane < np ? __ldcg(ml + k + lane) : make_float2(-INFINITY, 0.f);
+          wt = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
+          den += wt * mine.y;
+        }
+        if (k > 0) fetch(k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k + i < n) {
-              const float* p = op + (size_t)(k0 + k + i) * step;
-              if (c0) v[i][0] = __ldg(reinterpret_cast<const float4*>(p));
-              if (c1) v[i][1] = __ldg(reinterpret_cast<const float4*>(p + 128));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float wk = __shfl_sync(0xffffffffu, wt, (k + i) & 31);
-            if (k + i < n) {
-              acc[0] += wk * v[i][0].x; acc[1] += wk * v[i][0].y; acc[2] += wk * v[i][0].z; acc[3] += wk * v[i][0].w;
-              acc[4] += wk * v[i][1].x; acc[5] += wk * v[i][1].y; acc[6] += wk * v[i][1].z; acc[7] += wk * v[i][1].w;
-            }
-          }
+        for (int i = 0; i < kMBatch; ++i) {
+          const float wk = __shfl_sync(0xffffffffu, wt, (k + i) & 31);   // 0 past the last piece
+          acc[0] += wk * v[i][0].x; acc[1] += wk * v[i][0].y; acc[2] += wk * v[i][0].z; acc[3] += wk * v[i][0].w;
+          acc[4] += wk * v[i][1].x; acc[5] += wk * v[i][1].y; acc[6] += wk * v[i][1].z; acc[7] += wk * v[i][1].w;
         }
       }
 #pragma unroll
@@ -1058,6 +1058,7 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
   }
   cp_async_wait_all();
   __syncthreads();
+  if (warp >= kMCols / 8) return;
   const int n0 = 8 * warp;   // this warp's columns
   float ahi[4] = {}, alo[4] = {};
 #pragma unroll 2
