@@ -441,8 +441,10 @@ mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache,
   if ((st = mla_pick_window_kernel(*plan, *cache, &kernel)) != MLA_OK) return st;
   DecodeLayout L = mla_decode_layout(*plan, B, kernel);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  return cuda_status(mla_launch_decode(*plan, *cache, seq_lens, q, B, out, workspace, L, (cudaStream_t)stream,
-                                       window_of(*cache, n_sink, window)));
+  const MlaWindow win = window_of(*cache, n_sink, window);
+  if (plan->opt_kernel == 0 && mla_window_small_pick(*plan, *cache, B, win))
+    return cuda_status(mla_launch_window_small(*plan, *cache, seq_lens, q, B, out, win, (cudaStream_t)stream));
+  return cuda_status(mla_launch_decode(*plan, *cache, seq_lens, q, B, out, workspace, L, (cudaStream_t)stream, win));
 }
 
 mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* cache, const int32_t* seq_lens,

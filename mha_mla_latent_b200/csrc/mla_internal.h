@@ -196,6 +196,12 @@ bool mla_window_decode_capable(const mla_plan& p);
 cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q,
                                      int B, void* out, void* ws, const DecodeLayout& D, MlaWindow win, cudaStream_t s);
 
+// The windowed decode of small problems in one launch (window_small.cu): whether this call is
+// one, and its launch.  It needs no workspace.
+bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win);
+cudaError_t mla_launch_window_small(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q, int B,
+                                    void* out, MlaWindow win, cudaStream_t s);
+
 cudaError_t mla_launch_select_pairs(const mla_config_t& cfg, const void* q, const void* k, int T,
                                     int32_t* pair_idx, float* contrib, cudaStream_t s);
 cudaError_t mla_launch_append(const mla_plan& p, const void* x, const int32_t* seq_idx,
