@@ -41,6 +41,12 @@ LAYERS = {
     "gqa64": dict(H=64, n_kv=32, d_h=64, d_c=128),
     "one_head_r13": dict(H=1, n_kv=1, d_h=64, r=13, d_c=64),
     "nope": dict(H=8, n_kv=8, d_h=32, r=0, d_c=32),
+    # key boxes of 8 KV heads: partly filled ones, two and three query heads per KV head
+    "h24_gqa2": dict(H=24, n_kv=12, d_h=32, d_c=64),
+    "h27_gqa3": dict(H=27, n_kv=9, d_h=48, d_c=32),
+    "h20_dh40": dict(H=20, n_kv=20, d_h=40, d_c=160),
+    "h16_int4": dict(H=16, n_kv=16, d_h=32, d_c=192, cache="int4"),
+    "h32_gqa8_int2": dict(H=32, n_kv=4, d_h=64, d_c=128, cache="int2"),
 }
 WINDOWS = [(0, 1), (1, 1), (3, 5), (64, 64), (65, 63), (0, 128), (4, 200), (130, 300), (5000, 7), (0, 5000)]
 LENS = [1, 700, 0, 64, 65, 200, 513, 2, 331]
@@ -141,7 +147,8 @@ def test_full_window_is_decode():
     plan.close()
 
 
-CHUNK_LAYERS = ["smollm", "llama_dc256", "llama_dc64", "llama_int4", "llama_int4_dc256", "llama_int2", "gqa64"]
+CHUNK_LAYERS = ["smollm", "llama_dc256", "llama_dc64", "llama_dc96", "llama_int4", "llama_int4_dc256", "llama_int2", "gqa64",
+                "h24_gqa2", "h27_gqa3", "h20_dh40", "h32_gqa8_int2"]
 
 
 @pytest.mark.parametrize("Q", [1, 2, 5, 70])
@@ -169,6 +176,159 @@ def test_chunk_window(name, Q):
             for i in sorted({0, Q // 2, Q - 1}):
                 ref = layer.reference(q[b, i], seqs[b], L - Q + i, n_sink, window).numpy()
                 assert_close(got[b, i], ref, "bf16", f"{name} Q {Q} query {i} sinks {n_sink} window {window} length {L}")
+    plan.close()
+
+
+def _exact_layer(cache="same", d_c=32, H=9, n_kv=3, dtype="bf16"):
+    """A layer in which scores are exact: W_uk passes the first d_c NoPE dims of the query to the
+    latent dims, the softmax scale makes a unit of q . c one unit of log2, the RoPE keys are 0."""
+    layer = Layer(dtype=dtype, cache=cache, H=H, n_kv=n_kv, d_h=64, r=4, d_c=d_c, seed=12, scale=float(np.log(2.0)))
+    layer.W_uk = torch.zeros_like(layer.W_uk)
+    for c in range(d_c):
+        layer.W_uk[:, c, c] = 1.0
+    layer.W_uv = torch.zeros_like(layer.W_uv)
+    for c in range(d_c):
+        layer.W_uv[:, c, c] = 1.0
+    return layer
+
+
+def _exact_sequence(layer, L, ramp):
+    """Latent 0 of token t is ramp[t] (the score), the others small whole numbers."""
+    s = layer.sequence(L)
+    g = torch.Generator().manual_seed(5)
+    s["c_kv"] = torch.randint(-4, 5, (L, layer.d_c), generator=g).to(layer.td)
+    s["c_kv"][:, 0] = torch.as_tensor(ramp).to(layer.td)
+    s["c"] = s["c_kv"].double()
+    s["kr"] = torch.zeros_like(s["kr"])
+    return s
+
+
+RAMPS = {
+    "rising": lambda L: np.minimum(np.arange(L), 200),                    # the maximum moves on and on
+    "falling": lambda L: -np.minimum(np.arange(L), 200),
+    "jumps": lambda L: np.where(np.arange(L) % 97 == 50, 96, -128) + np.where(np.arange(L) == L - 3, 120, 0),
+    "first_low": lambda L: np.where(np.arange(L) % 64 == 0, -240, 16),    # far below the rest of its tile
+    "flat": lambda L: np.zeros(L),
+}
+
+
+@pytest.mark.parametrize("ramp", list(RAMPS))
+@pytest.mark.parametrize("kind", ["smollm", "llama", "f32"])
+def test_score_ranges(kind, ramp):
+    """Scores that are whole numbers of log2 units over ranges of up to 368: probabilities are
+    powers of two, sums and products exact in float32, so what is left is the output's rounding
+    (2^-8 of the value, float32: some 2^-20 of the sums) and, where a probability is below 2^-126
+    of the largest, nothing.  Decode over every window kernel, and a chunk."""
+    import mha_mla_latent_b200 as mla
+    layer = _exact_layer(**{"smollm": dict(), "llama": dict(d_c=32, H=32, n_kv=32), "f32": dict(dtype="f32", H=4, n_kv=4)}[kind])
+    lens = [700, 1, 130, 513]
+    B, T_cap = len(lens), 768
+    seqs = [_exact_sequence(layer, L, RAMPS[ramp](L)) for L in lens]
+    q = torch.zeros(B, layer.H, layer.d_h)
+    # dims 2k and 2k + 1 of the kept pairs do not reach the latent: score dim 0 must be a NoPE dim
+    for h in range(layer.H):
+        g = h // (layer.H // layer.n_kv)
+        rope = set(np.stack([2 * layer.pairs[g], 2 * layer.pairs[g] + 1], -1).reshape(-1).tolist())
+        nope = [i for i in range(layer.d_h) if i not in rope]
+        q[:, h, nope[0]] = 1.0
+    q = q.to(layer.td)
+    eps = 2.0 ** -8 if layer.dtype == "bf16" else 2.0 ** -18
+    plan = layer.plan(mla)
+    cache = make_cache(mla, layer, B, T_cap, True)
+    for b, s in enumerate(seqs):
+        store(cache, b, s)
+    for kernel in (0, 1) if kind == "f32" else (0, 1, 3):
+        mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+        for n_sink, window in [(0, 5000), (3, 100), (70, 300)]:
+            got = run_decode(mla, layer, cache, lens, q, n_sink, window, plan).double().cpu()
+            for b, L in enumerate(lens):
+                ref = layer.reference(q[b], seqs[b], L - 1, n_sink, window)
+                worst = ((got[b] - ref).abs() / (ref.abs() * eps + eps / 8)).max().item()
+                assert worst <= 1.0, f"{kind} {ramp} kernel {kernel} sinks {n_sink} window {window} length {L}: {worst}"
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, 0)
+    if layer.dtype == "bf16":
+        Q, use = 5, [0, 2, 3]
+        qc = torch.stack([q[b].unsqueeze(0).expand(Q, -1, -1) for b in use]).contiguous()
+        sub = make_cache(mla, layer, len(use), T_cap, False)
+        for k, b in enumerate(use):
+            store(sub, k, seqs[b])
+        out = torch.empty_like(qc, device="cuda")
+        ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, len(use), Q), dtype=torch.uint8, device="cuda")
+        mla.mla_decode_chunk_window(plan, sub.struct, torch.tensor([lens[b] for b in use], dtype=torch.int32, device="cuda"),
+                                    qc.cuda(), out, ws, 3, 100)
+        assert mla.mla_device_error(plan) == 0
+        for k, b in enumerate(use):
+            for i in range(Q):
+                ref = layer.reference(qc[k, i], seqs[b], lens[b] - Q + i, 3, 100)
+                worst = ((out[k, i].double().cpu() - ref).abs() / (ref.abs() * eps + eps / 8)).max().item()
+                assert worst <= 1.0, f"chunk {kind} {ramp} length {lens[b]} query {i}: {worst}"
+    plan.close()
+
+
+@pytest.mark.parametrize("B,splits", [(100, 1), (700, 0), (300, 2)])
+def test_many_short_sequences(B, splits):
+    """More pieces per worker than its list holds, more sequences than threads, empty ones among them."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=13)
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 200, size=B).tolist()
+    seq = layer.sequence(200)
+    cache = make_cache(mla, layer, B, 256, B != 300, seed=1)
+    for b, L in enumerate(lens):
+        if L:
+            store(cache, b, {k: (v[:L] if torch.is_tensor(v) else v) for k, v in seq.items()} | {"L": L})
+    q = layer.queries(B)
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_SPLITS, splits)
+    got = run_decode(mla, layer, cache, lens, q, 20, 150, plan).double().cpu().numpy()
+    for b in list(range(0, B, B // 12)) + [B - 1]:
+        if lens[b] == 0:
+            assert not got[b].any()
+        else:
+            assert_close(got[b], layer.reference(q[b], seq, lens[b] - 1, 20, 150).numpy(), "bf16", f"{B} {splits} {b}")
+    plan.close()
+
+
+@pytest.mark.parametrize("B,Q,name", [(24, 3, "llama_dc64"), (1, 130, "llama_dc64"), (2, 33, "smollm"), (30, 2, "smollm")])
+def test_chunk_window_unit_shapes(B, Q, name):
+    """Numbers of sequences and queries that make the chunk's units of one, two and four KV heads."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=14)
+    rng = np.random.default_rng(Q)
+    lens = rng.integers(Q, 400, size=B).tolist()
+    seq = layer.sequence(400)
+    cache = make_cache(mla, layer, B, 512, True)
+    for b, L in enumerate(lens):
+        store(cache, b, {k: (v[:L] if torch.is_tensor(v) else v) for k, v in seq.items()} | {"L": L})
+    q = layer.queries(B, Q)
+    plan = layer.plan(mla)
+    out = torch.full_like(q, float("nan"), device="cuda")
+    ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+    mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(), out, ws, 5, 120)
+    assert mla.mla_device_error(plan) == 0
+    got = out.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    for b in {0, B // 2, B - 1}:
+        for i in {0, Q // 2, Q - 1}:
+            ref = layer.reference(q[b, i], seq, lens[b] - Q + i, 5, 120).numpy()
+            assert_close(got[b, i], ref, "bf16", f"{name} {B} {Q} seq {b} query {i}")
+    plan.close()
+
+
+def test_without_launch_overlap():
+    """Plain stream order gives the same bits."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=128, cache="int4", seed=15)
+    lens = [600, 333]
+    cache = make_cache(mla, layer, 2, 640, True)
+    for b, L in enumerate(lens):
+        store(cache, b, layer.sequence(L))
+    q = layer.queries(2)
+    plan = layer.plan(mla)
+    a = run_decode(mla, layer, cache, lens, q, 3, 400, plan)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_OVERLAP_LAUNCH, 0)
+    b = run_decode(mla, layer, cache, lens, q, 3, 400, plan)
+    assert torch.equal(a, b)
     plan.close()
 
 
