@@ -45,7 +45,8 @@ constexpr uint32_t kSlot = 2 * kHalf;     // ring slot: 128 tokens x 64 columns
 // Threads: four warpgroups with a quantised latent (the last one dequantises), else three.
 template <int QB> constexpr int kThreadsOf = QB ? 512 : 384;
 constexpr float kTau = 8.0f;              // lazy-rescale threshold, log2 units
-constexpr uint32_t kCols = 256, kSCol = 0, kOCol = 64;   // S: 2 x 32 columns, O: 2 streams x 2 blocks x 32
+constexpr int kSBufs = 4;                 // S tiles in tensor memory: keys go ahead of their tile's latent
+constexpr uint32_t kCols = 256, kSCol = 0, kOCol = 128;   // S: 4 x 32 columns, O: 2 streams x 2 blocks x 32
 constexpr uint32_t kSmemMax = 232448;
 constexpr int kMaxC = 4, kMaxK = 8, kMaxRaw = 3;
 constexpr int kPieces = 64;               // pieces of a worker kept in shared memory
@@ -53,7 +54,7 @@ constexpr int kPieces = 64;               // pieces of a worker kept in shared m
 struct Args {
   int H, G, d_c, dcp, R, P, T_cap;
   int n_cbox, n_kbox, kr_rows;            // boxes per token row; heads a key box is multiplied with
-  int kpb;                                // key boxes issued together
+  int n_blk;                              // parts of a latent tile: blocks of 128 columns
   int NC, NK, NRAW;                       // latent tiles, key boxes, code tiles in the rings
   int B, workers, cost;                   // cost of a piece, in units (see seq_units)
   MlaWindow win;
@@ -71,8 +72,8 @@ struct Args {
 };
 
 enum {
-  kCFull = 0, kCEmpty = kCFull + kMaxC, kKFull = kCEmpty + kMaxC, kKEmpty = kKFull + kMaxK, kRFull = kKEmpty + kMaxK,
-  kREmpty = kRFull + kMaxRaw, kSFull = kREmpty + kMaxRaw, kSEmpty = kSFull + 2, kPFull = kSEmpty + 2, kODone = kPFull + 2,
+  kCFull = 0, kCEmpty = kCFull + 2 * kMaxC, kKFull = kCEmpty + 2 * kMaxC, kKEmpty = kKFull + kMaxK, kRFull = kKEmpty + kMaxK,
+  kREmpty = kRFull + kMaxRaw, kSFull = kREmpty + kMaxRaw, kSEmpty = kSFull + kSBufs, kPFull = kSEmpty + kSBufs, kODone = kPFull + 2,
   kOEmpty = kODone + 2, kQFull, kQEmpty, kMeet, kDone, kBars
 };
 // Exchange area, floats: per group the tile maxima of its warps [2][4][32] (first row also the
@@ -126,6 +127,27 @@ struct Walk {
   __device__ void next() {
     x += kT;
     if (x >= x1) { ++pc; if (pc < end) load(); }
+  }
+};
+
+// The same walk where only the pieces' ends count.
+struct Tiles {
+  const Walk* w;      // pieces, as of the walk's start
+  int pc, left, n;    // left: tiles of the piece, with this one; n: tiles gone by
+  bool first;
+  __device__ void init(const Walk& walk) { w = &walk; pc = 0; n = 0; load(); }
+  __device__ bool valid() const { return pc < w->end; }
+  __device__ void load() {
+    if (!valid()) return;
+    const int4 p = pc < kPieces ? w->list[pc] : w->a->pieces[w->slot0 + pc];
+    left = (p.z - p.y + kT - 1) / kT;
+    first = true;
+  }
+  __device__ bool last() const { return left == 1; }
+  __device__ void next() {
+    ++n;
+    first = false;
+    if (--left == 0) { ++pc; load(); }
   }
 };
 
@@ -266,181 +288,207 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
   const int n_pieces = worker_pieces(a, blockIdx.x, list, &slot0, s_warp, s_misc);
   // Registers with a quantised latent: 512 threads x 128 = 65536 = 128 x (88 + 168 + 168 + 88).
   if (warp < 4) {
-  if (QB) setmaxnreg_dec<88>();
-  if (warp == 0) {
-    // ============================================================ TMA producer (converged warp, elected lane)
-    // Cursors: latent (or code) tiles, key boxes, queries, whose places free up at different
-    // times.  The cache rows of a tile's units are looked up when the cursor reaches it, not
-    // when its place is free.  Nothing is copied before the absorption is done: copies started
-    // ahead of it slow its few loads down by more than they gain (Llama-shaped layers, us: 47.9
-    // against 47.0 at d_c = 256, 25.5 against 23.8 at d_c = 64).
-    auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
-    auto row_of = [&](const Walk& it, int unit) {
-      const MlaLoc lc = mla_loc(a.cache, it.b, it.token(unit), a.err);   // a unit lies in one block
-      return lc.pb * lc.cap + lc.pt;
-    };
-    Walk wc, wk, wq;
-    wc.init(&a, list, n_pieces, slot0);
-    wk = wc;
-    wq = wc;
-    int c_row[2] = {0, 0}, k_row[2] = {0, 0};
-    auto rows_at = [&](const Walk& it, int (&row)[2]) {
-      row[0] = row_of(it, 0);
-      row[1] = it.units() > 1 ? row_of(it, 1) : row[0];
-    };
-    if (wc.valid()) rows_at(wc, c_row);
-    k_row[0] = c_row[0]; k_row[1] = c_row[1];
-    int nc = 0, nk = 0, kb = 0, tk = 0, u = 0;   // u: query loads issued
-    RingPos rc, rk;
-    const int c_ring = QB ? NRAW : NC;
-    int looks = 0;
-    uint64_t idle = 0;
-    auto load_q = [&]() {
-      if (elect_one()) {
-        mbar_expect_tx(bar(kQFull), (uint32_t)a.n_cbox * a.H * 128u);
-        for (int k = 0; k < a.n_cbox; ++k) tma_load_2d(sb + a.off_q + k * N * 128, &tm_q, bar(kQFull), k * 64, wq.b * a.H);
-      }
-      __syncwarp();
-      ++u;
-      if (++wq.pc < wq.end) wq.load();
-    };
-    bool ok = true;
-    if (wq.valid()) {
-      pdl_wait();
-      load_q();
-    }
-    while (ok && (wc.valid() || wk.valid() || wq.valid())) {
-      bool progress = false;
-      if (wc.valid()) {
-        const int s = rc.slot;
-        if (nc < c_ring || ready((QB ? kREmpty : kCEmpty) + s, rc.parity ^ 1)) {
-          const int units = wc.units();
-          if (elect_one()) {
-            if (QB) {
-              const uint32_t dst = sb + a.off_raw + s * a.raw_stage;
-              mbar_expect_tx(bar(kRFull + s), (uint32_t)units * kUnit * a.code_row);
-              tma_load_2d(dst, &tm_c, bar(kRFull + s), 0, c_row[0]);
-              if (units > 1) tma_load_2d(dst + kUnit * a.code_row, &tm_c, bar(kRFull + s), 0, c_row[1]);
-            } else {
-              const uint32_t dst = sb + a.off_c + s * c_bytes;
-              mbar_expect_tx(bar(kCFull + s), (uint32_t)units * a.n_cbox * kHalf);
-              for (int k = 0; k < a.n_cbox; ++k) {
-                tma_load_2d(dst + k * kSlot, &tm_c, bar(kCFull + s), k * 64, c_row[0]);
-                if (units > 1) tma_load_2d(dst + k * kSlot + kHalf, &tm_c, bar(kCFull + s), k * 64, c_row[1]);
-              }
-            }
+    if (QB) setmaxnreg_dec<88>();
+    if (warp == 0) {
+      // ============================================================ TMA producer (converged warp, elected lane)
+      // Cursors: latent (or code) tiles, key boxes, queries, whose places free up at different
+      // times.  The cache rows of a tile's units are looked up when the cursor reaches it, not
+      // when its place is free.  Nothing is copied before the absorption is done: copies started
+      // ahead of it slow its few loads down by more than they gain (Llama-shaped layers, us: 47.9
+      // against 47.0 at d_c = 256, 25.5 against 23.8 at d_c = 64).
+      auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
+      Walk wc, wk, wq;
+      wc.init(&a, list, n_pieces, slot0);
+      wk = wc;
+      wq = wc;
+      // Cache rows of the next 32 units of a walk's piece, one per lane (a unit lies in one block),
+      // and the two of its tile: one look into the block table per 32 units.
+      struct Rows { int unit0, lane_row, row[2]; } c_at, k_at;
+      auto rows_at = [&](const Walk& it, Rows& o) {
+        const int unit = (it.x - it.x0) / kUnit;
+        if (it.first() || unit + 1 - o.unit0 >= 32) {
+          o.unit0 = unit;
+          const int ux = it.x + lane * kUnit;
+          o.lane_row = 0;
+          if (ux < it.x1) {
+            const MlaLoc lc = mla_loc(a.cache, it.b, it.span.token(ux), a.err);
+            o.lane_row = (int)(lc.pb * lc.cap + lc.pt);
           }
-          __syncwarp();
-          wc.next();
-          rc.next(c_ring);
-          ++nc;
-          if (wc.valid()) rows_at(wc, c_row);
-          progress = true;
         }
-      }
-      while (wk.valid() && tk < nc) {   // keys never run ahead of their tile's latent copy
-        const int s = rk.slot;
-        if (!(nk < NK || ready(kKEmpty + s, rk.parity ^ 1))) break;
-        const int units = wk.units();
+        o.row[0] = __shfl_sync(0xffffffffu, o.lane_row, unit - o.unit0);
+        o.row[1] = __shfl_sync(0xffffffffu, o.lane_row, unit - o.unit0 + 1);
+      };
+      if (wc.valid()) rows_at(wc, c_at);
+      k_at = c_at;
+      int nc = 0, pc = 0, nk = 0, kb = 0, u = 0;   // pc: parts of latent tile nc copied; u: query loads issued
+      RingPos rc, rk;
+      const int c_ring = QB ? NRAW : NC;
+      int looks = 0;
+      uint64_t idle = 0;
+      auto load_q = [&]() {
         if (elect_one()) {
-          mbar_expect_tx(bar(kKFull + s), (uint32_t)units * kHalf);
-          tma_load_2d(sb + a.off_k + s * kSlot, &tm_kr, bar(kKFull + s), kb * 64, k_row[0]);
-          if (units > 1) tma_load_2d(sb + a.off_k + s * kSlot + kHalf, &tm_kr, bar(kKFull + s), kb * 64, k_row[1]);
+          mbar_expect_tx(bar(kQFull), (uint32_t)a.n_cbox * a.H * 128u);
+          for (int k = 0; k < a.n_cbox; ++k) tma_load_2d(sb + a.off_q + k * N * 128, &tm_q, bar(kQFull), k * 64, wq.b * a.H);
         }
         __syncwarp();
-        rk.next(NK);
-        ++nk;
-        if (++kb == a.n_kbox) {
-          kb = 0;
-          ++tk;
-          wk.next();
-          if (wk.valid()) rows_at(wk, k_row);
-        }
-        progress = true;
-      }
-      if (wq.valid() && ready(kQEmpty, (u - 1) & 1)) {
+        ++u;
+        if (++wq.pc < wq.end) wq.load();
+      };
+      bool ok = true;
+      if (wq.valid()) {
+        pdl_wait();
         load_q();
-        progress = true;
       }
-      if (progress) {
-        looks = 0;
-      } else if ((++looks & 63) == 0) {
-        const uint64_t now = globaltimer();
-        if (looks == 64) idle = now;
-        if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
-        ok = __all_sync(0xffffffffu, ok) != 0;
-      }
-    }
-    // every issued copy lands before the CTA exits
-    volatile int never = 0;
-    auto drain = [&](int first, int ring, int issued) {
-      for (int i = max(0, issued - ring); i < issued; ++i) mbar_spin(bar(first + i % ring), (i / ring) & 1, &never, lim);
-    };
-    drain(QB ? kRFull : kCFull, QB ? NRAW : NC, nc);
-    drain(kKFull, NK, nk);
-    if (*abort_flag && u > 0) {   // the queries' copy (its barrier may still miss the RoPE rows: wait a moment instead)
-      const uint64_t t0 = globaltimer();
-      while (!mbar_test(bar(kQFull), (u - 1) & 1) && globaltimer() - t0 < 1000000ull) {}
-    }
-  } else if (warp == 1) {
-    // ============================================================ MMA issuer (converged warp, elected lane)
-    const uint32_t id_s = idesc_bf16_f32(kT, N, false, false), id_k = idesc_bf16_f32(kT, a.kr_rows, false, false);
-    const uint32_t id_o = idesc_bf16_f32(kT, N, true, true);
-    const uint64_t desc_q = smem_desc(sb + a.off_q, 16, 1024, kLayoutSW128);
-    const uint64_t desc_qr = smem_desc(sb + a.off_qr, 16, 1024, kLayoutSW128);
-    auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
-    const int n_blk = (a.dcp + 127) / 128;   // blocks of 128 latent columns
-    Walk i1, i2;                             // tiles whose S, and whose O, is issued next
-    i1.init(&a, list, n_pieces, slot0);
-    i2 = i1;
-    // S(n1) is issued in batches, the latent product with the first kpb key boxes, then kpb key
-    // boxes at a time (all of them in one batch where the ring holds them): a batch costs about
-    // 200 cycles before its first product starts
-    int n1 = 0, kb1 = 0, n2 = 0, u1 = 0, u2 = 0;   // kb1: key boxes of S(n1) issued
-    RingPos r1, r2, rk;                            // latent tiles of S and of O, key boxes
-    bool ok = true;
-    int looks = 0;
-    uint64_t idle = 0;
-    while (ok && i2.valid()) {
-      bool progress = false;
-      if (i1.valid()) {
-        const int s = n1 & 1, take = min(a.kpb, a.n_kbox - kb1);
-        bool go = kb1 > 0 || ((n1 < 2 || ready(kSEmpty + s, ((n1 >> 1) - 1) & 1)) &&
-                              ready(kCFull + r1.slot, r1.parity) && (!i1.first() || ready(kQFull, u1 & 1)));
-        RingPos rt = rk;
-        for (int k = 0; go && k < take; ++k) {
-          go = ready(kKFull + rt.slot, rt.parity);
-          rt.next(NK);
-        }
-        if (go) {
-          tc_fence_after();
-          const bool done = kb1 + take == a.n_kbox;
-          if (elect_one()) {
-            const uint32_t d0 = tmem + kSCol + s * 32;
-            if (kb1 == 0) {
-              uint64_t da = smem_desc(sb + a.off_c + r1.slot * c_bytes, 16, 1024, kLayoutSW128), db = desc_q;
-              for (int k = 0; k < a.n_cbox; ++k) {   // a box of 64 columns is four steps
-                tc_mma_bf16(d0, da, db, id_s, k > 0);
-                tc_mma_bf16(d0, da + 2, db + 2, id_s, 1);
-                tc_mma_bf16(d0, da + 4, db + 4, id_s, 1);
-                tc_mma_bf16(d0, da + 6, db + 6, id_s, 1);
-                da += kSlot >> 4;
-                db += (N * 128) >> 4;
+      while (ok && (wc.valid() || wk.valid() || wq.valid())) {
+        bool progress = false;
+        if (wc.valid()) {
+          const int s = rc.slot;
+          if (nc < c_ring || ready(QB ? kREmpty + s : kCEmpty + 2 * s + pc, rc.parity ^ 1)) {
+            const int units = wc.units(), k1 = min(2 * pc + 2, a.n_cbox);
+            if (elect_one()) {
+              if (QB) {
+                const uint32_t dst = sb + a.off_raw + s * a.raw_stage;
+                mbar_expect_tx(bar(kRFull + s), (uint32_t)units * kUnit * a.code_row);
+                tma_load_2d(dst, &tm_c, bar(kRFull + s), 0, c_at.row[0]);
+                if (units > 1) tma_load_2d(dst + kUnit * a.code_row, &tm_c, bar(kRFull + s), 0, c_at.row[1]);
+              } else {
+                const uint32_t dst = sb + a.off_c + s * c_bytes;
+                const uint32_t full = bar(kCFull + 2 * s + pc);
+                mbar_expect_tx(full, (uint32_t)(units * (k1 - 2 * pc)) * kHalf);
+                for (int k = 2 * pc; k < k1; ++k) {
+                  tma_load_2d(dst + k * kSlot, &tm_c, full, k * 64, c_at.row[0]);
+                  if (units > 1) tma_load_2d(dst + k * kSlot + kHalf, &tm_c, full, k * 64, c_at.row[1]);
+                }
               }
             }
-            for (int j = 0; j < take; ++j) {
-              // KV heads 8 kb .. 8 kb + 7: query heads from col on
-              const int kb = kb1 + j, slot = rk.slot;
-              const uint32_t d = d0 + (a.kr_rows == N ? 0 : (kb * 8 * a.G) & ~15);
-              const uint64_t da = smem_desc(sb + a.off_k + slot * kSlot, 16, 1024, kLayoutSW128);
-              const uint64_t db = desc_qr + (uint32_t)kb * (a.kr_rows * 128u >> 4);
-              const int steps = min(4, (a.R - kb * 64 + 15) / 16);
-              tc_mma_bf16(d, da, db, id_k, 1);
-              if (steps > 1) tc_mma_bf16(d, da + 2, db + 2, id_k, 1);
-              if (steps > 2) tc_mma_bf16(d, da + 4, db + 4, id_k, 1);
-              if (steps > 3) tc_mma_bf16(d, da + 6, db + 6, id_k, 1);
-              tc_commit(bar(kKEmpty + slot));
-              rk.next(NK);
+            __syncwarp();
+            if (QB || ++pc == a.n_blk) {
+              pc = 0;
+              wc.next();
+              rc.next(c_ring);
+              ++nc;
+              if (wc.valid()) rows_at(wc, c_at);
+            }
+            progress = true;
+          }
+        }
+        while (wk.valid()) {
+          const int s = rk.slot;
+          if (!(nk < NK || ready(kKEmpty + s, rk.parity ^ 1))) break;
+          const int units = wk.units();
+          if (elect_one()) {
+            mbar_expect_tx(bar(kKFull + s), (uint32_t)units * kHalf);
+            tma_load_2d(sb + a.off_k + s * kSlot, &tm_kr, bar(kKFull + s), kb * 64, k_at.row[0]);
+            if (units > 1) tma_load_2d(sb + a.off_k + s * kSlot + kHalf, &tm_kr, bar(kKFull + s), kb * 64, k_at.row[1]);
+          }
+          __syncwarp();
+          rk.next(NK);
+          ++nk;
+          if (++kb == a.n_kbox) {
+            kb = 0;
+            wk.next();
+            if (wk.valid()) rows_at(wk, k_at);
+          }
+          progress = true;
+        }
+        if (wq.valid() && ready(kQEmpty, (u - 1) & 1)) {
+          load_q();
+          progress = true;
+        }
+        if (progress) {
+          looks = 0;
+        } else if ((++looks & 63) == 0) {
+          const uint64_t now = globaltimer();
+          if (looks == 64) idle = now;
+          if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+          ok = __all_sync(0xffffffffu, ok) != 0;
+        }
+      }
+      // every issued copy lands before the CTA exits
+      volatile int never = 0;
+      auto drain = [&](int first, int ring, int issued) {
+        for (int i = max(0, issued - ring); i < issued; ++i) mbar_spin(bar(first + i % ring), (i / ring) & 1, &never, lim);
+      };
+      if (QB) drain(kRFull, NRAW, nc);
+      for (int i = max(0, nc - NC); !QB && i < nc + (pc > 0); ++i)
+        for (int m = 0; m < (i < nc ? a.n_blk : pc); ++m) mbar_spin(bar(kCFull + 2 * (i % NC) + m), (i / NC) & 1, &never, lim);
+      drain(kKFull, NK, nk);
+      if (*abort_flag && u > 0) {   // the queries' copy (its barrier may still miss the RoPE rows: wait a moment instead)
+        const uint64_t t0 = globaltimer();
+        while (!mbar_test(bar(kQFull), (u - 1) & 1) && globaltimer() - t0 < 1000000ull) {}
+      }
+    } else if (warp == 1) {
+      // ============================================================ MMA issuer (converged warp, elected lane)
+      const uint32_t id_s = idesc_bf16_f32(kT, N, false, false), id_k = idesc_bf16_f32(kT, a.kr_rows, false, false);
+      const uint32_t id_o = idesc_bf16_f32(kT, N, true, true);
+      const uint64_t desc_q = smem_desc(sb + a.off_q, 16, 1024, kLayoutSW128);
+      const uint64_t desc_qr = smem_desc(sb + a.off_qr, 16, 1024, kLayoutSW128);
+      auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
+      Walk i2;                // the tile whose O is issued next
+      i2.init(&a, list, n_pieces, slot0);
+      const Walk start = i2;
+      Tiles ik, i1;           // the tiles whose key product, and whose latent product, is issued next
+      ik.init(start);
+      i1.init(start);
+      // S is the sum of the key product, which goes first, and the latent product.  The keys of a
+      // tile wait for its place in tensor memory only and so leave their ring early, most of them
+      // while the tile's latent is still being copied.
+      int kb = 0, m1 = 0, uk = 0, n2 = 0, u2 = 0;   // key boxes of ik, latent parts of i1 issued; pieces begun, finished
+      RingPos r1, r2, rk;                           // latent tiles of S and of O, key boxes
+      bool ok = true;
+      int looks = 0;
+      uint64_t idle = 0;
+      while (ok && i2.valid()) {
+        bool progress = false;
+        // O(n2): its P, and for a stream's first tile of a piece the accumulators read out
+        if (n2 < i1.n && ready(kPFull + (n2 & 1), (n2 >> 1) & 1)) {
+          const bool fresh = i2.x - i2.x0 < 2 * kT;   // the piece's first or second tile: its stream starts
+          if (!fresh || u2 == 0 || ready(kOEmpty, (u2 - 1) & 1)) {
+            tc_fence_after();
+            const int s = n2 & 1;
+            if (elect_one()) {
+              const uint64_t dp = smem_desc(sb + a.off_p + s * kPBytes, 16, 8 * kPRow, kPLayout);
+              const uint64_t dc = smem_desc(sb + a.off_c + r2.slot * c_bytes, kSlot, 1024, kLayoutSW128);
+              const int steps = (i2.rows() + 15) / 16;
+              for (int m = 0; m < a.n_blk; ++m) {
+                const uint32_t d = tmem + kOCol + s * 64 + m * 32;
+                const uint64_t dm = dc + (uint32_t)m * (2 * kSlot >> 4);
+                if (steps == kT / 16) {
+                  tc_mma_bf16(d, dm, dp, id_o, !fresh);
+  #pragma unroll
+                  for (int k = 1; k < kT / 16; ++k) tc_mma_bf16(d, dm + 128 * k, dp + k * (16 * kPRow >> 4), id_o, 1);
+                } else {
+                  for (int k = 0; k < steps; ++k)
+                    tc_mma_bf16(d, dm + 128u * k, dp + (uint32_t)k * (16 * kPRow >> 4), id_o, !fresh || k > 0);
+                }
+                tc_commit(bar(kCEmpty + 2 * r2.slot + m));
+              }
+              tc_commit(bar(kODone + s));
+            }
+            __syncwarp();
+            if (i2.last()) ++u2;
+            i2.next();
+            r2.next(NC);
+            ++n2;
+            progress = true;
+          }
+        }
+        // latent parts of S(i1)
+        if (i1.n < ik.n && ready(kCFull + 2 * r1.slot + m1, r1.parity)) {
+          tc_fence_after();
+          const int s = i1.n & (kSBufs - 1);
+          const bool done = m1 + 1 == a.n_blk;
+          if (elect_one()) {
+            const uint32_t d = tmem + kSCol + s * 32;
+            uint64_t da = smem_desc(sb + a.off_c + r1.slot * c_bytes + m1 * 2 * kSlot, 16, 1024, kLayoutSW128);
+            uint64_t db = desc_q + (uint32_t)m1 * (2 * N * 128 >> 4);
+            for (int k = 2 * m1; k < min(2 * m1 + 2, a.n_cbox); ++k) {   // a box of 64 columns is four steps
+              tc_mma_bf16(d, da, db, id_s, 1);
+              tc_mma_bf16(d, da + 2, db + 2, id_s, 1);
+              tc_mma_bf16(d, da + 4, db + 4, id_s, 1);
+              tc_mma_bf16(d, da + 6, db + 6, id_s, 1);
+              da += kSlot >> 4;
+              db += (N * 128) >> 4;
             }
             if (done) {
               tc_commit(bar(kSFull + s));
@@ -448,65 +496,69 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
             }
           }
           __syncwarp();
-          rk = rt;
-          kb1 += take;
           if (done) {
-            kb1 = 0;
+            m1 = 0;
             r1.next(NC);
-            if (i1.last()) ++u1;
             i1.next();
-            ++n1;
+          } else {
+            ++m1;
           }
           progress = true;
         }
-      }
-      // O(n2): its P, and for a stream's first tile of a piece the accumulators read out
-      if (n2 < n1 && ready(kPFull + (n2 & 1), (n2 >> 1) & 1)) {
-        const bool fresh = i2.x - i2.x0 < 2 * kT;   // the piece's first or second tile: its stream starts
-        if (!fresh || u2 == 0 || ready(kOEmpty, (u2 - 1) & 1)) {
-          tc_fence_after();
-          const int s = n2 & 1;
-          if (elect_one()) {
-            const uint64_t dp = smem_desc(sb + a.off_p + s * kPBytes, 16, 8 * kPRow, kPLayout);
-            const uint64_t dc = smem_desc(sb + a.off_c + r2.slot * c_bytes, kSlot, 1024, kLayoutSW128);
-            const int steps = (i2.rows() + 15) / 16;
-            for (int m = 0; m < n_blk; ++m) {
-              const uint32_t d = tmem + kOCol + s * 64 + m * 32;
-              const uint64_t dm = dc + (uint32_t)m * (2 * kSlot >> 4);
-              if (steps == kT / 16) {
-                tc_mma_bf16(d, dm, dp, id_o, !fresh);
-#pragma unroll
-                for (int k = 1; k < kT / 16; ++k) tc_mma_bf16(d, dm + 128 * k, dp + k * (16 * kPRow >> 4), id_o, 1);
-              } else {
-                for (int k = 0; k < steps; ++k)
-                  tc_mma_bf16(d, dm + 128u * k, dp + (uint32_t)k * (16 * kPRow >> 4), id_o, !fresh || k > 0);
+        // key boxes of S(ik), as many as are there
+        if (ik.valid() && (kb > 0 || ((ik.n < kSBufs || ready(kSEmpty + (ik.n & (kSBufs - 1)), (ik.n / kSBufs - 1) & 1)) &&
+                                      (!ik.first || ready(kQFull, uk & 1))))) {
+          int take = 0;
+          RingPos rt = rk;
+          while (take < a.n_kbox - kb && ready(kKFull + rt.slot, rt.parity)) {
+            ++take;
+            rt.next(NK);
+          }
+          if (take > 0) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t d0 = tmem + kSCol + (ik.n & (kSBufs - 1)) * 32;
+              for (int j = 0; j < take; ++j, ++kb) {
+                // KV heads 8 kb .. 8 kb + 7: query heads from col on
+                const uint32_t col = a.kr_rows == N ? 0 : (kb * 8 * a.G) & ~15;
+                const bool more = a.kr_rows == N ? kb > 0 : kb > 0 && col == (uint32_t)(((kb - 1) * 8 * a.G) & ~15);   // columns begun
+                const uint64_t da = smem_desc(sb + a.off_k + rk.slot * kSlot, 16, 1024, kLayoutSW128);
+                const uint64_t db = desc_qr + (uint32_t)kb * (a.kr_rows * 128u >> 4);
+                const int steps = min(4, (a.R - kb * 64 + 15) / 16);
+                tc_mma_bf16(d0 + col, da, db, id_k, more);
+                if (steps > 1) tc_mma_bf16(d0 + col, da + 2, db + 2, id_k, 1);
+                if (steps > 2) tc_mma_bf16(d0 + col, da + 4, db + 4, id_k, 1);
+                if (steps > 3) tc_mma_bf16(d0 + col, da + 6, db + 6, id_k, 1);
+                tc_commit(bar(kKEmpty + rk.slot));
+                rk.next(NK);
               }
+              kb -= take;
             }
-            tc_commit(bar(kCEmpty + r2.slot));
-            tc_commit(bar(kODone + s));
+            __syncwarp();
+            rk = rt;
+            kb += take;
+            if (kb == a.n_kbox) {
+              kb = 0;
+              if (ik.first) ++uk;
+              ik.next();
+            }
+            progress = true;
           }
-          __syncwarp();
-          if (i2.last()) ++u2;
-          i2.next();
-          r2.next(NC);
-          ++n2;
-          progress = true;
+        }
+        if (progress) {
+          looks = 0;
+        } else if ((++looks & 63) == 0) {
+          const uint64_t now = globaltimer();
+          if (looks == 64) idle = now;
+          if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+          ok = __all_sync(0xffffffffu, ok) != 0;
         }
       }
-      if (progress) {
-        looks = 0;
-      } else if ((++looks & 63) == 0) {
-        const uint64_t now = globaltimer();
-        if (looks == 64) idle = now;
-        if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
-        ok = __all_sync(0xffffffffu, ok) != 0;
-      }
-    }
-    if (elect_one()) tc_commit(bar(kDone));   // whatever was issued has finished before tensor memory is freed
-    __syncwarp();
-    volatile int never = 0;
-    mbar_spin(bar(kDone), 0, &never, lim);
-  }   // (warps 2 and 3 idle)
+      if (elect_one()) tc_commit(bar(kDone));   // whatever was issued has finished before tensor memory is freed
+      __syncwarp();
+      volatile int never = 0;
+      mbar_spin(bar(kDone), 0, &never, lim);
+    }   // (warps 2 and 3 idle)
   } else if (QB != 0 && warp >= 12) {
     // ============================================================ dequantisation (a token row per thread)
     if (QB) setmaxnreg_dec<88>();
@@ -557,60 +609,67 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       if (w2.valid()) w2.next();
       const long long row2 = cache_row(w2);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(kRFull + rs), rr.parity, abort_flag, lim));
-      if (ok && n >= NC) ok = __all_sync(0xffffffffu, mbar_wait(bar(kCEmpty + cs), rc.parity ^ 1, abort_flag, lim));
       if (!ok) break;
       uint8_t* C = smem + a.off_c + cs * c_bytes;
       auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4*>(C + (chunk >> 3) * kSlot + sw128(r, chunk)) = v; };
-      if (cur.live && cur.tag >= 0 && cur.tag == cur.pos) {   // one of the window's unquantised tokens
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) + cur.slot * a.d_c);
-        for (int c = 0; c < a.d_c / 8; ++c) put(c, __ldg(src + c));
-      } else if (cur.live) {
-        const uint8_t* codes = smem + a.off_raw + rs * a.raw_stage + r * a.code_row;
-        // (a rolled loop: unrolled, the roles' code no longer fits the instruction caches)
-        uint32_t scw[4];
+      const bool kept = cur.live && cur.tag >= 0 && cur.tag == cur.pos;   // one of the window's unquantised tokens
+      const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) + cur.slot * a.d_c);
+      const uint8_t* codes = smem + a.off_raw + rs * a.raw_stage + r * a.code_row;
+      uint32_t scw[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) scw[k] = cur.sc[2 * k] | (uint32_t)cur.sc[2 * k + 1] << 16;
+      for (int k = 0; k < 4; ++k) scw[k] = cur.sc[2 * k] | (uint32_t)cur.sc[2 * k + 1] << 16;
 #pragma unroll 1
-        for (int g = 0; g < a.d_c / 32; ++g) {
-          // An offset code u = code + top sits in the mantissa of 1.0 from bit 23 - QB on: the
-          // float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at
-          // most QB + 11 bits), rounded once to bf16, the products' operand type.
-          constexpr uint32_t kTop = 1u << (QB ? QB - 1 : 0), kMask = (2 * kTop - 1) << (23 - QB);
-          constexpr uint32_t kOne = 0x3F800000u ^ (kTop << (23 - QB));
-          const float sv = __half2float(__ushort_as_half((unsigned short)scw[0]));
-          const float mul = sv * (float)(2 * kTop), add = -sv * (float)(3 * kTop);
+      for (int m = 0; m < a.n_blk; ++m) {   // a part: 128 columns
+        if (n >= NC) ok = __all_sync(0xffffffffu, mbar_wait(bar(kCEmpty + 2 * cs + m), rc.parity ^ 1, abort_flag, lim));
+        if (!ok) break;
+        const int g1 = min(4 * m + 4, a.d_c / 32);
+        if (kept) {
+          for (int c = 16 * m; c < 4 * g1; ++c) put(c, __ldg(src + c));
+        } else if (cur.live) {
+          // (rolled loops, eight values a time: with more code per pass the roles no longer fit the
+          // instruction caches; 4-bit Llama-shaped case, us: 57.5 so, 61.1 with 32 values a pass)
+#pragma unroll 1
+          for (int g = 4 * m; g < g1; ++g) {
+            // An offset code u = code + top sits in the mantissa of 1.0 from bit 23 - QB on: the
+            // float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at
+            // most QB + 11 bits), rounded once to bf16, the products' operand type.
+            constexpr uint32_t kTop = 1u << (QB ? QB - 1 : 0), kMask = (2 * kTop - 1) << (23 - QB);
+            constexpr uint32_t kOne = 0x3F800000u ^ (kTop << (23 - QB));
+            const float sv = __half2float(__ushort_as_half((unsigned short)scw[0]));
+            const float mul = sv * (float)(2 * kTop), add = -sv * (float)(3 * kTop);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) scw[k] = __funnelshift_r(scw[k], k < 3 ? scw[k + 1] : 0u, 16);   // the next group's scale
-          uint32_t wd[4];
-          if (QB == 4) {
-            const uint4 cw = *reinterpret_cast<const uint4*>(codes + g * 16);
-            wd[0] = cw.x; wd[1] = cw.y; wd[2] = cw.z; wd[3] = cw.w;
-          } else {
-            const uint2 cw = *reinterpret_cast<const uint2*>(codes + g * 8);
-            wd[0] = cw.x; wd[1] = cw.x >> 16; wd[2] = cw.y; wd[3] = cw.y >> 16;
-          }
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int sh = 23 - QB - QB * e;
-              const uint32_t at = sh >= 0 ? wd[ch] << (sh & 31) : wd[ch] >> (-sh & 31);
-              f[e] = fmaf(__uint_as_float((at & kMask) ^ kOne), mul, add);
+            for (int k = 0; k < 4; ++k) scw[k] = __funnelshift_r(scw[k], k < 3 ? scw[k + 1] : 0u, 16);   // the next group's scale
+            uint32_t wd[4];
+            if (QB == 4) {
+              const uint4 cw = *reinterpret_cast<const uint4*>(codes + g * 16);
+              wd[0] = cw.x; wd[1] = cw.y; wd[2] = cw.z; wd[3] = cw.w;
+            } else {
+              const uint2 cw = *reinterpret_cast<const uint2*>(codes + g * 8);
+              wd[0] = cw.x; wd[1] = cw.x >> 16; wd[2] = cw.y; wd[3] = cw.y >> 16;
             }
-            put(4 * g + ch, make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int sh = 23 - QB - QB * e;
+                const uint32_t at = sh >= 0 ? wd[0] << (sh & 31) : wd[0] >> (-sh & 31);
+                f[e] = fmaf(__uint_as_float((at & kMask) ^ kOne), mul, add);
+              }
+              put(4 * g + ch, make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
+              wd[0] = wd[1]; wd[1] = wd[2]; wd[2] = wd[3];
+            }
           }
+        } else {
+          for (int c = 16 * m; c < 4 * g1; ++c) put(c, make_uint4(0, 0, 0, 0));
         }
-      } else {
-        for (int c = 0; c < a.d_c / 8; ++c) put(c, make_uint4(0, 0, 0, 0));
+        for (int c = max(16 * m, a.d_c / 8); c < min(16 * m + 16, a.dcp / 8); ++c) put(c, make_uint4(0, 0, 0, 0));   // padding columns
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kCFull + 2 * cs + m));
       }
-      for (int c = a.d_c / 8; c < a.dcp / 8; ++c) put(c, make_uint4(0, 0, 0, 0));   // padding columns
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kREmpty + rs));
-        mbar_arrive(bar(kCFull + cs));
-      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(bar(kREmpty + rs));
       cur = nxt;
       w1 = w2;
       row1 = row2;
@@ -661,12 +720,13 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       }
       if ((n & 1) == s) {
         const int k = n >> 1;
-        if (!fail) fail = !warp_wait(kSFull + s, k & 1);
+        const int buf = n & (kSBufs - 1);
+        if (!fail) fail = !warp_wait(kSFull + buf, (n / kSBufs) & 1);
         float x[N];
         {
           uint32_t raw[N];
           tc_fence_after();
-          tmem_ld<N>(lane0 + kSCol + s * 32, raw);
+          tmem_ld<N>(lane0 + kSCol + buf * 32, raw);
           tmem_wait_ld();
           const bool vis = it.visible(r);
 #pragma unroll
@@ -676,7 +736,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           }
         }
         tc_fence_before();
-        arrive(kSEmpty + s);
+        arrive(kSEmpty + buf);
         if (!some) {
           // the stream starts from the scores of its first visible token plus kTau: a raise (a
           // reduction over the tile, microseconds with its code cold) is then needed only for
@@ -715,7 +775,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
             l[h] *= al[h];
           }
           if (some) {
-            for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk) {
+            for (int blk = 0; blk < a.n_blk; ++blk) {
 #pragma unroll
               for (int h0 = 0; h0 < N; h0 += 8) {
                 uint32_t o[8];
@@ -801,7 +861,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         for (int e = 0; e < HN; ++e) { w0[e] = wts[HN * s + e]; w1[e] = wts[32 + HN * s + e]; }
         float* dst = a.opart + ((size_t)it.slot() * a.H + HN * s) * a.d_c + r;
 #pragma unroll 1
-        for (int blk = 0; blk < (a.dcp + 127) / 128; ++blk, dst += 128) {
+        for (int blk = 0; blk < a.n_blk; ++blk, dst += 128) {
           uint32_t o0[HN], o1[HN];
 #pragma unroll
           for (int e = 0; e < HN; e += 8) {
@@ -1126,7 +1186,8 @@ struct Layout {
 
 // [Q_lat boxes][RoPE query boxes][P of two streams][latent ring][key-box ring][code ring]
 // [exchange][pieces][barriers].  Of the slots left (16 KB: 128 tokens x 64 columns) a tile's key boxes
-// come first, the others hold latent tiles, at least two (one per stream).
+// come first, the others hold latent tiles, at least two (one per stream).  Dequantised latents
+// are not in flight: two tiles of them, three of codes, and key boxes in all the rest.
 static bool layout(const mla_config_t& c, int R, Layout* out) {
   Layout L{};
   const int G = c.n_heads / c.n_kv_heads, qbits = mla_kind_quant(c.cache_kind) ? mla_quant_bits(c.cache_kind) : 0;
@@ -1134,7 +1195,7 @@ static bool layout(const mla_config_t& c, int R, Layout* out) {
   L.n_cbox = (c.d_c + 63) / 64;
   L.n_kbox = (R + 63) / 64;
   L.kr_rows = L.n_kbox == 1 || G > 2 ? L.N : 16;
-  L.NRAW = qbits ? 2 : 0;
+  L.NRAW = qbits ? 3 : 0;
   L.raw_stage = (uint32_t)(kT * c.d_c * qbits / 8);
   L.off_qr = (uint32_t)(L.n_cbox * L.N) * 128;
   L.off_p = L.off_qr + (uint32_t)(L.n_kbox * L.kr_rows) * 128;
@@ -1143,7 +1204,7 @@ static bool layout(const mla_config_t& c, int R, Layout* out) {
   const uint32_t fixed = L.off_c + L.NRAW * L.raw_stage + tail;
   if (fixed > kSmemMax) return false;
   const int slots = (int)((kSmemMax - fixed) / kSlot);
-  L.NC = std::max(2, std::min(kMaxC, (slots - L.n_kbox) / L.n_cbox));
+  L.NC = qbits ? 2 : std::max(2, std::min(kMaxC, (slots - L.n_kbox) / L.n_cbox));
   L.NK = std::min(kMaxK, slots - L.NC * L.n_cbox);
   if (L.NK < 1) return false;
   L.off_k = L.off_c + (uint32_t)(L.NC * L.n_cbox) * kSlot;
@@ -1181,9 +1242,7 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   a.H = cfg.n_heads; a.G = a.H / cfg.n_kv_heads; a.d_c = cfg.d_c; a.dcp = L.n_cbox * 64; a.R = p.R; a.P = D.P;
   a.T_cap = c.T_cap; a.n_cbox = L.n_cbox; a.n_kbox = L.n_kbox; a.kr_rows = L.kr_rows;
   a.NC = L.NC; a.NK = L.NK; a.NRAW = L.NRAW;
-  // a tile's key boxes go in one batch where the ring also holds half of the next tile's, else in
-  // two, so that places free up earlier (4-bit, d_c = 128: 69 us in one batch, 66 in two)
-  a.kpb = 2 * L.NK >= 3 * L.n_kbox ? L.n_kbox : L.NK >= L.n_kbox ? std::max(1, L.n_kbox / 2) : std::max(1, L.NK - 1);
+  a.n_blk = (L.n_cbox + 1) / 2;
   a.B = B; a.workers = D.G; a.win = win;
   // about 5 us, the time a CTA takes for 220 KB; a unit of short rows is bound by latency instead
   a.cost = std::max(2, std::min(8, (int)(3400 / mla_cache_bytes_per_token(&cfg))));
