@@ -244,4 +244,28 @@ __device__ __forceinline__ long long worker_begin(int w, int total, int G) { ret
 // The worker whose range holds unit c of `total` (the last one that starts at or before it).
 __device__ __forceinline__ int worker_of(long long c, int total, int G) { return (int)(((c + 1) * G - 1) / total); }
 
+// Eight two's-complement codes of QB bits (4 or 2; the low QB x 8 bits of `w`) times a scale, as
+// bf16.  An offset code u = code + 2^(QB-1) sits in the mantissa of 1.0 from bit 23 - QB on: the
+// float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at most QB + 11
+// bits with an fp16 scale), rounded once to bf16, the products' operand type.
+template <int QB>
+__device__ __forceinline__ uint4 dequant8(uint32_t w, float scale) {
+  constexpr uint32_t kTop = 1u << (QB - 1), kMask = (2 * kTop - 1) << (23 - QB), kOne = 0x3F800000u ^ (kTop << (23 - QB));
+  const float mul = scale * (float)(2 * kTop), add = -scale * (float)(3 * kTop);
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float f[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int sh = 23 - QB - QB * (e + k);
+      const uint32_t at = sh >= 0 ? w << (sh & 31) : w >> (-sh & 31);
+      f[k] = fmaf(__uint_as_float((at & kMask) ^ kOne), mul, add);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f[0], f[1]);
+    o[e / 2] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 }  // namespace mla

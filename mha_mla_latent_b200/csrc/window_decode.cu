@@ -630,13 +630,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           // instruction caches; 4-bit Llama-shaped case, us: 57.5 so, 61.1 with 32 values a pass)
 #pragma unroll 1
           for (int g = 4 * m; g < g1; ++g) {
-            // An offset code u = code + top sits in the mantissa of 1.0 from bit 23 - QB on: the
-            // float is 1 + u / 2^QB, and one FMA with the scale gives code x scale exactly (at
-            // most QB + 11 bits), rounded once to bf16, the products' operand type.
-            constexpr uint32_t kTop = 1u << (QB ? QB - 1 : 0), kMask = (2 * kTop - 1) << (23 - QB);
-            constexpr uint32_t kOne = 0x3F800000u ^ (kTop << (23 - QB));
             const float sv = __half2float(__ushort_as_half((unsigned short)scw[0]));
-            const float mul = sv * (float)(2 * kTop), add = -sv * (float)(3 * kTop);
 #pragma unroll
             for (int k = 0; k < 4; ++k) scw[k] = __funnelshift_r(scw[k], k < 3 ? scw[k + 1] : 0u, 16);   // the next group's scale
             uint32_t wd[4];
@@ -649,14 +643,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
             }
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
-              float f[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int sh = 23 - QB - QB * e;
-                const uint32_t at = sh >= 0 ? wd[0] << (sh & 31) : wd[0] >> (-sh & 31);
-                f[e] = fmaf(__uint_as_float((at & kMask) ^ kOne), mul, add);
-              }
-              put(4 * g + ch, make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])));
+              put(4 * g + ch, dequant8<QB ? QB : 4>(wd[0], sv));
               wd[0] = wd[1]; wd[1] = wd[2]; wd[2] = wd[3];
             }
           }

@@ -21,9 +21,17 @@
 // [384, 512) S of even and odd tiles, also q, the merged latent's high halves and the output.
 //
 // Roles: warp 0 TMA producer (W_uk slices, tiles, W_uv slices through one ring), warp 1 MMA
-// issuer, warps 4-11 the rows, two threads per row (queries, softmax, epilogue).  Every wait is
+// issuer, warps 4-11 the rows, two threads per row (queries, softmax, epilogue), warps 12-15 with
+// a quantised latent the dequantisation, straight from the cache into the ring.  Every wait is
 // bounded; waits poll without the suspended form, whose wake-up costs more than it frees here
 // (each scheduler holds two row warps and at most one of the others).
+//
+// Bound by the tensor cores once the tiles flow (10 tiles of 128 tokens at d_c = 256 take 1.4 to
+// 1.8 us each, some 85% of the measured dense rate) and by the latency of its ends: about 6 us
+// from the launch to the first scores and 5 us from the last tile to the stored rows.  B200, 8
+// sequences x 64 queries, 32 KV heads, window 1024, d_c = 256: 33.7 us; 4-bit latent 51 us, where
+// a tile's conversion (a thread per row, about 3 us) bounds it, and 33 us at d_c = 128.  The
+// head-row units with their absorption and merge launches take 179, 202 and 157 us there.
 #include <cuda.h>
 
 #include "decode_common.cuh"
@@ -36,7 +44,7 @@ using namespace sm100;
 
 constexpr int kT = 128;               // tokens per tile
 constexpr int kRows = 128;            // rows per unit
-constexpr int kThreads = 384;         // 12 warps
+template <int QB> constexpr int kThreadsOf = QB ? 512 : 384;   // a quantised latent: a warpgroup that dequantises
 constexpr uint32_t kBox = kT * 128;   // bytes of 128 rows x 64 bf16 columns
 constexpr uint32_t kKrTile = kT * 64; // RoPE keys of a tile: 32 columns (4 KV heads)
 constexpr int kMaxG = 4;              // KV heads per unit
@@ -62,7 +70,7 @@ struct Args {
 };
 
 enum { kBarFull = 0, kBarEmpty = 4, kBarQ = 8, kBarAccFull, kBarAccEmpty, kBarQlat, kBarS, kBarP = kBarS + 2,
-       kBarO = kBarP + 2, kBarA = kBarO + 2, kBarDone, kBarX, kBars = kBarX + 4 };
+       kBarO = kBarP + 2, kBarA = kBarO + 2, kBarDone, kBarX, kBarC = kBarX + 4, kBars = kBarC + 4 };
 
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4); }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -87,8 +95,9 @@ __device__ __forceinline__ uint64_t below64(int n) {
   return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-template <bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+// QB: code width of a quantised latent (4 or 2), 0 for bf16.
+template <bool PAGED, int QB>
+__global__ void __launch_bounds__(kThreadsOf<QB>, 1)
 window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_kr,
                     const __grid_constant__ CUtensorMap tm_uk, const __grid_constant__ CUtensorMap tm_uv,
                     const __grid_constant__ Args a) {
@@ -116,6 +125,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
     for (int i : rows) mbar_init(bar(i), 8);   // the row warps
     for (int i : one) mbar_init(bar(i), 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar(kBarX + i), 2);   // the two warps of the same rows
+    for (int i = 0; i < 4; ++i) mbar_init(bar(kBarC + i), 4);   // the dequantising warps
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -140,10 +150,10 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   if (warp == 0 && lane == 0)
     while (loaded < min(ng, NST)) load_uk(loaded, loaded);
   // rows (warps 4-11): thread -> row r of the unit, half hf of its tokens and columns
-  const int w = warp & 3, hf = warp >= 8, r = 32 * w + lane;   // tensor memory lane = row
+  const int w = warp & 3, hf = warp >= 8 && warp < 12, r = 32 * w + lane;   // tensor memory lane = row
   const int per_g = a.G * a.qb;
   const int gi = r / per_g, hi = (r / a.qb) % a.G, qi = r % a.qb;
-  const bool valid = warp >= 4 && gi < ng && qi < nq;
+  const bool valid = warp >= 4 && warp < 12 && gi < ng && qi < nq;
   const int g = g0 + gi;
   const size_t row = ((size_t)b * a.Q + q0 + qi) * a.H + g * a.G + hi;
   const uint32_t lane0 = tmem + ((uint32_t)(32 * w) << 16);
@@ -183,146 +193,213 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
   const int T = (span.len + kT - 1) / kT;           // tiles
   auto tile_token = [&](int n) { return span.token(n * kT); };
 
-  if (warp == 0) {
-    // ============================================================ TMA producer (lane 0)
-    if (lane == 0) {
-      const int items = T > 0 ? 2 * ng + T : 0;
-      bool ok = true;
-      RingPos rp;
-      for (int i = 0; i < loaded; ++i) rp.next(NST);
-      while (ok && loaded < items) {
-        const int i = loaded, s = rp.slot;
-        if (i >= NST) ok = mbar_spin(bar(kBarEmpty + s), rp.parity ^ 1, abort_flag, lim);
-        if (!ok) break;
-        rp.next(NST);
-        if (i < ng) { load_uk(i, s); continue; }
-        const uint32_t at = sb + a.off_ring + (uint32_t)s * a.stage;
-        if (i < ng + T) {
-          const int t = tile_token(i - ng);
-          const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
-          const int row = lc.pb * lc.cap + lc.pt;
-          mbar_expect_tx(bar(kBarFull + s), (uint32_t)n_cbox * kBox + kKrTile);
-          for (int k = 0; k < n_cbox; ++k) tma_load_2d(at + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
-          tma_load_2d(at + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
-        } else {
-          const int gi = i - ng - T;
-          mbar_expect_tx(bar(kBarFull + s), uv_bytes);
-          for (int k = 0; k < n_hbox; ++k)
-            tma_load_2d(at + k * a.d_c * 128, &tm_uv, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_c);
+  if (warp < 4) {
+    if (QB) setmaxnreg_dec<88>();
+    if (warp == 0) {
+      // ============================================================ TMA producer (lane 0)
+      if (lane == 0) {
+        const int items = T > 0 ? 2 * ng + T : 0;
+        bool ok = true;
+        RingPos rp;
+        for (int i = 0; i < loaded; ++i) rp.next(NST);
+        while (ok && loaded < items) {
+          const int i = loaded, s = rp.slot;
+          if (i >= NST) ok = mbar_spin(bar(kBarEmpty + s), rp.parity ^ 1, abort_flag, lim);
+          if (!ok) break;
+          rp.next(NST);
+          if (i < ng) { load_uk(i, s); continue; }
+          const uint32_t at = sb + a.off_ring + (uint32_t)s * a.stage;
+          if (i < ng + T) {
+            const int t = tile_token(i - ng);
+            const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
+            const int row = lc.pb * lc.cap + lc.pt;
+            mbar_expect_tx(bar(kBarFull + s), (QB ? 0u : (uint32_t)n_cbox * kBox) + kKrTile);
+            for (int k = 0; k < (QB ? 0 : n_cbox); ++k) tma_load_2d(at + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
+            tma_load_2d(at + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
+          } else {
+            const int gi = i - ng - T;
+            mbar_expect_tx(bar(kBarFull + s), uv_bytes);
+            for (int k = 0; k < n_hbox; ++k)
+              tma_load_2d(at + k * a.d_c * 128, &tm_uv, bar(kBarFull + s), k * 64, (g0 + gi) * a.d_c);
+          }
+          ++loaded;
         }
-        ++loaded;
+        volatile int never = 0;   // every copy lands before the CTA exits
+        for (int i = max(0, loaded - NST); i < loaded; ++i) mbar_spin(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
       }
-      volatile int never = 0;   // every copy lands before the CTA exits
-      for (int i = max(0, loaded - NST); i < loaded; ++i) mbar_spin(bar(kBarFull + i % NST), (i / NST) & 1, &never, lim);
-    }
-  } else if (warp == 1) {
-    // ============================================================ MMA issuer
-    // The whole warp walks the same path, with every condition the same in all lanes, and one
-    // elected lane issues: the compiler then keeps descriptors in uniform registers.  (Issued
-    // from a branch of lane 0 a product took 110 to 190 cycles, more than most of them compute.)
-    if (T > 0) {
-      auto wait_all = [&](int i, int parity) {
-        return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)) != 0;
-      };
-      auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
-      auto stage_at = [&](const RingPos& p) { return sb + a.off_ring + (uint32_t)p.slot * a.stage; };
-      RingPos r1;   // ring items: weights, then tiles (S), then weights
-      bool ok = wait_all(kBarQ, 0);
-      // absorption: q (tensor memory) x W_ukF[g], once per KV head over all rows
-      const uint32_t id_abs = idesc_bf16_f32(kRows, a.dcp, false, true);
-      for (int gi = 0; ok && gi < ng; ++gi) {
-        ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (gi - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t w0 = smem_desc(stage_at(r1), a.d_h * 128, 1024, kLayoutSW128);
-          for (int k = 0; k < a.d_h / 16; ++k) mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, w0 + 128u * k, id_abs, k > 0);
-          tc_commit(bar(kBarEmpty + r1.slot));
-          tc_commit(bar(kBarAccFull));
-        }
-        __syncwarp();
-        r1.next(NST);
-      }
-      ok = ok && wait_all(kBarQlat, 0);
-      tc_fence_after();
-      // tiles: S(n) needs its tile and the buffer of tile n - 2, whose P was read by O(n - 2)
-      // issued before it; O(n) needs P(n).  Whichever can go next is issued.
-      const uint32_t id_s = idesc_bf16_f32(kRows, kT, false, false), id_o = idesc_bf16_f32(kRows, a.dcp, false, true);
-      // descriptors are made once; a step along K adds its bytes / 16 to the address field
-      const uint64_t desc_q = smem_desc(sb, 16, 1024, kLayoutSW128), desc_qr = smem_desc(sb + a.off_qr, 16, 512, kLayoutSW64);
-      int n1 = 0, n2 = 0;
-      RingPos r2 = r1;     // tiles of O
-      uint64_t idle = 0;   // when nothing could be issued: since when (read every 64th look only)
-      int looks = 0;
-      while (ok && n2 < T) {
-        if (n1 < T && n1 <= n2 + 1 && ready(kBarFull + r1.slot, r1.parity)) {
+    } else if (warp == 1) {
+      // ============================================================ MMA issuer
+      // The whole warp walks the same path, with every condition the same in all lanes, and one
+      // elected lane issues: the compiler then keeps descriptors in uniform registers.  (Issued
+      // from a branch of lane 0 a product took 110 to 190 cycles, more than most of them compute.)
+      if (T > 0) {
+        auto wait_all = [&](int i, int parity) {
+          return __all_sync(0xffffffffu, mbar_spin(bar(i), parity, abort_flag, lim)) != 0;
+        };
+        auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, mbar_test(bar(i), parity)) != 0; };
+        auto stage_at = [&](const RingPos& p) { return sb + a.off_ring + (uint32_t)p.slot * a.stage; };
+        RingPos r1;   // ring items: weights, then tiles (S), then weights
+        bool ok = wait_all(kBarQ, 0);
+        // absorption: q (tensor memory) x W_ukF[g], once per KV head over all rows
+        const uint32_t id_abs = idesc_bf16_f32(kRows, a.dcp, false, true);
+        for (int gi = 0; ok && gi < ng; ++gi) {
+          ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (gi - 1) & 1));
+          if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t c0 = stage_at(r1), d = tmem + kSCol + (n1 & 1) * kT;
-            uint64_t da = desc_q, db = smem_desc(c0, 16, 1024, kLayoutSW128);
-            const uint64_t dk = smem_desc(c0 + n_cbox * kBox, 16, 512, kLayoutSW64);
-            tc_mma_bf16(d, desc_qr, dk, id_s, 0);
-            if (ng > 2) tc_mma_bf16(d, desc_qr + 2, dk + 2, id_s, 1);
-            for (int k = 0; k < n_cbox; ++k) {   // a box: four steps of 16 columns
-              tc_mma_bf16(d, da, db, id_s, 1);
-              tc_mma_bf16(d, da + 2, db + 2, id_s, 1);
-              tc_mma_bf16(d, da + 4, db + 4, id_s, 1);
-              tc_mma_bf16(d, da + 6, db + 6, id_s, 1);
-              da += kBox >> 4;
-              db += kBox >> 4;
-            }
-            tc_commit(bar(kBarS + (n1 & 1)));
+            const uint64_t w0 = smem_desc(stage_at(r1), a.d_h * 128, 1024, kLayoutSW128);
+            for (int k = 0; k < a.d_h / 16; ++k) mma_a_tmem(tmem + kOCol, tmem + kSCol + 8 * k, w0 + 128u * k, id_abs, k > 0);
+            tc_commit(bar(kBarEmpty + r1.slot));
+            tc_commit(bar(kBarAccFull));
           }
           __syncwarp();
           r1.next(NST);
-          ++n1;
-          looks = 0;
-        } else if (n2 < n1 && ready(kBarP + (n2 & 1), (n2 >> 1) & 1)) {
+        }
+        ok = ok && wait_all(kBarQlat, 0);
+        tc_fence_after();
+        // tiles: S(n) needs its tile and the buffer of tile n - 2, whose P was read by O(n - 2)
+        // issued before it; O(n) needs P(n).  Whichever can go next is issued.
+        const uint32_t id_s = idesc_bf16_f32(kRows, kT, false, false), id_o = idesc_bf16_f32(kRows, a.dcp, false, true);
+        // descriptors are made once; a step along K adds its bytes / 16 to the address field
+        const uint64_t desc_q = smem_desc(sb, 16, 1024, kLayoutSW128), desc_qr = smem_desc(sb + a.off_qr, 16, 512, kLayoutSW64);
+        int n1 = 0, n2 = 0;
+        RingPos r2 = r1;     // tiles of O
+        RingPos rc;          // dequantised tiles
+        uint64_t idle = 0;   // when nothing could be issued: since when (read every 64th look only)
+        int looks = 0;
+        while (ok && n2 < T) {
+          if (n1 < T && n1 <= n2 + 1 && ready(kBarFull + r1.slot, r1.parity) && (!QB || ready(kBarC + rc.slot, rc.parity))) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t c0 = stage_at(r1), d = tmem + kSCol + (n1 & 1) * kT;
+              uint64_t da = desc_q, db = smem_desc(c0, 16, 1024, kLayoutSW128);
+              const uint64_t dk = smem_desc(c0 + n_cbox * kBox, 16, 512, kLayoutSW64);
+              tc_mma_bf16(d, desc_qr, dk, id_s, 0);
+              if (ng > 2) tc_mma_bf16(d, desc_qr + 2, dk + 2, id_s, 1);
+              for (int k = 0; k < n_cbox; ++k) {   // a box: four steps of 16 columns
+                tc_mma_bf16(d, da, db, id_s, 1);
+                tc_mma_bf16(d, da + 2, db + 2, id_s, 1);
+                tc_mma_bf16(d, da + 4, db + 4, id_s, 1);
+                tc_mma_bf16(d, da + 6, db + 6, id_s, 1);
+                da += kBox >> 4;
+                db += kBox >> 4;
+              }
+              tc_commit(bar(kBarS + (n1 & 1)));
+            }
+            __syncwarp();
+            r1.next(NST);
+            rc.next(NST);
+            ++n1;
+            looks = 0;
+          } else if (n2 < n1 && ready(kBarP + (n2 & 1), (n2 >> 1) & 1)) {
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t p = tmem + kSCol + (n2 & 1) * kT;
+              const uint64_t dv = smem_desc(stage_at(r2), kBox, 1024, kLayoutSW128);
+              mma_a_tmem(tmem + kOCol, p, dv, id_o, n2 > 0);
+  #pragma unroll
+              for (int k = 1; k < kT / 16; ++k) mma_a_tmem(tmem + kOCol, p + 8 * k, dv + 128 * k, id_o, 1);
+              tc_commit(bar(kBarEmpty + r2.slot));
+              tc_commit(bar(kBarO + (n2 & 1)));
+            }
+            __syncwarp();
+            r2.next(NST);
+            ++n2;
+            looks = 0;
+          } else if ((++looks & 63) == 0) {
+            const uint64_t now = globaltimer();
+            if (looks == 64) idle = now;
+            if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
+            ok = __all_sync(0xffffffffu, ok) != 0;
+          }
+        }
+        // output: merged latent (tensor memory, high and low halves) x W_uv[g]
+        const uint32_t id_out = idesc_bf16_f32(kRows, a.dhp, false, true);
+        ok = ok && wait_all(kBarA, 0);
+        for (int gi = 0; ok && gi < ng; ++gi) {
+          ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (ng + gi - 1) & 1));
+          if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t p = tmem + kSCol + (n2 & 1) * kT;
-            const uint64_t dv = smem_desc(stage_at(r2), kBox, 1024, kLayoutSW128);
-            mma_a_tmem(tmem + kOCol, p, dv, id_o, n2 > 0);
-#pragma unroll
-            for (int k = 1; k < kT / 16; ++k) mma_a_tmem(tmem + kOCol, p + 8 * k, dv + 128 * k, id_o, 1);
-            tc_commit(bar(kBarEmpty + r2.slot));
-            tc_commit(bar(kBarO + (n2 & 1)));
+            const uint64_t w0 = smem_desc(stage_at(r1), a.d_c * 128, 1024, kLayoutSW128);
+            for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kSCol + 8 * k, w0 + 128u * k, id_out, k > 0);
+            for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kOCol + 8 * k, w0 + 128u * k, id_out, 1);
+            tc_commit(bar(kBarEmpty + r1.slot));
+            tc_commit(bar(kBarAccFull));
           }
           __syncwarp();
-          r2.next(NST);
-          ++n2;
-          looks = 0;
-        } else if ((++looks & 63) == 0) {
-          const uint64_t now = globaltimer();
-          if (looks == 64) idle = now;
-          if (*abort_flag || now - idle > lim) { *abort_flag = 1; ok = false; }
-          ok = __all_sync(0xffffffffu, ok) != 0;
+          r1.next(NST);
         }
-      }
-      // output: merged latent (tensor memory, high and low halves) x W_uv[g]
-      const uint32_t id_out = idesc_bf16_f32(kRows, a.dhp, false, true);
-      ok = ok && wait_all(kBarA, 0);
-      for (int gi = 0; ok && gi < ng; ++gi) {
-        ok = wait_all(kBarFull + r1.slot, r1.parity) && (gi == 0 || wait_all(kBarAccEmpty, (ng + gi - 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t w0 = smem_desc(stage_at(r1), a.d_c * 128, 1024, kLayoutSW128);
-          for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kSCol + 8 * k, w0 + 128u * k, id_out, k > 0);
-          for (int k = 0; k < a.d_c / 16; ++k) mma_a_tmem(tmem + kSCol + kT, tmem + kOCol + 8 * k, w0 + 128u * k, id_out, 1);
-          tc_commit(bar(kBarEmpty + r1.slot));
-          tc_commit(bar(kBarAccFull));
-        }
+        if (elect_one()) tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
         __syncwarp();
-        r1.next(NST);
+        volatile int never = 0;
+        mbar_spin(bar(kBarDone), 0, &never, lim);
       }
-      if (elect_one()) tc_commit(bar(kBarDone));   // whatever was issued has finished before tensor memory is freed
+    }   // (warps 2 and 3 idle)
+  } else if (QB != 0 && warp >= 12) {
+    // ============================================================ dequantisation (a token row per thread)
+    if (QB) setmaxnreg_dec<88>();
+    constexpr int kQ = QB ? QB : 4;
+    const int tr = 32 * w + lane, code_row = a.d_c * kQ / 8, groups = a.d_c / 32;
+    // The codes come straight from the cache, a group of 32 ahead of the one in work (the first
+    // touch of a row brings its whole line); where a tile's rows lie, their lines and group
+    // scales are asked for a tile ahead.
+    struct Src { long long row = -1; uint32_t sc[4] = {0, 0, 0, 0}; } cur, nxt;
+    auto source = [&](int n, Src& o) {
+      const int t0 = tile_token(n), t = t0 + tr;
+      o.row = -1;
+      // a row that no query of the unit sees is zero (its codes and scales may be stale)
+      if (n >= T || tr >= span.len - n * kT || (t >= a.win.n_sink && t < span.lo)) return;
+      const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t0, a.err) : MlaLoc{b, t0, a.T_cap};
+      o.row = (long long)lc.pb * lc.cap + lc.pt + tr;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(a.cache.c_kv) + o.row * code_row));
+      const unsigned short* sp = reinterpret_cast<const unsigned short*>(a.cache.c_scales) + o.row * groups;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o.sc[k] = (2 * k < groups ? (uint32_t)__ldg(sp + 2 * k) : 0u) | (2 * k + 1 < groups ? (uint32_t)__ldg(sp + 2 * k + 1) << 16 : 0u);
+    };
+    if (T > 0) source(0, cur);
+    bool ok = true;
+    RingPos rt, rc;
+    for (int i = 0; i < ng; ++i) rt.next(NST);
+    for (int n = 0; ok && n < T; ++n, rt.next(NST), rc.next(NST)) {
+      source(n + 1, nxt);
+      const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.cache.c_kv) + cur.row * code_row;
+      auto group = [&](int g) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (cur.row < 0 || g >= groups) return v;
+        if (kQ == 4) return __ldg(reinterpret_cast<const uint4*>(codes) + g);
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes) + g);
+        return make_uint4(x.x, x.x >> 16, x.y, x.y >> 16);
+      };
+      uint4 ahead = group(0);
+      if (n + ng >= NST) ok = wwait(kBarEmpty + rt.slot, rt.parity ^ 1);
+      if (!ok) break;
+      uint8_t* C = smem + a.off_ring + (uint32_t)rt.slot * a.stage;
+      auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4*>(C + (chunk >> 3) * kBox + sw128(tr, chunk)) = v; };
+      // (rolled loops: little code, for the instruction caches)
+#pragma unroll 1
+      for (int g = 0; g < groups; ++g) {
+        uint4 wd = ahead;
+        ahead = group(g + 1);
+        const float sv = __half2float(__ushort_as_half((unsigned short)cur.sc[0]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cur.sc[k] = __funnelshift_r(cur.sc[k], k < 3 ? cur.sc[k + 1] : 0u, 16);   // the next group's scale
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch) {
+          put(4 * g + ch, cur.row >= 0 ? dequant8<kQ>(wd.x, sv) : make_uint4(0, 0, 0, 0));
+          wd.x = wd.y; wd.y = wd.z; wd.z = wd.w;
+        }
+      }
+      for (int c = a.d_c / 8; c < a.dcp / 8; ++c) put(c, make_uint4(0, 0, 0, 0));   // padding columns
+      fence_proxy_async_smem();
       __syncwarp();
-      volatile int never = 0;
-      mbar_spin(bar(kBarDone), 0, &never, lim);
+      if (lane == 0) mbar_arrive(bar(kBarC + rc.slot));
+      cur = nxt;
     }
-  } else if (warp >= 4) {
+  } else {
     // ============================================================ rows
+    if (QB) setmaxnreg_inc<168>();
     // Two threads per row, in warps w and w + 4 of the same tensor memory lanes: each takes
     // half of every tile's tokens and of every accumulator's columns.
     auto arrive = [&](int i) {
@@ -438,14 +515,16 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
           for (int t = 0; t < 64; ++t) s[t] = ((uint32_t)(seen >> (t & 32)) >> (t & 31)) & 1u ? s[t] : -INFINITY;
           // rows that no query of the unit sees (stale or hidden, possibly not finite) are
           // zeroed before O's product multiplies them by P = 0; S of this tile has been read
-          uint8_t* C = smem + a.off_ring + (uint32_t)rt.slot * a.stage;
-          auto zero_rows = [&](int from, int to) {   // consecutive threads, consecutive 16-byte chunks
-            for (int i = from * 8 + 128 * hf + r; i < to * 8; i += 256)
-              for (int k = 0; k < n_cbox; ++k) *reinterpret_cast<uint4*>(C + k * kBox + i * 16) = make_uint4(0, 0, 0, 0);
-          };
-          zero_rows(max(0, a.win.n_sink - t0), min(nvalid, span.lo - t0));
-          zero_rows(nvalid, kT);
-          fence_proxy_async_smem();
+          if (!QB) {
+            uint8_t* C = smem + a.off_ring + (uint32_t)rt.slot * a.stage;
+            auto zero_rows = [&](int from, int to) {   // consecutive threads, consecutive 16-byte chunks
+              for (int i = from * 8 + 128 * hf + r; i < to * 8; i += 256)
+                for (int k = 0; k < n_cbox; ++k) *reinterpret_cast<uint4*>(C + k * kBox + i * 16) = make_uint4(0, 0, 0, 0);
+            };
+            zero_rows(max(0, a.win.n_sink - t0), min(nvalid, span.lo - t0));
+            zero_rows(nvalid, kT);
+            fence_proxy_async_smem();
+          }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -635,11 +714,11 @@ static int pick_gb(int B, int Q, int G, int n_kv, int tiles, int sms) {
 }  // namespace fused
 }  // namespace mla
 
-// Shapes: bf16 cache and weights, r = 4 kept pairs, d_c a multiple of 32 up to 256, head dim a
+// Shapes: bf16 weights, latent in bf16 or 4- or 2-bit groups, r = 4 kept pairs, d_c a multiple of 32 up to 256, head dim a
 // multiple of 16 up to 128, at most 128 query heads per KV head, RoPE rows of whole 16 bytes.
 bool mla_window_fused_capable(const mla_plan& p) {
   const mla_config_t& c = p.cfg;
-  return c.dtype == MLA_BF16 && c.cache_kind == MLA_CACHE_SAME && c.r_pairs == 4 && c.d_c % 32 == 0 && c.d_c <= 256 &&
+  return c.dtype == MLA_BF16 && c.cache_kind != MLA_CACHE_INT4_G32_R128 && c.r_pairs == 4 && c.d_c % 32 == 0 && c.d_c <= 256 &&
          c.head_dim % 16 == 0 && c.head_dim <= 128 && c.n_heads / c.n_kv_heads <= 128;
 }
 
@@ -667,15 +746,20 @@ cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, con
   a.NST = L.NST; a.stage = L.stage; a.off_qr = L.off_qr; a.off_ring = L.off_ring; a.off_xchg = L.off_xchg; a.off_bar = L.off_bar;
   const uint64_t rows = mla_cache_rows(c);
   CUtensorMap tm_c, tm_kr, tm_uk, tm_uv;
-  if (!map_2d(&tm_c, c.c_kv, a.d_c, rows, 64, kT) || !map_2d(&tm_kr, c.k_rope, p.R, rows, 32, kT) ||
+  const int qbits = mla_kind_quant(cfg.cache_kind) ? mla_quant_bits(cfg.cache_kind) : 0;   // (no map of codes)
+  if (!map_2d(&tm_c, qbits ? p.W_ukF : c.c_kv, a.d_c, qbits ? (uint64_t)a.d_h : rows, 64, qbits ? a.d_h : kT) || !map_2d(&tm_kr, c.k_rope, p.R, rows, 32, kT) ||
       !map_2d(&tm_uk, p.W_ukF, a.d_c, (uint64_t)a.n_kv * a.d_h, 64, a.d_h) ||
       !map_2d(&tm_uv, p.W_uv, a.d_h, (uint64_t)a.n_kv * a.d_c, 64, a.d_c))
     return cudaErrorInvalidValue;
-  auto kern = c.block_table ? window_fused_kernel<true> : window_fused_kernel<false>;
+  auto pick = [&](auto paged) {
+    constexpr bool PAGED = decltype(paged)::value;
+    return qbits == 4 ? window_fused_kernel<PAGED, 4> : qbits == 2 ? window_fused_kernel<PAGED, 2> : window_fused_kernel<PAGED, 0>;
+  };
+  const auto kern = c.block_table ? pick(std::true_type()) : pick(std::false_type());
   cudaError_t e = mla_smem_limit((const void*)kern, L.total);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
-  e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(kThreads), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);
+  e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(qbits ? kThreadsOf<4> : kThreadsOf<0>), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);
   if (e != cudaSuccess) return e;
   return mla_profile_event(p, kProfAttention, true, s);
 }

@@ -289,6 +289,33 @@ def test_many_short_sequences(B, splits):
     plan.close()
 
 
+@pytest.mark.parametrize("name", ["llama_dc96", "llama_int4_dc256", "llama_int2", "gqa64"])
+def test_chunk_window_head_rows(name):
+    """The head-row units (MLA_OPT_DECODE_KERNEL 3), which also serve the head dims that the one-launch form lacks."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=16)
+    B, Q = 3, 20
+    lens = [20, 131, 390]
+    seqs = [layer.sequence(L) for L in lens]
+    cache = make_cache(mla, layer, B, 512, True)
+    for b, s in enumerate(seqs):
+        store(cache, b, s)
+    q = layer.queries(B, Q)
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, 3)
+    out = torch.full_like(q, float("nan"), device="cuda")
+    ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+    for n_sink, window in [(0, 1), (5, 120), (70, 200)]:
+        mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(), out, ws, n_sink, window)
+        assert mla.mla_device_error(plan) == 0
+        got = out.double().cpu().numpy()
+        for b, L in enumerate(lens):
+            for i in (0, Q // 2, Q - 1):
+                ref = layer.reference(q[b, i], seqs[b], L - Q + i, n_sink, window).numpy()
+                assert_close(got[b, i], ref, "bf16", f"{name} sinks {n_sink} window {window} seq {b} query {i}")
+    plan.close()
+
+
 @pytest.mark.parametrize("B,Q,name", [(24, 3, "llama_dc64"), (1, 130, "llama_dc64"), (2, 33, "smollm"), (30, 2, "smollm")])
 def test_chunk_window_unit_shapes(B, Q, name):
     """Numbers of sequences and queries that make the chunk's units of one, two and four KV heads."""
