@@ -316,9 +316,14 @@ MLA_API mla_status_t mla_decode_chunk(const mla_plan_t* plan, const mla_cache_t*
  * rotated at p, the keys keep the rotation they were appended with.  The cost follows the
  * visible tokens, not the length.  With window >= T_cap it is mla_decode's attention.
  *   n_sink >= 0, window >= 1; the other arguments, the workspace and L == 0 as for mla_decode
- * Every cache kind.  Kernel: the head-row tensor-core kernel where its shapes allow
- * (mla_decode_kernel_choice, 3), else the CUDA-core kernel; MLA_OPT_DECODE_KERNEL = 2 returns
- * MLA_ERR_UNSUPPORTED (the token-row kernel has no window). */
+ * Every cache kind and shape that mla_decode's CUDA-core kernel takes, and more heads where a
+ * tensor-core kernel does.  Kernel (MLA_OPT_DECODE_KERNEL = 0): one launch on the CUDA cores for
+ * few visible tokens of an unquantised cache with at most 4 query heads per KV head; else the
+ * windowed tensor-core kernel (bf16, r = 4, at most 32 query heads, head dim a multiple of 8,
+ * d_c a multiple of 32 up to 256); else the head-row kernel where its shapes allow; else the
+ * CUDA-core split.  1 and 3 force the last two's kernels as for mla_decode, 2 returns
+ * MLA_ERR_UNSUPPORTED (the token-row kernel has no window).  The plan's device must be the
+ * current one, else MLA_ERR_INVALID_ARG (mla_decode_chunk_window too). */
 MLA_API mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache, const int32_t* seq_lens,
                                        const void* q, int32_t B, int32_t n_sink, int32_t window, void* out,
                                        void* workspace, size_t ws_bytes, void* stream);
@@ -330,7 +335,9 @@ MLA_API mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t
  * (queries share the tiles they read, so what a non-finite row does to the sequence's other
  * queries is unspecified).  Arguments, workspace (mla_decode_chunk_workspace_bytes) and
  * supported shapes as for mla_decode_chunk; n_sink >= 0, window >= 1; Q == 1 is
- * mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED. */
+ * mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED.  Head dims that are
+ * multiples of 16 up to 128 run in one launch, the others (and option 3) as the head-row units
+ * of mla_decode_chunk. */
 MLA_API mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* cache,
                                              const int32_t* seq_lens, const void* q, int32_t B, int32_t Q,
                                              int32_t n_sink, int32_t window, void* out, void* workspace,
@@ -503,11 +510,14 @@ MLA_API mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t*
                                      int32_t max_copies, int32_t* status, void* stream);
 
 /* Copy the residual window (MLA_CACHE_INT4_G32_R128: ring rows and their positions) of
- * sequence src[i] to sequence dst[i] in one layer's cache, for a fork.  A pair is skipped and
- * MLA_DEVERR_ROW set in status[1] under the conditions of mla_blocks_fork's rows.
- *   src, dst device [n] int32 in [0, cache->B).  MLA_ERR_INVALID_ARG for a cache without a ring. */
+ * sequence src[i] to sequence dst[i] in one layer's cache, for a fork.  The pairs that
+ * mla_blocks_fork skips with the same arguments are skipped here too, with the same bits set in
+ * status[1].
+ *   src, dst device [n] int32 in [0, cache->B); seq_lens device [cache->B] int32 or NULL (the
+ *   lengths are not looked at).  MLA_ERR_INVALID_ARG for a cache without a ring. */
 MLA_API mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src,
-                                   const int32_t* dst, int32_t n, int32_t* status, void* stream);
+                                   const int32_t* dst, int32_t n, const int32_t* seq_lens, int32_t* status,
+                                   void* stream);
 
 #ifdef __cplusplus
 }

@@ -92,7 +92,7 @@ def _load():
         "mla_blocks_trim": (i32, [vp, vp, i32, i32, i32, vp, i32, i32, vp, vp, vp, vp]),
         "mla_blocks_compact": (i32, [vp, vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
         "mla_blocks_copy": (i32, [cfgp, cachep, vp, i32, vp, vp]),
-        "mla_ring_copy": (i32, [cfgp, cachep, vp, vp, i32, vp, vp]),
+        "mla_ring_copy": (i32, [cfgp, cachep, vp, vp, i32, vp, vp, vp]),
         "mla_decode_step_host": (i32, [vp, cachep, vp, vp, vp, i32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
@@ -314,6 +314,8 @@ def _i32(t, name, n):
 def _table(table, refs):
     """Sizes of a block table [B][n_cols] and its holder counts [n_blocks]."""
     B, C = table.shape
+    if table.is_cuda and table.get_device() != _current_device():
+        raise ValueError("the block table must be on the current device")
     return B, C, refs.numel()
 
 
@@ -389,11 +391,13 @@ def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None
     return st
 
 
-def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True):
-    """Copies the residual windows of sequences src to sequences dst in one layer's cache."""
+def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True, seq_lens=None):
+    """Copies the residual windows of sequences src to sequences dst in one layer's cache; with
+    the seq_lens of the fork, pairs that it skips for their length are skipped here too."""
     n = src.numel()
+    lens = None if seq_lens is None else _i32(seq_lens, "seq_lens", cache.B)
     st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src", n), _i32(dst, "dst", n), n,
-                            _block_status(status), _stream(stream))
+                            lens, _block_status(status), _stream(stream))
     if check:
         _check(st, "mla_ring_copy")
     return st

@@ -59,7 +59,10 @@ class LatentCache:
         if not self.paged:
             return torch.full_like(t, b), t
         BT = _lib.MLA_BLOCK_TOKENS
-        return self.block_table[b].cpu()[t // BT].long(), t % BT   # as the device holds it: a BlockPool changes it
+        blocks = self.block_table[b].cpu()[t // BT].long()   # as the device holds it: a BlockPool changes it
+        if (blocks < 0).any():
+            raise ValueError(f"sequence {b} has no block for some of the tokens [{t0}, {t1})")
+        return blocks, t % BT
 
     def _rows(self, arr, b, t0, t1):
         pb, pt = self._loc(b, t0, t1)
@@ -122,7 +125,10 @@ class BlockPool:
     """The blocks that the paged caches of a model's layers are made of: one block table
     [B][T_cap/128] (-1: no block) and one count of holders per block, kept on the device by the
     mla_blocks_* entry points.  Layers made with `layer` share the table; what a call moves is
-    moved in every one of them.  Nothing here waits for the device but `errors` and `in_use`."""
+    moved in every one of them.  Calls follow one another on one stream (the argument, else the
+    current one); rows and lengths are device tensors or anything that torch makes a tensor
+    of.  With int32 device tensors nothing waits for the device but `errors` and `in_use`, and
+    the others can be captured into a graph."""
 
     def __init__(self, B: int, T_cap: int, n_blocks: int, device="cuda"):
         BT = _lib.MLA_BLOCK_TOKENS
@@ -146,40 +152,51 @@ class BlockPool:
         self.layers.append(c)
         return c
 
-    def _int32(self, x):
-        return torch.as_tensor(x, dtype=torch.int32).to(self.device).contiguous()
+    @staticmethod
+    def _on(stream):
+        """What the call makes itself (converted arguments) belongs to its stream."""
+        if stream is None or isinstance(stream, torch.cuda.Stream):
+            return torch.cuda.stream(stream)
+        return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
 
-    def _move(self, stream):
+    def _int32(self, x):
+        return torch.as_tensor(x).to(self.device, torch.int32).contiguous()
+
+    def _move(self):
         for c in self.layers:
-            _lib.mla_blocks_copy(c.cfg, c.struct, self.copies, self.status, stream=stream)
+            _lib.mla_blocks_copy(c.cfg, c.struct, self.copies, self.status)
 
     def fork(self, src, dst, seq_lens, stream=None) -> None:
         """Sequence dst[i] shares the blocks of the first seq_lens[src[i]] tokens of src[i]
         (the residual windows are copied)."""
-        src, dst, lens = self._int32(src), self._int32(dst), self._int32(seq_lens)
-        _lib.mla_blocks_fork(self.table, self.refs, src, dst, lens, self.table, self.refs, self.status, stream=stream)
-        for c in self.layers:
-            if c.c_resid is not None:
-                _lib.mla_ring_copy(c.cfg, c.struct, src, dst, self.status, stream=stream)
+        with self._on(stream):
+            src, dst, lens = self._int32(src), self._int32(dst), self._int32(seq_lens)
+            _lib.mla_blocks_fork(self.table, self.refs, src, dst, lens, self.table, self.refs, self.status)
+            for c in self.layers:
+                if c.c_resid is not None:
+                    _lib.mla_ring_copy(c.cfg, c.struct, src, dst, self.status, seq_lens=lens)
 
     def reserve(self, seq_lens, new_lens, stream=None) -> None:
         """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence; shared, partly
         filled blocks are copied on write."""
-        _lib.mla_blocks_reserve(self.table, self.refs, self._int32(seq_lens), self._int32(new_lens), self.table,
-                                self.refs, self.copies, self.status, self.workspace, stream=stream)
-        self._move(stream)
+        with self._on(stream):
+            _lib.mla_blocks_reserve(self.table, self.refs, self._int32(seq_lens), self._int32(new_lens), self.table,
+                                    self.refs, self.copies, self.status, self.workspace)
+            self._move()
 
     def trim(self, seq_lens, n_sink: int, window: int, stream=None) -> None:
         """Releases the blocks that mla_decode_window does not read any more; a sequence of
         length 0 is freed."""
-        _lib.mla_blocks_trim(self.table, self.refs, self._int32(seq_lens), n_sink, window, self.table, self.refs,
-                             self.status, stream=stream)
+        with self._on(stream):
+            _lib.mla_blocks_trim(self.table, self.refs, self._int32(seq_lens), n_sink, window, self.table, self.refs,
+                                 self.status)
 
     def compact(self, stream=None) -> None:
         """Moves the blocks in use to the front of the pool."""
-        _lib.mla_blocks_compact(self.table, self.refs, self.table, self.refs, self.copies, self.status,
-                                self.workspace, stream=stream)
-        self._move(stream)
+        with self._on(stream):
+            _lib.mla_blocks_compact(self.table, self.refs, self.table, self.refs, self.copies, self.status,
+                                    self.workspace)
+            self._move()
 
     def errors(self) -> int:
         """The error bits (MLA_DEVERR_*) since the last call of this method."""

@@ -517,14 +517,19 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
 
 // ------------------------------------------------------------------ residual ring
 __global__ void __launch_bounds__(256) ring_kernel(mla_cache_t c, uint32_t row_bytes, const int32_t* __restrict__ src,
-                                                   const int32_t* __restrict__ dst, int n, int32_t* status) {
+                                                   const int32_t* __restrict__ dst, int n,
+                                                   const int32_t* __restrict__ seq_lens, int32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x;
   if (r == 0) check_rows(dst, n, c.B, status, threadIdx.x, blockDim.x);
   __shared__ int s_pair;
   if (threadIdx.x < 32) {
-    const int i = pair_of(src, dst, n, r, c.B, status);
+    int i = pair_of(src, dst, n, r, c.B, status);
+    if (i >= 0 && seq_lens && (unsigned)seq_lens[src[i]] > (unsigned)c.T_cap) {   // the fork skips the pair too
+      if (threadIdx.x == 0) flag(status, MLA_DEVERR_SEQ_LEN);
+      i = -1;
+    }
     if (threadIdx.x == 0) s_pair = i;
   }
   __syncthreads();
@@ -659,14 +664,14 @@ mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, 
 }
 
 mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src, const int32_t* dst,
-                           int32_t n, int32_t* status, void* stream) {
+                           int32_t n, const int32_t* seq_lens, int32_t* status, void* stream) {
   mla_status_t st = mla_validate_config(cfg);
   if (st != MLA_OK) return st;
   if ((st = mla_validate_cache(*cfg, cache)) != MLA_OK) return st;
   if (!cache->c_resid || !src || !dst || !status || n <= 0) return MLA_ERR_INVALID_ARG;
-  if (!aligned4(src) || !aligned4(dst) || !aligned4(status)) return MLA_ERR_ALIGNMENT;
+  if (!aligned4(src) || !aligned4(dst) || !aligned4(status) || !aligned4(seq_lens)) return MLA_ERR_ALIGNMENT;
   return cuda_status(mla_launch_kernel(ring_kernel, dim3(cache->B), dim3(256), 0, (cudaStream_t)stream, true, *cache,
-                                       (uint32_t)cfg->d_c * 2, src, dst, n, status));
+                                       (uint32_t)cfg->d_c * 2, src, dst, n, seq_lens, status));
 }
 
 }  // extern "C"

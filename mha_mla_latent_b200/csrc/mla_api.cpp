@@ -105,7 +105,8 @@ void free_plan(mla_plan* p) {
 
 // The decode kernel a call runs: the tensor-core kernel where the plan, cache and options
 // allow it, else the CUDA-core kernel.  MLA_OK, or the status that refuses the call.
-// Kernel ids of the decode layout: 1 CUDA cores, 2 tcgen05 token rows, 4 tcgen05 head rows.
+// Kernel ids of the decode layout: 1 CUDA cores, 2 tcgen05 token rows, 4 tcgen05 head rows, 5 the
+// windowed decode (token rows with streams).
 mla_status_t mla_pick_decode_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel) {
   *kernel = 1;
   const bool head_rows = mla_decode_t_supported(p, c);
@@ -383,6 +384,12 @@ mla_status_t pick_kernel(const mla_plan& p, const mla_cache_t& c, int* kernel) {
   return mla_pick_decode_kernel(p, c, kernel);
 }
 
+// Launches go to the current device; a plan's weights are on its own.
+bool on_device(const mla_plan& p) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == p.device;
+}
+
 // The window arguments of a call, cut to the capacity (no position lies beyond it).
 MlaWindow window_of(const mla_cache_t& c, int32_t n_sink, int32_t window) {
   MlaWindow w;
@@ -437,6 +444,7 @@ mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache,
   if (B > cache->B) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)seq_lens & 3))
     return MLA_ERR_ALIGNMENT;
+  if (!on_device(*plan)) return MLA_ERR_INVALID_ARG;
   int kernel = 1;
   if ((st = mla_pick_window_kernel(*plan, *cache, &kernel)) != MLA_OK) return st;
   DecodeLayout L = mla_decode_layout(*plan, B, kernel);
@@ -459,6 +467,7 @@ mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* 
   if (B > cache->B || Q > cache->T_cap) return MLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)seq_lens & 3))
     return MLA_ERR_ALIGNMENT;
+  if (!on_device(*plan)) return MLA_ERR_INVALID_ARG;
   if (!mla_chunk_supported(*plan, *cache) || plan->opt_kernel == 1 || plan->opt_kernel == 2) return MLA_ERR_UNSUPPORTED;
   DecodeLayout L = mla_chunk_layout(*plan, B, Q);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;

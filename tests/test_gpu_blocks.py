@@ -298,6 +298,48 @@ def test_ring_copy():
     assert status[1] == mla.MLA_DEVERR_ROW
 
 
+def test_fork_leaves_skipped_rings():
+    """A pair that the fork skips for its source's length keeps its ring as well."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(d_c=96, cache="int4_r128", seed=3)
+    pool = BlockPool(4, 256, 8)
+    cache = pool.layer(layer.config(mla))
+    cache.c_resid.copy_(torch.randn_like(cache.c_resid))
+    ring, table = cache.c_resid.clone(), pool.table.clone()
+    pool.fork([0, 2], [1, 3], [257, 0, 100, 0])
+    torch.cuda.synchronize()
+    ring[3] = ring[2]
+    assert torch.equal(cache.c_resid, ring) and torch.equal(pool.table, table)
+    assert pool.errors() == mla.MLA_DEVERR_SEQ_LEN
+
+
+def test_pool_calls_on_another_stream():
+    """Arguments that a call has to convert are converted on the call's stream, not on a busy one."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(d_c=64, seed=3)
+    pool = BlockPool(4, 1024, 32)
+    cache = pool.layer(layer.config(mla))
+    i64 = lambda *x: torch.tensor(x, device="cuda")  # noqa: E731
+    zero, lens, more, src, dst = i64(0, 0, 0, 0), i64(300, 0, 130, 0), i64(301, 301, 131, 131), i64(0, 2), i64(1, 3)
+    forked = i64(300, 300, 130, 130)
+    cache.c_kv.normal_()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(400_000_000)   # the current stream is busy from here on
+    for stream, call in [(side, lambda s: pool.reserve(zero, lens, stream=s)), (side, lambda s: pool.fork(src, dst, lens, stream=s)),
+                         (side.cuda_stream, lambda s: pool.reserve(forked, more, stream=s)),
+                         (side.cuda_stream, lambda s: pool.trim(more, 0, 150, stream=s)), (side, lambda s: pool.compact(stream=s))]:
+        call(stream)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        assert pool.errors() == 0
+        # rows [0 1 5] [0 1 2] [3 6] [3 4] with 2 and 4 copied on write; block 0 hidden by the window, 6 moved there
+        assert pool.table[:, :3].tolist() == [[-1, 1, 5], [-1, 1, 2], [3, 0, -1], [3, 4, -1]] and pool.in_use() == 6
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("kind", [dict(d_c=64), dict(d_c=128, cache="int4_r128")], ids=["bf16", "int4_r128"])
 def test_serving_run(kind):
     """Two prompts, three samples of each by forking, steps with room made, appended, attended

@@ -72,7 +72,7 @@ def test_copy_calls_refuse_bad_arguments(mla):
     assert copy(ring, paged) == mla.MLA_ERR_INVALID_ARG            # no scales, no ring
     assert copy(cfg, paged, P + 1) == mla.MLA_ERR_ALIGNMENT
     assert mla._lib.mla_blocks_copy(None, ctypes.byref(paged), P, 4, P, None) == mla.MLA_ERR_INVALID_ARG
-    rc = lambda cfg, c: mla._lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(c), P, P, 1, P, None)  # noqa: E731
+    rc = lambda cfg, c: mla._lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(c), P, P, 1, None, P, None)  # noqa: E731
     assert rc(cfg, flat) == mla.MLA_ERR_INVALID_ARG                # no residual window
     full = mla.MlaCache(P, 2 * P, 3 * P, 2, 256, 4 * P, None)
     assert rc(ring, full) == mla.MLA_ERR_INVALID_ARG
@@ -85,6 +85,17 @@ def test_binding_checks_tensors(mla):
         mla.mla_blocks_trim(t, r, r[:2], 0, 4, t, r, st)
     with pytest.raises(ValueError):   # int64 lengths
         mla.mla_blocks_trim(t.long(), r, r[:2], 0, 4, t, r, st)
+
+
+def test_tokens_without_a_block(mla):
+    from mha_mla_latent_b200.cache import LatentCache
+    c = LatentCache(mla.make_config(64, 8, 4, 64, 4, 64), 1, 256, "cpu", block_table=[[1, -1]], n_blocks=2)
+    c.set_latent_rows(0, 120, torch.ones(8, 64))
+    assert c.latent_rows(0, 120, 128).eq(1).all()
+    with pytest.raises(ValueError):   # not the pool's last block
+        c.latent_rows(0, 120, 129)
+    with pytest.raises(ValueError):
+        c.set_latent_rows(0, 128, torch.ones(1, 64))
 
 
 def test_pool_refuses_bad_sizes(mla):
