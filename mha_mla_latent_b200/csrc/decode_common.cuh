@@ -228,15 +228,16 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
 struct SeqUnits {
   int L = 0, len = 0, n = 0;   // length, visible tokens, units with the cost (0 for an empty sequence)
 };
-__device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, int cost, MlaWindow win) {
+__device__ __forceinline__ SeqUnits units_of(int L, int T_cap, int tile, int cost, MlaWindow win) {
   SeqUnits s;
-  if (b >= B) return s;
-  const int L = __ldg(seq_lens + b);
   if (L <= 0 || L > T_cap) return s;
   s.L = L;
   s.len = unit_span(L, 1, tile, win).len;
   s.n = (s.len + tile - 1) / tile + cost;
   return s;
+}
+__device__ __forceinline__ SeqUnits seq_units(const int32_t* __restrict__ seq_lens, int b, int B, int T_cap, int tile, int cost, MlaWindow win) {
+  return b < B ? units_of(__ldg(seq_lens + b), T_cap, tile, cost, win) : SeqUnits();
 }
 // Workers that get units: no more than there are units, so that none in between is empty.
 __device__ __forceinline__ int busy_workers(int total, int G) { return min(total, G); }

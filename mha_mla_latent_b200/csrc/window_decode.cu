@@ -231,6 +231,58 @@ __device__ __forceinline__ int worker_pieces(const Args& a, int w, int4* list, i
   return s_misc[1];
 }
 
+// The same for up to kWarpSeqs sequences, by one warp, while the others set the CTA up; n and
+// slot0 go to s_misc.  (Most CTAs can start only when the absorption's have left their SMs, so
+// what they do before their first copy counts: barriers of the whole CTA here cost 1 us.)
+constexpr int kWarpSeqs = 128;
+__device__ __forceinline__ void warp_pieces(const Args& a, int w, int4* list, int* s_misc) {
+  constexpr int K = kWarpSeqs / 32;
+  const int lane = threadIdx.x & 31;
+  int L[K], ex[K], total = 0;
+  SeqUnits u[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) L[k] = 32 * k + lane < a.B ? __ldg(a.seq_lens + 32 * k + lane) : 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    u[k] = units_of(L[k], a.T_cap, kUnit, a.cost, a.win);
+    ex[k] = total;
+    if (32 * k >= a.B) continue;
+    int x = u[k].n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    ex[k] += x - u[k].n;
+    total += __shfl_sync(0xffffffffu, x, 31);
+  }
+  const int busy = busy_workers(total, a.workers);
+  int slot0 = 0, n = 0;
+  if (w < busy) {
+    const int w0 = (int)worker_begin(w, total, busy), w1 = (int)worker_begin(w + 1, total, busy);
+    int ne0 = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (32 * k >= a.B) continue;
+      const uint32_t some = __ballot_sync(0xffffffffu, u[k].n > 0);
+      const int ne = ne0 + __popc(some & ((1u << lane) - 1)), first = ex[k] + a.cost;   // where the sequence's own units begin
+      const bool in = u[k].n > 0 && first < w1 && ex[k] + u[k].n > w0;
+      const uint32_t mine = __ballot_sync(0xffffffffu, in);
+      if (mine && n == 0) slot0 = w + __shfl_sync(0xffffffffu, ne, __ffs(mine) - 1);
+      if (in) {
+        const int4 p = make_int4(32 * k + lane, max(0, w0 - first) * kUnit, min(u[k].len, (w1 - first) * kUnit), L[k]);
+        const int i = w + ne - slot0;
+        if (i < kPieces) list[i] = p;
+        else a.pieces[w + ne] = p;
+      }
+      n += __popc(mine);
+      ne0 += __popc(some);
+    }
+  }
+  __threadfence_block();
+  if (lane == 0) { s_misc[0] = slot0; s_misc[1] = n; }
+}
+
 // N: heads padded to 16 or 32; QB: code width of a quantised latent (4 or 2), 0 for bf16.
 template <int N, int QB>
 __global__ void __launch_bounds__(kThreadsOf<QB>, 1)
@@ -249,9 +301,24 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
   constexpr uint32_t kPLayout = N == 32 ? (uint32_t)kLayoutSW64 : 6u;   // 64- or 32-byte swizzle
   const int NC = a.NC, NK = a.NK, NRAW = a.NRAW;
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < kBars; ++i) {
+  __shared__ int s_warp[32], s_misc[2];
+  int4* list = reinterpret_cast<int4*>(smem + a.off_list);
+  const bool by_warp = a.B <= kWarpSeqs;
+  // The kernel ahead is this call's absorption, which started once everything before it was
+  // done: lengths and block table can be read now.
+  if (warp == 0) {
+    if (by_warp) warp_pieces(a, blockIdx.x, list, s_misc);
+    if (lane == 0) {
+      *abort_flag = 0;
+      tma_prefetch_desc(&tm_c);
+      tma_prefetch_desc(&tm_kr);
+      tma_prefetch_desc(&tm_q);
+    }
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), kCols);
+    tmem_relinquish();
+  } else if (warp == 2) {
+    for (int i = lane; i < kBars; i += 32) {
       int n = 1;
       if (i >= kCFull && i < kCEmpty && QB) n = 4;      // the dequantising warps
       if (i >= kREmpty && i < kSFull) n = 4;
@@ -261,31 +328,19 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       mbar_init(bar(i), n);
     }
     fence_mbar_init();
-  }
-  // query rows past the last head and the zero blocks of the RoPE operand stay zero
-  for (uint32_t i = threadIdx.x; i < (a.off_p - a.off_q) / 16; i += kThreadsOf<QB>)
-    reinterpret_cast<uint4*>(smem + a.off_q)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_c);
-    tma_prefetch_desc(&tm_kr);
-    tma_prefetch_desc(&tm_q);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(s_tmem), kCols);
-    tmem_relinquish();
+  } else {
+    // query rows past the last head and the zero blocks of the RoPE operand stay zero
+    for (uint32_t i = threadIdx.x - 96; i < (a.off_p - a.off_q) / 16; i += kThreadsOf<QB> - 96)
+      reinterpret_cast<uint4*>(smem + a.off_q)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const uint32_t c_bytes = (uint32_t)a.n_cbox * kSlot;
-  // The kernel ahead is this call's absorption, which started once everything before it was
-  // done: lengths and block table can be read now.
-  __shared__ int s_warp[32], s_misc[2];
-  int4* list = reinterpret_cast<int4*>(smem + a.off_list);
-  int slot0 = 0;
-  const int n_pieces = worker_pieces(a, blockIdx.x, list, &slot0, s_warp, s_misc);
+  int slot0 = s_misc[0], n_pieces = s_misc[1];
+  if (!by_warp) n_pieces = worker_pieces(a, blockIdx.x, list, &slot0, s_warp, s_misc);
   // Registers with a quantised latent: 512 threads x 128 = 65536 = 128 x (88 + 168 + 168 + 88).
   if (warp < 4) {
     if (QB) setmaxnreg_dec<88>();
@@ -337,7 +392,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
       bool ok = true;
       if (wq.valid()) {
         pdl_wait();
-        load_q();
+        load_q();   // ahead of the first tile: behind it, ragged Llama-shaped sequences take 21.3 us instead of 20.3
       }
       while (ok && (wc.valid() || wk.valid() || wq.valid())) {
         bool progress = false;
@@ -983,11 +1038,13 @@ __global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) 
 
 // ------------------------------------------------------------------ merge of the pieces, W_uv
 // out[row][d] = sum_c (sum_j 2^(m_j - M) O_j[c] / sum_j 2^(m_j - M) l_j) W_uv[g][c][d] for 16 rows
-// (sequence, query head of KV head g) and 64 columns per CTA.  Latency bound: the W_uv chunk and
-// the pieces' slots are fetched and counted before the attention kernel is waited for, and a
-// warp, which merges one row, has the partials of four pieces in flight.  The merged latent goes into the warp
+// (sequence, query head of KV head g) and 64 columns per CTA.  Latency bound: the W_uv chunk is
+// fetched and the pieces' slots are counted before the attention kernel is waited for, and a
+// warp, which merges one row, has eight 16-byte loads per lane in flight: 4, 8 or 16 pieces of
+// up to 256, 128 or 64 columns (CP quads of columns; with twice the loads only one CTA fits an
+// SM, and 32 sequences at d_c = 256 take 2 us more).  The merged latent goes into the warp
 // products as two bf16 halves, so its rounding does not count.
-constexpr int kMRows = 16, kMCols = 64, kMThreads = 512, kMBatch = 4;
+constexpr int kMRows = 16, kMCols = 64, kMThreads = 512, kMSlots = 8;
 struct MergeArgs {
   int B, H, G, n_kv, d_c, d_h, P, workers, T_cap, cost;
   MlaWindow win;
@@ -999,10 +1056,9 @@ struct MergeArgs {
   int32_t* err;
 };
 
-__global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
+template <int CP>
+__global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(MergeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_warp[32];
-  __shared__ int3 s_seq[kMRows];   // first unit, units, non-empty sequences before it
   using bf16 = __nv_bfloat16;
   constexpr int WLD = kMCols + 8;
   const int ALD = a.d_c + 8;
@@ -1020,47 +1076,58 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
     cp_async16(smem_u32(sw + c * WLD + d), ok ? (const void*)(W + (size_t)c * a.d_h + d0 + d) : a.W_uv, ok ? 16u : 0u);
   }
   cp_async_commit();
-  const int b_first = row0 / a.G;
-  int total = 0, ne = 0;
-  for (int base = 0; base < a.B; base += kMThreads) {
-    const SeqUnits u = seq_units(a.seq_lens, base + tid, a.B, a.T_cap, kUnit, a.cost, a.win);
-    int tot_u, tot_ne;
-    const int ex_u = block_exscan(u.n, &tot_u, s_warp), ex_ne = block_exscan(u.n > 0 ? 1 : 0, &tot_ne, s_warp);
-    if (blockIdx.x == 0 && base + tid < a.B && (unsigned)__ldg(a.seq_lens + base + tid) > (unsigned)a.T_cap)
-      raise_error(a.err, MLA_DEVERR_SEQ_LEN);   // treated as empty
-    const int k = base + tid - b_first;
-    if (k >= 0 && k < kMRows && base + tid < a.B) s_seq[k] = make_int3(total + ex_u, u.n, ne + ex_ne);
-    total += tot_u;
-    ne += tot_ne;
+  // Each warp finds its row's sequence among the units by itself: the last CTAs start when the
+  // attention's have left their SMs, so barriers here cost time.
+  const int r = warp, row = row0 + r, b = row / a.G;
+  int total = 0, before = 0, units = 0, ne = 0;   // units of all, of the sequences before b, of b; non-empty ones before b
+  for (int base = 0; base < a.B; base += 128) {
+    int L[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int v = base + 32 * k + lane;
+      L[k] = v < a.B ? __ldg(a.seq_lens + v) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int v = base + 32 * k + lane, n = units_of(L[k], a.T_cap, kUnit, a.cost, a.win).n;
+      if (base + 32 * k >= a.B) continue;
+      if (blockIdx.x == 0 && warp == 0 && (unsigned)L[k] > (unsigned)a.T_cap) raise_error(a.err, MLA_DEVERR_SEQ_LEN);   // treated as empty
+      total += __reduce_add_sync(0xffffffffu, n);
+      before += __reduce_add_sync(0xffffffffu, v < b ? n : 0);
+      units += __reduce_add_sync(0xffffffffu, v == b ? n : 0);
+      ne += __popc(__ballot_sync(0xffffffffu, v < b && n > 0));
+    }
   }
-  __syncthreads();
   const int busy = busy_workers(total, a.workers);
   pdl_wait();   // the partials
   pdl_trigger();
   {   // a row per warp
-    const int r = warp, row = row0 + r;
-    float acc[8] = {};   // columns 4 lane + 0..3 and 128 + 4 lane + 0..3
+    constexpr int kBatch = kMSlots * 32 / CP;         // pieces per batch
+    constexpr int kAcc = CP > 32 ? 2 : 1;             // quads of columns per lane
+    const int quad = lane % CP, sub = lane / CP;      // (CP = 16: two pieces side by side)
+    float4 acc[kAcc];
+#pragma unroll
+    for (int e = 0; e < kAcc; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows_g) {
-      const int b = row / a.G, h = g * a.G + row % a.G;
-      const int3 sq = s_seq[b - b_first];
+      const int h = g * a.G + row % a.G;
       int first = 0, np = 0;
-      if (sq.y > 0) {
-        const int w0 = worker_of(sq.x + a.cost, total, busy), w1 = worker_of(sq.x + sq.y - 1, total, busy);
-        first = w0 + sq.z;
+      if (units > 0) {
+        const int w0 = worker_of(before + a.cost, total, busy), w1 = worker_of(before + units - 1, total, busy);
+        first = w0 + ne;
         np = w1 - w0 + 1;
       }
       const float2* ml = reinterpret_cast<const float2*>(a.mlpart) + (size_t)h * a.P + first;
-      const float* op = a.opart + ((size_t)first * a.H + h) * a.d_c + 4 * lane;
+      const float* op = a.opart + ((size_t)first * a.H + h) * a.d_c + 4 * quad;
       const size_t step = (size_t)a.H * a.d_c;
-      const bool c0 = 4 * lane < a.d_c, c1 = 128 + 4 * lane < a.d_c;
-      float4 v[kMBatch][2];
-      auto fetch = [&](int k) {   // pieces k .. k + kMBatch - 1
+      float4 v[kMSlots];
+      // slot s of the batch from piece k on: its piece, and the lane's quad of columns there
+      auto piece = [&](int k, int s) { return k + (CP > 32 ? s / 2 : CP == 32 ? s : 2 * s + sub); };
+      auto fetch = [&](int k) {
 #pragma unroll
-        for (int i = 0; i < kMBatch; ++i) {
-          v[i][0] = v[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float* p = op + (size_t)(k + i) * step;
-          if (k + i < np && c0) v[i][0] = __ldcg(reinterpret_cast<const float4*>(p));
-          if (k + i < np && c1) v[i][1] = __ldcg(reinterpret_cast<const float4*>(p + 128));
+        for (int s = 0; s < kMSlots; ++s) {
+          const int c = 128 * (s % kAcc);
+          v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (piece(k, s) < np && 4 * quad + c < a.d_c) v[s] = __ldcg(reinterpret_cast<const float4*>(op + piece(k, s) * step + c));
         }
       };
       fetch(0);   // in the same round trip as the maxima
@@ -1071,7 +1138,7 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       float wt = 0.f, den = 0.f;
 #pragma unroll 1
-      for (int k = 0; k < np; k += kMBatch) {
+      for (int k = 0; k < np; k += kBatch) {
         if ((k & 31) == 0) {   // the weights of pieces k .. k + 31, one per lane
           if (k > 0) mine = k + lane < np ? __ldcg(ml + k + lane) : make_float2(-INFINITY, 0.f);
           wt = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
@@ -1079,31 +1146,31 @@ __global__ void __launch_bounds__(kMThreads) window_merge_kernel(MergeArgs a) {
         }
         if (k > 0) fetch(k);
 #pragma unroll
-        for (int i = 0; i < kMBatch; ++i) {
-          const float wk = __shfl_sync(0xffffffffu, wt, (k + i) & 31);   // 0 past the last piece
-          acc[0] += wk * v[i][0].x; acc[1] += wk * v[i][0].y; acc[2] += wk * v[i][0].z; acc[3] += wk * v[i][0].w;
-          acc[4] += wk * v[i][1].x; acc[5] += wk * v[i][1].y; acc[6] += wk * v[i][1].z; acc[7] += wk * v[i][1].w;
+        for (int s = 0; s < kMSlots; ++s) {
+          const float wk = __shfl_sync(0xffffffffu, wt, piece(k, s) & 31);   // 0 past the last piece
+          float4& x = acc[s % kAcc];
+          x.x += wk * v[s].x; x.y += wk * v[s].y; x.z += wk * v[s].z; x.w += wk * v[s].w;
         }
+      }
+      if (CP == 16) {
+        acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16); acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
+        acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16); acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
       const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] *= inv;
+      for (int e = 0; e < kAcc; ++e) { acc[e].x *= inv; acc[e].y *= inv; acc[e].z *= inv; acc[e].w *= inv; }
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = 128 * k + 4 * lane;
-      if (c >= a.d_c) continue;
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = acc[4 * k + 2 * e], y = acc[4 * k + 2 * e + 1];
-        hi[e] = pack2(x, y);
-        lo[e] = pack2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
-      }
-      *reinterpret_cast<uint2*>(shi + r * ALD + c) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(slo + r * ALD + c) = make_uint2(lo[0], lo[1]);
+    for (int e = 0; e < kAcc; ++e) {
+      const int c = 128 * e + 4 * quad;
+      if (c >= a.d_c || sub > 0) continue;
+      const uint32_t h0 = pack2(acc[e].x, acc[e].y), h1 = pack2(acc[e].z, acc[e].w);
+      const uint32_t l0 = pack2(acc[e].x - __uint_as_float(h0 << 16), acc[e].y - __uint_as_float(h0 & 0xFFFF0000u));
+      const uint32_t l1 = pack2(acc[e].z - __uint_as_float(h1 << 16), acc[e].w - __uint_as_float(h1 & 0xFFFF0000u));
+      *reinterpret_cast<uint2*>(shi + r * ALD + c) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(slo + r * ALD + c) = make_uint2(l0, l1);
     }
   }
   cp_async_wait_all();
@@ -1278,10 +1345,11 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   m.W_uv = (const __nv_bfloat16*)p.W_uv; m.out = (__nv_bfloat16*)out; m.err = p.err;
   const size_t smem = sizeof(__nv_bfloat16) * ((size_t)cfg.d_c * (kMCols + 8) + 2 * (size_t)kMRows * (cfg.d_c + 8));
   const int n_rb = (B * a.G + kMRows - 1) / kMRows, n_cc = (cfg.head_dim + kMCols - 1) / kMCols;
-  e = mla_smem_limit((const void*)window_merge_kernel, smem);
+  const auto merge = cfg.d_c <= 64 ? window_merge_kernel<16> : cfg.d_c <= 128 ? window_merge_kernel<32> : window_merge_kernel<64>;
+  e = mla_smem_limit((const void*)merge, smem);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfCombine, false, s);
   if (e == cudaSuccess)
-    e = mla_launch_kernel(window_merge_kernel, dim3(cfg.n_kv_heads * n_rb * n_cc), dim3(kMThreads), smem, s, p.opt_pdl, m);
+    e = mla_launch_kernel(merge, dim3(cfg.n_kv_heads * n_rb * n_cc), dim3(kMThreads), smem, s, p.opt_pdl, m);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfCombine, true, s);
   return e;
 }
