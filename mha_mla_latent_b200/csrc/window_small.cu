@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) window_small_kernel(const __grid_con
       }
 #pragma unroll
       for (int k = 0; k < kFly; ++k) {
+        if (i0 + k * kWarps * tpw >= n) break;   // (the whole warp)
         float acc[G] = {}, c0[V];
         unpack(v[k], c0);
         if (sub < units) {   // (a lane past the row's end holds another unit, which may not be finite)
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads) window_small_kernel(const __grid_con
       const int u = u0 + (groups > 1 ? tid % units : tid), grp = groups > 1 ? tid / units : 0;
       float acc[G][V] = {};
       if (u < units && grp < groups) {
-        constexpr int kFly = 8;   // rows in flight: past the end the last row, with weight 0
+        constexpr int kFly = 8;   // rows in flight: past the end the last row again
         for (int i0 = grp; i0 < n; i0 += kFly * groups) {
           uint4 v[kFly];
 #pragma unroll
@@ -232,11 +233,12 @@ __global__ void __launch_bounds__(kThreads) window_small_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < kFly; ++k) {
             const int i = i0 + k * groups;
+            if (i >= n) break;
             float c[V];
             unpack(v[k], c);
 #pragma unroll
             for (int h = 0; h < G; ++h) {
-              const float p = i < n ? s_p[h * kMaxTokens + i] : 0.f;
+              const float p = s_p[h * kMaxTokens + i];
 #pragma unroll
               for (int e = 0; e < V; ++e) acc[h][e] += p * c[e];
             }
@@ -316,12 +318,12 @@ static bool small_shape(const mla_plan& p) {
 }
 
 // The rule.  Without the tensor-core form (float32, other numbers of kept pairs) it is taken for
-// up to 1152 visible tokens: 6 us against 15 us for the split CUDA-core form at 64 tokens of
-// the tiny float32 layer, 17 us against 24 us at 1000.  Else while a CTA's rows are few (64 KB
+// up to 1152 visible tokens: 5.6 us against 15 us for the split CUDA-core form at 64 tokens of
+// the tiny float32 layer, 17 us against 24 us at 1000.  Else while a CTA's rows are few (66 KB
 // with 64 B for the keys and the look-up of each) and the CTAs run at once: Llama-shaped layer,
-// 4 sequences, one launch against three: d_c = 64 11.2 / 13.4 us at 256 tokens, 15.2 / 15.2 at
-// 512; d_c = 256 10.5 / 16 us at 16 tokens, 18.7 / 16.5 at 128; SmolLM-shaped 13.5 / 13.3 at 512
-// (and 4 us less of the host's time for two launches fewer).
+// 4 sequences, one launch against three: d_c = 64 9.4 / 12.7 us at 256 tokens, 13.4 / 12.8 at
+// 512; d_c = 256 10.0 / 14.5 us at 16 tokens, 16.6 / 14.4 at 128; SmolLM-shaped, 16 sequences
+// 8.8 / 11.9 at 256, 12.6 / 12.1 at 516 (and 4 us less of the host's time for two launches fewer).
 bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win) {
   if (!small_shape(p)) return false;
   const long long tokens = std::min<long long>(c.T_cap, (long long)win.n_sink + win.window);
