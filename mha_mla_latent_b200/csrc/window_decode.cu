@@ -14,15 +14,18 @@
 // and the chain load -> S -> softmax -> O of one overlaps the other's.  The streams' results are
 // merged in tensor memory when a piece (part of one sequence) ends.
 //
-// What bounds it is HBM: the cached rows of the visible tokens, read once.  The products take
-// about a third of that time at d_c = 256 and the softmax a tenth.
+// What bounds it is HBM: the cached rows of the visible tokens, read once (ncu: 1.01 times their
+// bytes).  The products take about a third of that time at d_c = 256 and the softmax a tenth.
+// B200, whole calls: 32 sequences, 4160 visible tokens, 32 heads, d_c = 256: 43 us for 136 MB, of
+// which tiles flow for about 28 (4.9 TB/s); the rest is the hand-over between the three launches,
+// the first tiles and the last tile's chain.  64 sequences, 4005 tokens, 4-bit d_c = 128: 56 us.
 //
 // The running maximum is raised lazily: a thread that sees a score above m[h] + kTau reports it
 // in the group's per-tile barrier (an OR over its 128 threads) and the group then takes the
 // tile's maxima, rescales its accumulator and goes on.  Between raises P stays below 2^kTau.
 //
-// Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 2-3 dequantise a quantised latent,
-// warps 4-7 and 8-11 the softmax groups.  Every wait is bounded; a group leaves its loop only
+// Roles: warp 0 TMA producer, warp 1 MMA issuer, warps 4-7 and 8-11 the softmax groups,
+// warps 12-15 dequantise a quantised latent.  Every wait is bounded; a group leaves its loop only
 // where all of it does (the barrier carries the failure too).
 #include <cuda.h>
 

@@ -698,7 +698,7 @@ static Layout layout(int dcp) {
 
 // KV heads per unit: few of them re-read the window more often but fill the machine and its
 // rows' products; the candidate with the least (rounds of CTAs) x (time of a unit) is taken.
-// Times in units of a tile's products at d_c = 256; see the launch comment for the measurement.
+// Times in units of a tile's products at d_c = 256: a tile 1, a unit's ends 2, a KV head's weights 2.
 static int pick_gb(int B, int Q, int G, int n_kv, int tiles, int sms) {
   int best = 1;
   double best_cost = 1e30;
