@@ -234,7 +234,7 @@ __device__ __forceinline__ Row row_of(const Table& t, const int32_t* refs, const
   return r;
 }
 
-// Latency bound (5 to 6 us on 32 to 160 rows).  CTA 0 decides while the others copy the table and the counts (calls that are not in place);
+// Latency bound (5 to 6 us on 16 to 160 rows, 11 us with 65536 blocks).  CTA 0 decides while the others copy the table and the counts (calls that are not in place);
 // after the cluster's barrier CTA 0 writes what changes.  Decisions read the input only.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_lens,
@@ -469,29 +469,27 @@ struct CopyArgs {
   int32_t* status;
   char* base[3];        // c_kv, c_scales, k_rope (null: none)
   uint32_t row[3];      // bytes per token row
+  uint32_t chunks[3];   // steps per block
 };
-constexpr int kCopyThreads = 256, kCopyCtas = 4;             // threads, CTAs per SM
-constexpr int kCopyVec = 8;                                  // 16-byte loads a thread has in flight
-constexpr uint32_t kChunk = kCopyThreads * kCopyVec * 16;    // bytes per CTA step: 32 KB
+constexpr int kCopyThreads = 256, kCopyCtas = 8;             // threads, CTAs per SM
+constexpr int kCopyVec = 4;                                  // 16-byte loads a thread has in flight
+constexpr uint32_t kChunk = kCopyThreads * kCopyVec * 16;    // bytes per CTA step: 16 KB
 
 // Work items: (copy, array, chunk); a block's rows are contiguous in each array.  Bound by HBM:
-// 134 MB moved in 48 us, 86% of the measured copy rate.
+// 134 MB moved in 47 us, 88% of the measured copy rate
+// (32 KB steps of 4 CTAs 48 us; one warp with 16 KB bulk copies through a ring in shared memory
+// 46 to 49, depending on how much is in flight).
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
   pdl_wait();
   pdl_trigger();
   const int n = min(__ldcg(a.status), a.max_copies);
-  uint32_t chunks[3], per = 0;
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    chunks[k] = a.base[k] ? (a.row[k] * kBT + kChunk - 1) / kChunk : 0;
-    per += chunks[k];
-  }
+  const uint32_t per = a.chunks[0] + a.chunks[1] + a.chunks[2];
   const long long items = (long long)n * per;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int32_t* c = a.copies + 3 * (it / per);
     uint32_t chunk = (uint32_t)(it % per);
     int k = 0;
-    while (chunk >= chunks[k]) chunk -= chunks[k++];
+    while (chunk >= a.chunks[k]) chunk -= a.chunks[k++];
     const int src = c[0], dst = c[1], rows = c[2];
     if (src < 0 || src >= a.n_blocks || dst < 0 || dst >= a.n_blocks || rows < 0 || rows > kBT) {
       if (threadIdx.x == 0) flag(a.status, MLA_DEVERR_BLOCK);
@@ -658,10 +656,15 @@ mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t* cache, 
   a.row[1] = quant ? (uint32_t)(cfg->d_c / 32 * 2) : 0;
   a.base[2] = cfg->r_pairs > 0 ? (char*)cache->k_rope : nullptr;
   a.row[2] = (uint32_t)(cfg->n_kv_heads * 2 * cfg->r_pairs) * eb;
+  long long items = 0;   // no CTAs without work where the list is short
+  for (int k = 0; k < 3; ++k) {
+    a.chunks[k] = a.base[k] ? (a.row[k] * kBT + kChunk - 1) / kChunk : 0;
+    items += (long long)a.chunks[k] * max_copies;
+  }
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return MLA_ERR_CUDA;
-  return cuda_status(mla_launch_kernel(copy_kernel, dim3(kCopyCtas * sms), dim3(kCopyThreads), 0, (cudaStream_t)stream, true, a));
+  return cuda_status(mla_launch_kernel(copy_kernel, dim3((unsigned)std::min<long long>(items, kCopyCtas * sms)), dim3(kCopyThreads), 0, (cudaStream_t)stream, true, a));
 }
 
 mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src, const int32_t* dst,
