@@ -117,6 +117,8 @@ __device__ inline void build_schedule(const int32_t* __restrict__ seq_lens, int 
     int nti = 0;
     if (b < B) {
       int L = unit_len(seq_lens, b, q_chunk, q_block);
+      // a sequence beyond the capacity is empty as a whole, its chunk's first queries too
+      if (q_chunk > 1 && __ldg(seq_lens + b / ((q_chunk + q_block - 1) / q_block)) > T_cap) L = -1;
       if (L < 0 || L > T_cap) { raise_error(err, MLA_DEVERR_SEQ_LEN); L = 0; }
       L = unit_span(L, unit_queries(b, q_chunk, q_block), tile, win).len;
       nti = (L + tile - 1) / tile;

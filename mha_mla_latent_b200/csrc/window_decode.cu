@@ -173,6 +173,10 @@ __device__ __forceinline__ float columns(float (&x)[N], int lane, F op) {
   return x[0];
 }
 
+// The larger of two streams' maxima, NaN if one is: scores that are not numbers must not pass
+// for a stream without a tile (-inf).
+__device__ __forceinline__ float top_of(float a, float b) { return a != a ? a : b != b ? b : fmaxf(a, b); }
+
 // Barrier of 128 threads that returns the OR of their predicates.
 __device__ __forceinline__ bool group_or(int id, bool p) {
   uint32_t r;
@@ -890,7 +894,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         if (!fail) fail = !warp_wait(kMeet, u & 1);
         const float* t0 = tops + par * 2 * 32;
         if (r < N) {   // a stream without a tile in this piece weighs nothing
-          const float m0 = t0[r], m1 = t0[32 + r], M = fmaxf(m0, m1);
+          const float m0 = t0[r], m1 = t0[32 + r], M = top_of(m0, m1);
           wts[r] = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M);
           wts[32 + r] = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
         }
@@ -917,12 +921,12 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
 #pragma unroll
           for (int e = 0; e < HN; ++e) {
             asm volatile("" : "+r"(o0[e]), "+r"(o1[e]));
-            const float v = (w0[e] > 0.f ? w0[e] * __uint_as_float(o0[e]) : 0.f) + (w1[e] > 0.f ? w1[e] * __uint_as_float(o1[e]) : 0.f);
+            const float v = (w0[e] != 0.f ? w0[e] * __uint_as_float(o0[e]) : 0.f) + (w1[e] != 0.f ? w1[e] * __uint_as_float(o1[e]) : 0.f);
             if (HN * s + e < a.H && blk * 128 + r < a.d_c) dst[(size_t)e * a.d_c] = v;
           }
         }
         if (s == 0 && r < a.H) {
-          const float M = fmaxf(t0[r], t0[32 + r]);
+          const float M = top_of(t0[r], t0[32 + r]);
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

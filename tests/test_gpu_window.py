@@ -359,6 +359,112 @@ def test_without_launch_overlap():
     plan.close()
 
 
+def _poison(cache):
+    """Every row as an earlier owner may have left it: not finite."""
+    for a in (cache.c_kv, cache.c_scales, cache.k_rope):
+        if a is not None:
+            a.fill_(float("nan") if a.is_floating_point() else 0x77)
+
+
+@pytest.mark.parametrize("T_cap", [200, 333])
+@pytest.mark.parametrize("name", ["tiny_f32", "smollm", "llama_dc256", "llama_dc64", "llama_int4", "llama_int2"])
+def test_stale_rows_and_odd_capacity(name, T_cap):
+    """Sequences that end inside a tile, the tile in the next sequence or behind the array; every
+    row that is not a visible token holds NaN.  The largest n_sink and window too."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=17)
+    lens = [T_cap, 70, T_cap - 5, 9, T_cap]
+    B, Q, big = len(lens), 7, 2 ** 31 - 1
+    seqs = [layer.sequence(L) for L in lens]
+    plan = layer.plan(mla)
+    q, qc = layer.queries(B), layer.queries(B, Q)
+    for n_sink, window in [(3, 90), (0, 1), (70, 31), (big, big), (0, big)]:
+        cache = make_cache(mla, layer, B, T_cap, False)
+        _poison(cache)
+        for b, s in enumerate(seqs):
+            store(cache, b, s, hidden_tokens(lens[b], lens[b] - 1, n_sink, window))
+        got = run_decode(mla, layer, cache, lens, q, n_sink, window, plan).double().cpu().numpy()
+        for b, L in enumerate(lens):
+            ref = layer.reference(q[b], seqs[b], L - 1, n_sink, window).numpy()
+            assert_close(got[b], ref, layer.dtype, f"{name} {T_cap} sinks {n_sink} window {window} length {L}")
+        if layer.dtype != "bf16":
+            continue
+        for b, s in enumerate(seqs):
+            store(cache, b, s, hidden_tokens(lens[b], lens[b] - Q, n_sink, window))
+        out = torch.empty_like(qc, device="cuda")
+        ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+        mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), qc.cuda(),
+                                    out, ws, n_sink, window)
+        assert mla.mla_device_error(plan) == 0
+        for b, L in enumerate(lens):
+            for i in (0, Q - 1):
+                ref = layer.reference(qc[b, i], seqs[b], L - Q + i, n_sink, window).numpy()
+                assert_close(out[b, i].double().cpu().numpy(), ref, "bf16", f"{name} {T_cap} chunk {n_sink} {window} {L} {i}")
+    plan.close()
+
+
+@pytest.mark.parametrize("name", ["smollm", "llama_dc256", "llama_int4", "tiny_f32"])
+@pytest.mark.parametrize("splits", [0, 1])
+def test_a_bad_sequence_stays_alone(name, splits):
+    """A sequence whose visible rows are not finite changes no other sequence's bits, with its
+    pieces beside theirs in the same worker too."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=18)
+    lens = [300, 500, 129, 700]
+    B, T_cap, Q = len(lens), 768, 6
+    seqs = [layer.sequence(L) for L in lens]
+    q, qc = layer.queries(B), layer.queries(B, Q)
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_SPLITS, splits)
+    outs = []
+    for bad in (False, True):
+        cache = make_cache(mla, layer, B, T_cap, True)
+        for b, s in enumerate(seqs):
+            store(cache, b, s, torch.arange(lens[b]) if bad and b == 1 else None)
+        o = [run_decode(mla, layer, cache, lens, q, 5, 1000, plan), run_decode(mla, layer, cache, lens, q, 5, 150, plan)]
+        if layer.dtype == "bf16":
+            out = torch.empty_like(qc, device="cuda")
+            ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+            mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                        qc.cuda(), out, ws, 5, 150)
+            o.append(out)
+        outs.append(o)
+    for good, bad in zip(*outs):
+        for b in (0, 2, 3):
+            assert torch.isfinite(good[b].float()).all() and torch.equal(good[b], bad[b])
+        assert not torch.isfinite(bad[1].float()).any()
+    plan.close()
+
+
+def test_short_sequences_in_a_chunk():
+    """Sequences shorter than the chunk (empty ones too) are flagged and give zeros; the others are computed."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=19)
+    lens, Q = [0, 5, 300, 257, 8], 8
+    cache = make_cache(mla, layer, 5, 256, True)
+    seq = layer.sequence(256)
+    for b in (0, 1, 3, 4):
+        store(cache, b, seq)
+    lens[2] = 256
+    store(cache, 2, seq)
+    q = layer.queries(5, Q)
+    plan = layer.plan(mla)
+    for kernel in (0, 3):
+        mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+        out = torch.full_like(q, float("nan"), device="cuda")
+        ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, 5, Q), dtype=torch.uint8, device="cuda")
+        mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(),
+                                    out, ws, 4, 40)
+        assert mla.mla_device_error(plan) == mla.MLA_DEVERR_SEQ_LEN
+        got = out.double().cpu().numpy()
+        assert not got[0].any() and not got[1].any() and not got[3].any()
+        for b in (2, 4):
+            for i in (0, Q - 1):
+                ref = layer.reference(q[b, i], seq, lens[b] - Q + i, 4, 40).numpy()
+                assert_close(got[b, i], ref, "bf16", f"kernel {kernel} {b} {i}")
+    plan.close()
+
+
 def test_out_of_range_length():
     """A length beyond the capacity is flagged and treated as empty; the others are computed."""
     import mha_mla_latent_b200 as mla
