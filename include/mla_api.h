@@ -158,8 +158,8 @@ enum {
                                  then drains its copies, releases its tensor memory and
                                  returns, and the decode output of that call is invalid. */
   MLA_OPT_TEST_SKIP_COPY = 6, /* testing the timeout path only (0 = off, the default): with
-                                 value k > 0 every CTA of the tensor-core kernel leaves out
-                                 the latent copy of its k-th tile, so the waits for that tile
+                                 value k > 0 every CTA of the token-row and the windowed
+                                 tensor-core kernels leaves out the copy of its k-th tile, so the waits for that tile
                                  run out (after MLA_OPT_WAIT_LIMIT_US) and the call reports
                                  MLA_DEVERR_TIMEOUT.  Nothing faults; later calls with the
                                  option cleared run normally. */

@@ -60,6 +60,7 @@ struct Args {
   int n_blk;                              // parts of a latent tile: blocks of 128 columns
   int NC, NK, NRAW;                       // latent tiles, key boxes, code tiles in the rings
   int B, workers, cost;                   // cost of a piece, in units (see seq_units)
+  int skip_tile;                          // testing only: 1-based tile whose latent is not copied (0 = none)
   MlaWindow win;
   int4* pieces;                           // [P] by slot: the pieces past the first kPieces of a worker
   const int32_t* seq_lens;
@@ -407,7 +408,7 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           const int s = rc.slot;
           if (nc < c_ring || ready(QB ? kREmpty + s : kCEmpty + 2 * s + pc, rc.parity ^ 1)) {
             const int units = wc.units(), k1 = min(2 * pc + 2, a.n_cbox);
-            if (elect_one()) {
+            if (nc + 1 != a.skip_tile && elect_one()) {
               if (QB) {
                 const uint32_t dst = sb + a.off_raw + s * a.raw_stage;
                 mbar_expect_tx(bar(kRFull + s), (uint32_t)units * kUnit * a.code_row);
@@ -1304,7 +1305,7 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   a.T_cap = c.T_cap; a.n_cbox = L.n_cbox; a.n_kbox = L.n_kbox; a.kr_rows = L.kr_rows;
   a.NC = L.NC; a.NK = L.NK; a.NRAW = L.NRAW;
   a.n_blk = (L.n_cbox + 1) / 2;
-  a.B = B; a.workers = D.G; a.win = win;
+  a.B = B; a.workers = D.G; a.win = win; a.skip_tile = p.opt_skip_tile;
   // about 5 us, the time a CTA takes for 220 KB; a unit of short rows is bound by latency instead
   a.cost = std::max(2, std::min(8, (int)(3400 / mla_cache_bytes_per_token(&cfg))));
   a.pieces = (int4*)(base + D.off_piece_b);

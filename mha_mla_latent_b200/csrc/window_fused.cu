@@ -56,6 +56,7 @@ struct Args {
   int Q, H, n_kv, G, d_h, d_c, dcp, dhp;   // dcp, dhp: padded to whole 64-column boxes
   int gb, qb, n_gblk, n_qblk;              // KV heads and queries per unit, units per sequence
   int T_cap, NST;
+  int skip_tile;                           // testing only: 1-based tile that is not copied (0 = none)
   float scale;                             // softmax scale x log2(e)
   MlaWindow win;
   const __nv_bfloat16* q;
@@ -210,12 +211,14 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
           if (i < ng) { load_uk(i, s); continue; }
           const uint32_t at = sb + a.off_ring + (uint32_t)s * a.stage;
           if (i < ng + T) {
-            const int t = tile_token(i - ng);
-            const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
-            const int row = lc.pb * lc.cap + lc.pt;
-            mbar_expect_tx(bar(kBarFull + s), (QB ? 0u : (uint32_t)n_cbox * kBox) + kKrTile);
-            for (int k = 0; k < (QB ? 0 : n_cbox); ++k) tma_load_2d(at + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
-            tma_load_2d(at + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
+            if (i - ng + 1 != a.skip_tile) {
+              const int t = tile_token(i - ng);
+              const MlaLoc lc = PAGED ? mla_loc(a.cache, b, t, a.err) : MlaLoc{b, t, a.T_cap};
+              const int row = lc.pb * lc.cap + lc.pt;
+              mbar_expect_tx(bar(kBarFull + s), (QB ? 0u : (uint32_t)n_cbox * kBox) + kKrTile);
+              for (int k = 0; k < (QB ? 0 : n_cbox); ++k) tma_load_2d(at + k * kBox, &tm_c, bar(kBarFull + s), k * 64, row);
+              tma_load_2d(at + n_cbox * kBox, &tm_kr, bar(kBarFull + s), g0 * 8, row);
+            }
           } else {
             const int gi = i - ng - T;
             mbar_expect_tx(bar(kBarFull + s), uv_bytes);
@@ -736,7 +739,7 @@ cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, con
   a.n_qblk = (Q + a.qb - 1) / a.qb;
   const long long units = (long long)B * a.n_gblk * a.n_qblk;
   if (units > INT32_MAX) return cudaErrorInvalidValue;
-  a.T_cap = c.T_cap;
+  a.T_cap = c.T_cap; a.skip_tile = p.opt_skip_tile;
   a.scale = mla::kLog2e * (cfg.softmax_scale > 0.0f ? cfg.softmax_scale : (float)(1.0 / sqrt((double)cfg.head_dim)));
   a.win = win;
   a.q = (const __nv_bfloat16*)q; a.out = (__nv_bfloat16*)out; a.seq_lens = seq_lens;

@@ -566,6 +566,41 @@ def test_graph_replay_and_two_streams():
         p.close()
 
 
+@pytest.mark.parametrize("name,skip,chunk", [("llama_dc256", 1, False), ("llama_dc256", 2, False), ("llama_int4", 1, False),
+                                             ("llama_dc64", 2, True), ("llama_int4_dc256", 1, True)])
+def test_wait_runs_out_then_plan_recovers(name, skip, chunk):
+    """A copy that never comes: every wait behind it is bounded, the call comes back and reports
+    it, and the next one on the same plan is right."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=20)
+    lens, Q = [512, 300], 3 if chunk else 1
+    seqs = [layer.sequence(L) for L in lens]
+    cache = make_cache(mla, layer, 2, 512, True)
+    for b, s in enumerate(seqs):
+        store(cache, b, s)
+    q = layer.queries(2, Q)
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_SPLITS, 1)   # (decode) one CTA with every tile
+    out = torch.empty_like(q, device="cuda")
+    ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, 2, Q), dtype=torch.uint8, device="cuda")
+    call = lambda: mla.mla_decode_chunk_window(  # noqa: E731
+        plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(), out, ws, 10, 400)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_WAIT_LIMIT_US, 2000)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_TEST_SKIP_COPY, skip)
+    call()
+    assert mla.mla_device_error(plan) & mla.MLA_DEVERR_TIMEOUT
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_TEST_SKIP_COPY, 0)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_WAIT_LIMIT_US, 1_000_000)
+    out.fill_(float("nan"))
+    call()
+    assert mla.mla_device_error(plan) == 0
+    for b, L in enumerate(lens):
+        for i in range(Q):
+            ref = layer.reference(q[b, i], seqs[b], L - Q + i, 10, 400).numpy()
+            assert_close(out[b, i].double().cpu().numpy(), ref, "bf16", f"{name} after the timeout {b} {i}")
+    plan.close()
+
+
 def test_refusals():
     import mha_mla_latent_b200 as mla
     layer = Layer(d_c=64, seed=10)
