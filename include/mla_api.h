@@ -512,7 +512,10 @@ MLA_API mla_status_t mla_blocks_copy(const mla_config_t* cfg, const mla_cache_t*
 /* Copy the residual window (MLA_CACHE_INT4_G32_R128: ring rows and their positions) of
  * sequence src[i] to sequence dst[i] in one layer's cache, for a fork.  The pairs that
  * mla_blocks_fork skips with the same arguments are skipped here too, with the same bits set in
- * status[1].
+ * status[1].  With seq_lens, slots that hold a token from seq_lens[src[i]] on become empty (-1)
+ * in sequence dst[i], dst[i] == src[i] included: the prefix was cut, and what the sequence
+ * appends itself takes their place.  (Tokens of the prefix whose ring rows were written over by
+ * those later ones are read from their int4 rows.)
  *   src, dst device [n] int32 in [0, cache->B); seq_lens device [cache->B] int32 or NULL (the
  *   lengths are not looked at).  MLA_ERR_INVALID_ARG for a cache without a ring. */
 MLA_API mla_status_t mla_ring_copy(const mla_config_t* cfg, const mla_cache_t* cache, const int32_t* src,

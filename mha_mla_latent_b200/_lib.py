@@ -393,7 +393,8 @@ def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None
 
 def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None, check=True, seq_lens=None):
     """Copies the residual windows of sequences src to sequences dst in one layer's cache; with
-    the seq_lens of the fork, pairs that it skips for their length are skipped here too."""
+    the seq_lens of the fork, pairs that it skips for their length are skipped here too and
+    tokens behind the length are left out."""
     n = src.numel()
     lens = None if seq_lens is None else _i32(seq_lens, "seq_lens", cache.B)
     st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src", n), _i32(dst, "dst", n), n,

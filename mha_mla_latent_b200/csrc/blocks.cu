@@ -515,6 +515,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
 }
 
 // ------------------------------------------------------------------ residual ring
+// A CTA per ring.  With the lengths, slots that hold a token behind the source's length are
+// empty in the destination: appends only raise a slot's position, so one of a later token would
+// keep the sequence's own token out.
 __global__ void __launch_bounds__(256) ring_kernel(mla_cache_t c, uint32_t row_bytes, const int32_t* __restrict__ src,
                                                    const int32_t* __restrict__ dst, int n,
                                                    const int32_t* __restrict__ seq_lens, int32_t* status) {
@@ -533,13 +536,19 @@ __global__ void __launch_bounds__(256) ring_kernel(mla_cache_t c, uint32_t row_b
   }
   __syncthreads();
   const int i = s_pair;
-  if (i < 0 || src[i] == r) return;
+  if (i < 0) return;
+  const int from = src[i], L = seq_lens ? seq_lens[from] : INT_MAX;
+  // (a row that is cut while others copy from it: they see a position before or after, and
+  // leave it out either way)
+  for (int o = threadIdx.x; o < MLA_RESID_WINDOW; o += blockDim.x) {
+    const int p = c.resid_pos[(size_t)from * MLA_RESID_WINDOW + o];
+    c.resid_pos[(size_t)r * MLA_RESID_WINDOW + o] = p < L ? p : -1;
+  }
+  if (from == r) return;
   const size_t bytes = (size_t)row_bytes * MLA_RESID_WINDOW;   // a multiple of 16: 128 rows
-  const uint4* s = reinterpret_cast<const uint4*>((const char*)c.c_resid + bytes * src[i]);
+  const uint4* s = reinterpret_cast<const uint4*>((const char*)c.c_resid + bytes * from);
   uint4* d = reinterpret_cast<uint4*>((char*)c.c_resid + bytes * r);
   for (size_t o = threadIdx.x; o < bytes / 16; o += blockDim.x) d[o] = s[o];
-  for (int o = threadIdx.x; o < MLA_RESID_WINDOW; o += blockDim.x)
-    c.resid_pos[(size_t)r * MLA_RESID_WINDOW + o] = c.resid_pos[(size_t)src[i] * MLA_RESID_WINDOW + o];
 }
 
 // ------------------------------------------------------------------ host side

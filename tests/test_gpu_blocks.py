@@ -463,3 +463,46 @@ def test_pool_calls_in_a_graph():
         torch.cuda.synchronize()
         assert np.array_equal(d.table.cpu().numpy(), table) and np.array_equal(d.refs.cpu().numpy(), refs)
         assert d.status[1] == 0
+
+
+@pytest.mark.parametrize("n", [400, 300])   # with and without ring rows of the prefix left
+def test_ring_of_a_cut_fork(n):
+    """A fork of a shorter prefix than the source's own length takes no ring row of the tokens behind
+    it: what the sequence appends there itself is in the window at full precision, as if the source
+    had never been longer.  Cutting a row to its own length does the same."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(d_c=96, cache="int4_r128", seed=5)
+    cfg = layer.config(mla)
+    g = torch.Generator().manual_seed(1)
+    W = [(torch.randn(64, n, generator=g) * 64 ** -0.5).to(layer.td) for n in (layer.d_c, layer.n_kv * layer.d_h)]
+    plan = mla.mla_plan_create(cfg, *W, torch.from_numpy(layer.pairs), layer.W_uk, layer.W_uv)
+    cut, more = 250, 40
+    x = torch.randn(n, 64, generator=g).to(layer.td).cuda()
+    y = torch.randn(more, 64, generator=g).to(layer.td).cuda()
+    pool = BlockPool(3, 512, 20)
+    cache = pool.layer(cfg)
+    i32 = lambda v: torch.as_tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def append(b, t0, rows):
+        k = rows.shape[0]
+        mla.mla_append(plan, rows, i32([b] * k), i32(range(t0, t0 + k)), cache.struct)
+
+    pool.reserve([0, 0, 0], [n, 0, 0])
+    append(0, 0, x)
+    pool.fork([0, 0], [1, 0], [cut, 0, 0])
+    assert int(cache.resid_pos[:2].max()) < cut
+    kept = torch.arange(min(n - 128, cut), cut)           # ring rows of the prefix that were not written over
+    for b in (0, 1):
+        assert cache.resid_pos[b, kept.cuda() % 128].tolist() == kept.tolist()
+    pool.reserve([cut, cut, 0], [cut + more, cut + more, cut + more])
+    for b in (0, 1):
+        append(b, cut, y)
+    append(2, cut, y)                           # a ring that never held anything else
+    t = torch.arange(cut, cut + more).cuda()
+    torch.cuda.synchronize()
+    for b in (0, 1):
+        assert cache.resid_pos[b, t % 128].tolist() == t.tolist()
+        assert torch.equal(cache.c_resid[b, t % 128], cache.c_resid[2, t % 128])
+    assert pool.errors() == 0 and mla.mla_device_error(plan) == 0
+    plan.close()
