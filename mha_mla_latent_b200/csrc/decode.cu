@@ -318,12 +318,12 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
       if (tid < H) {
         float mx = s_m[tid];
         for (int tt = 0; tt < n; ++tt) mx = fmaxf(mx, s_p[tt * H + tid]);
-        // exp2(-inf) = 0 on the first tile (a tile of the window's walk holds a visible token,
-        // so mx is finite)
-        float al = exp2f(s_m[tid] - mx);
+        // exp2(-inf) = 0 on the first tile, and where every score is -inf so far (an infinite key)
+        const float mb = mx == -INFINITY ? 0.f : mx;
+        float al = exp2f(s_m[tid] - mb);
         float l = s_l[tid] * al;
         for (int tt = 0; tt < n; ++tt) {
-          float p = exp2f(s_p[tt * H + tid] - mx);
+          float p = exp2f(s_p[tt * H + tid] - mb);
           s_p[tt * H + tid] = p;
           l += p;
         }
