@@ -314,7 +314,10 @@ MLA_API mla_status_t mla_decode_chunk(const mla_plan_t* plan, const mla_cache_t*
  * cache needs no block for a run of 128 hidden tokens (mla_blocks_trim releases them; their
  * table entries are not read).  Positions stay those of the whole sequence: the query is
  * rotated at p, the keys keep the rotation they were appended with.  The cost follows the
- * visible tokens, not the length.  With window >= T_cap it is mla_decode's attention.
+ * visible tokens, not the length.  With window >= T_cap it is mla_decode's attention.  A visible
+ * RoPE key that is not finite changes the outputs of its own KV head only, as the definition has
+ * it (a score of -inf weighs nothing, +inf and NaN make a head's output NaN); the rows next to it
+ * then take some milliseconds.
  *   n_sink >= 0, window >= 1; the other arguments, the workspace and L == 0 as for mla_decode
  * Every cache kind and shape that mla_decode's CUDA-core kernel takes, and more heads where a
  * tensor-core kernel does.  Kernel (MLA_OPT_DECODE_KERNEL = 0): one launch on the CUDA cores for

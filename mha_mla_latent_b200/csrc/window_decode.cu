@@ -9,14 +9,16 @@
 //     S[t][h]    = sum_c C[t][c] Q_lat[h][c] + sum_j KR[t][j] Q_rope[h][j]    M = 128, N = heads
 //     O[c][h]   += sum_t C[t][c] P[t][h],   P = 2^(S - m[h])                   M = 128 (twice for d_c > 128)
 // Q_rope is block-diagonal over the KV heads; a box of 64 key columns (8 KV heads) is multiplied
-// with the 16 (or all) heads it concerns only.  O^T needs 32 columns per 128 latent columns, so
+// with the 16 (or all) heads it concerns only.  (The operand's zeros times a key that is not
+// finite are NaN for the heads of the box's other KV heads: rows that come out NaN are computed
+// once more, head by head, when they are merged.)  O^T needs 32 columns per 128 latent columns, so
 // two streams of tiles (even and odd, one softmax group each) keep an accumulator of their own
 // and the chain load -> S -> softmax -> O of one overlaps the other's.  The streams' results are
 // merged in tensor memory when a piece (part of one sequence) ends.
 //
 // What bounds it is HBM: the cached rows of the visible tokens, read once (ncu: 1.01 times their
 // bytes).  The products take about a third of that time at d_c = 256 and the softmax a tenth.
-// B200, whole calls: 32 sequences, 4160 visible tokens, 32 heads, d_c = 256: 43 us for 136 MB, of
+// B200, whole calls: 32 sequences, 4160 visible tokens, 32 heads, d_c = 256: 45 us for 136 MB, of
 // which tiles flow for about 28 (4.9 TB/s); the rest is the hand-over between the three launches,
 // the first tiles and the last tile's chain.  64 sequences, 4005 tokens, 4-bit d_c = 128: 56 us.
 //
@@ -1055,8 +1057,12 @@ __global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) 
 constexpr int kMRows = 16, kMCols = 64, kMThreads = 512, kMSlots = 8;
 struct MergeArgs {
   int B, H, G, n_kv, d_c, d_h, P, workers, T_cap, cost;
+  int kind;                    // cache kind
   MlaWindow win;
+  mla_cache_t cache;
   const int32_t* seq_lens;
+  const __nv_bfloat16* qlat;   // [B][H][d_c], scaled
+  const float* qrope;          // [B][H][8], rotated, scaled
   const float* opart;
   const float* mlpart;
   const __nv_bfloat16* W_uv;   // [n_kv][d_c][d_h]
@@ -1064,8 +1070,84 @@ struct MergeArgs {
   int32_t* err;
 };
 
+// Latent columns c .. c + 7 of token t (cache row `row`) of sequence b, of length L.
+__device__ __forceinline__ void latent8(const MergeArgs& a, int b, int L, int t, size_t row, int c, float (&v)[8]) {
+  const __nv_bfloat16* kept = nullptr;
+  if (a.kind == MLA_CACHE_SAME) {
+    kept = reinterpret_cast<const __nv_bfloat16*>(a.cache.c_kv) + row * a.d_c + c;
+  } else if (a.cache.c_resid && t >= L - MLA_RESID_WINDOW) {
+    const size_t slot = (size_t)b * MLA_RESID_WINDOW + (t & (MLA_RESID_WINDOW - 1));
+    if (__ldg(a.cache.resid_pos + slot) == t) kept = reinterpret_cast<const __nv_bfloat16*>(a.cache.c_resid) + slot * a.d_c + c;
+  }
+  uint4 u;
+  if (kept) {
+    u = __ldg(reinterpret_cast<const uint4*>(kept));
+  } else {
+    const float scale = __half2float(__ldg(reinterpret_cast<const __half*>(a.cache.c_scales) + row * (a.d_c / 32) + c / 32));
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.cache.c_kv);
+    u = mla_kind_int4(a.kind) ? dequant8<4>(__ldg(reinterpret_cast<const uint32_t*>(codes + (row * a.d_c + c) / 2)), scale)
+                              : dequant8<2>(__ldg(reinterpret_cast<const unsigned short*>(codes + (row * a.d_c + c) / 4)), scale);
+  }
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(w[e] << 16);
+    v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+  }
+}
+
+// One row's merged latent once more, from the cache and its own KV head's keys only, a lane per 8
+// columns (whole warp; a token at a time, 3.5 ms for 4096: for rows that came out NaN).  Rows that
+// the definition makes NaN end at the first such score.  (The test and this code cost the
+// Llama-shaped calls 1.2 us at d_c = 256 and 0.6 with 4-bit latents, whether inlined or not; a test
+// of the scores in the attention kernel, whose softmax has no registers for it, 1.0 and 3.)
+__device__ __forceinline__ void exact_row(const MergeArgs& a, int b, int h, __nv_bfloat16* hi, __nv_bfloat16* lo) {
+  const int lane = threadIdx.x & 31, c = 8 * lane, L = __ldg(a.seq_lens + b);   // a valid length: the row has pieces
+  const bool mine = c < a.d_c;
+  const size_t qi = (size_t)b * a.H + h;
+  float q[8] = {}, o[8] = {}, m = -INFINITY, l = 0.f;
+  if (mine) {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(a.qlat + qi * a.d_c + c));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[2 * e] = __uint_as_float(w[e] << 16);
+      q[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+  }
+  const float qr = lane < 8 ? __bfloat162float(__float2bfloat16_rn(__ldcg(a.qrope + qi * 8 + lane))) : 0.f;
+  const int from = max(0, L - a.win.window), sinks = min(a.win.n_sink, from);
+#pragma unroll 1
+  for (int i = 0; i < sinks + L - from; ++i) {
+    const int t = i < sinks ? i : from + i - sinks;
+    const MlaLoc lc = mla_loc(a.cache, b, t, a.err);
+    const size_t row = (size_t)lc.pb * lc.cap + lc.pt;
+    float v[8] = {}, s = 0.f;
+    if (mine) latent8(a, b, L, t, row, c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += q[e] * v[e];
+    if (lane < 8) s += qr * __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(a.cache.k_rope) + (row * a.n_kv + h / a.G) * 8 + lane));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    const float top = fmaxf(m, s), base = top == -INFINITY ? 0.f : top, al = exp2f(m - base), p = exp2f(s - base);
+    m = top;
+    l = l * al + p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = o[e] * al + p * v[e];
+    if (l != l) break;
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float x = o[e] / l, y = o[e + 1] / l;
+    const uint32_t w = pack2(x, y);
+    *reinterpret_cast<uint32_t*>(hi + c + e) = w;
+    *reinterpret_cast<uint32_t*>(lo + c + e) = pack2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+
 template <int CP>
-__global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(MergeArgs a) {
+__global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(const __grid_constant__ MergeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   using bf16 = __nv_bfloat16;
   constexpr int WLD = kMCols + 8;
@@ -1109,6 +1191,7 @@ __global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(MergeArgs a)
   const int busy = busy_workers(total, a.workers);
   pdl_wait();   // the partials
   pdl_trigger();
+  bool sound_row = true;   // whole warp
   {   // a row per warp
     constexpr int kBatch = kMSlots * 32 / CP;         // pieces per batch
     constexpr int kAcc = CP > 32 ? 2 : 1;             // quads of columns per lane
@@ -1166,14 +1249,15 @@ __global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(MergeArgs a)
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-      const float inv = den > 0.f ? 1.f / den : 0.f;
+      sound_row = units == 0 || den > 0.f;                // a score that is no number makes the sum one as well
+      const float inv = units > 0 ? 1.f / den : 0.f;
 #pragma unroll
       for (int e = 0; e < kAcc; ++e) { acc[e].x *= inv; acc[e].y *= inv; acc[e].z *= inv; acc[e].w *= inv; }
     }
 #pragma unroll
     for (int e = 0; e < kAcc; ++e) {
       const int c = 128 * e + 4 * quad;
-      if (c >= a.d_c || sub > 0) continue;
+      if (c >= a.d_c || sub > 0 ) continue;
       const uint32_t h0 = pack2(acc[e].x, acc[e].y), h1 = pack2(acc[e].z, acc[e].w);
       const uint32_t l0 = pack2(acc[e].x - __uint_as_float(h0 << 16), acc[e].y - __uint_as_float(h0 & 0xFFFF0000u));
       const uint32_t l1 = pack2(acc[e].z - __uint_as_float(h1 << 16), acc[e].w - __uint_as_float(h1 & 0xFFFF0000u));
@@ -1182,6 +1266,10 @@ __global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(MergeArgs a)
     }
   }
   cp_async_wait_all();
+  if (!sound_row) {   // (off the way of the usual case)
+    __syncwarp();   // other lanes write over what was stored
+    exact_row(a, b, g * a.G + row % a.G, shi + r * ALD, slo + r * ALD);
+  }
   __syncthreads();
   if (warp >= kMCols / 8) return;
   const int n0 = 8 * warp;   // this warp's columns
@@ -1351,6 +1439,7 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   m.B = B; m.H = a.H; m.G = a.G; m.n_kv = cfg.n_kv_heads; m.d_c = cfg.d_c; m.d_h = cfg.head_dim; m.P = D.P;
   m.workers = D.G; m.cost = a.cost; m.T_cap = c.T_cap; m.win = win; m.seq_lens = seq_lens; m.opart = a.opart; m.mlpart = a.mlpart;
   m.W_uv = (const __nv_bfloat16*)p.W_uv; m.out = (__nv_bfloat16*)out; m.err = p.err;
+  m.kind = cfg.cache_kind; m.cache = c; m.qlat = b.qlat; m.qrope = a.qrope;
   const size_t smem = sizeof(__nv_bfloat16) * ((size_t)cfg.d_c * (kMCols + 8) + 2 * (size_t)kMRows * (cfg.d_c + 8));
   const int n_rb = (B * a.G + kMRows - 1) / kMRows, n_cc = (cfg.head_dim + kMCols - 1) / kMCols;
   const auto merge = cfg.d_c <= 64 ? window_merge_kernel<16> : cfg.d_c <= 128 ? window_merge_kernel<32> : window_merge_kernel<64>;
