@@ -83,6 +83,7 @@ struct ChunkArgs {
   uint32_t code_row;       // quantised cache: code bytes per token
   Sched sched;
   const int32_t* seq_lens;
+  const void* qlat;        // [B*Q][H][d_c] bf16, scaled
   const float* qrope;      // [B*Q][H][2r], rotated at each query's position, scaled
   float* opart;            // [P][rows][d_c]
   float* mlpart;           // [rows][P][2]
@@ -207,6 +208,13 @@ __device__ __forceinline__ MlaLoc chunk_loc(const ChunkArgs& a, int b, int t) {
 
 // Byte offset of 16-byte chunk `c` of row `r` in a 128-byte-swizzled box of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)r * 128u + (uint32_t)(((c ^ r) & 7) << 4); }
+
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
 
 // ROWS: rows per unit (see Geo); QB: code width of a quantised latent cache (4 or 2),
 // whose rows warps 2-3 dequantise into the latent ring, 0 for a bf16 latent loaded by TMA;
@@ -868,7 +876,43 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__
         for (int t = 0; t < TPL; ++t) {
           const float v = t < lim_t && (!WIN || t >= win_t || t < sink_t) ? s[t] : -INFINITY;
           s[t] = v;
-          mx = fmaxf(mx, v);
+          mx = WIN ? max_nan(mx, v) : fmaxf(mx, v);
+        }
+        if (WIN && mx != mx) {
+          // A key that is not finite: the block-diagonal rows' zeros times it are NaN for every
+          // other KV head.  The row's scores that came out NaN once more, with its own key from
+          // the cache and the latent, which stays until P is written (a latent that is not finite
+          // makes them NaN by the definition too).
+          uint64_t bad = 0;
+#pragma unroll
+          for (int t = 0; t < TPL; ++t) bad |= s[t] != s[t] ? 1ull << t : 0ull;
+          (void)mbar_wait(bars.c_full(n % a.NC), (n / a.NC) & 1, abort_flag, lim);   // (complete: S is)
+          const uint8_t* C = sbase + a.off_c + (n % a.NC) * a.c_stage;
+          const int bseq = it.v / a.nqb, i = (it.v % a.nqb) * a.qper + r / a.H;
+          const MlaLoc lc = chunk_loc<PAGED>(a, bseq, it.token());
+          const uint4* ql = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.qlat) +
+                                                           (((size_t)bseq * a.q_chunk + i) * a.H + hd) * dc);
+          const uint4* keys = reinterpret_cast<const uint4*>(a.cache.k_rope) + ((size_t)lc.pb * lc.cap + lc.pt) * n_kv + g;
+#pragma unroll 1
+          while (bad) {
+            const int t = __ffsll(bad) - 1;
+            bad &= bad - 1;
+            float v = 0.f;
+            bool finite = true;
+#pragma unroll 1
+            for (int c = 0; finite && c < dc / 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(C + (c >> 3) * kTBox + sw128(t, c)), y = __ldcg(ql + c);
+              const uint32_t none[4] = {0u, 0u, 0u, 0u}, w[4] = {y.x, y.y, y.z, y.w};
+              finite = rope_dot8_bf16(0.f, none, x) == 0.f;
+              v = rope_dot8_bf16(v, w, x);
+            }
+            v = finite ? rope_dot8_bf16(v, qb, __ldg(keys + (size_t)t * n_kv)) : __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int k = 0; k < TPL; ++k) s[k] = k == t ? v : s[k];
+          }
+          mx = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < TPL; ++t) mx = fmaxf(mx, s[t]);
         }
       } else {
         // RoPE score against the tile's keys: row tt of the swizzled stage, KV head g's chunk
@@ -1181,7 +1225,7 @@ cudaError_t mla_launch_chunk_tc(const mla_plan& p, const mla_cache_t& c, const i
   a.q_chunk = Q; a.nqb = (Q + qper - 1) / qper; a.d_c = dc; a.R = R; a.P = P; a.T_cap = c.T_cap;
   a.H = H; a.qper = qper; a.rows = qper * H; a.dcp = (dc + 63) / 64 * 64;
   a.scales = (const __half*)c.c_scales; a.code_row = code_row;
-  a.sched = sched; a.seq_lens = seq_lens; a.qrope = qrope; a.opart = opart; a.mlpart = mlpart;
+  a.sched = sched; a.seq_lens = seq_lens; a.qlat = qlat; a.qrope = qrope; a.opart = opart; a.mlpart = mlpart;
   a.cache = c; a.err = p.err;
   a.wait_ns = (uint64_t)p.opt_wait_us * 1000u;
   a.rtc = L.rtc ? 1 : 0;

@@ -45,7 +45,8 @@ def check(got, ref, dtype, what):
 
 
 CASES = [("llama_dc64", 0), ("llama_dc256", 0), ("llama_int4", 0), ("llama_int2", 0), ("llama_r128", 0), ("smollm", 0),
-         ("h24_gqa2", 0), ("h27_gqa3", 0), ("h32_gqa8_int2", 0), ("h20_dh40", 0), ("gqa64", 0), ("llama_dc64", 3), ("smollm", 3), ("gqa64", 3), ("smollm", 1), ("tiny_f32", 0), ("tiny_f32", 1),
+         ("h24_gqa2", 0), ("h27_gqa3", 0), ("h32_gqa8_int2", 0), ("h20_dh40", 0), ("gqa64", 0), ("gqa64_int4", 0),
+         ("llama_dc64", 3), ("smollm", 3), ("gqa64", 3), ("smollm", 1), ("tiny_f32", 0), ("tiny_f32", 1),
          ("gqa_f32_r3", 1)]
 
 
