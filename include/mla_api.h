@@ -333,10 +333,10 @@ MLA_API mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t
 
 /* mla_decode_chunk with a sliding window and sinks: query i of sequence b, at position
  * p = seq_lens[b] - Q + i, attends over the tokens t <= p with t < n_sink or t > p - window.
- * Per query this is mla_decode_window with length p + 1.  Cache rows of tokens that no query
- * of the sequence sees may hold anything; a row that some of its queries see must be finite
- * (queries share the tiles they read, so what a non-finite row does to the sequence's other
- * queries is unspecified).  Arguments, workspace (mla_decode_chunk_workspace_bytes) and
+ * Per query this is mla_decode_window with length p + 1, for keys that are not finite too.  Cache
+ * rows of tokens that no query of the sequence sees may hold anything; the latent of a token that
+ * some of its queries see must be finite (queries share the tiles they read, so what another
+ * one does to the sequence's other queries is unspecified).  Arguments, workspace (mla_decode_chunk_workspace_bytes) and
  * supported shapes as for mla_decode_chunk; n_sink >= 0, window >= 1; Q == 1 is
  * mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED.  Head dims that are
  * multiples of 16 up to 128 run in one launch, the others (and option 3) as the head-row units

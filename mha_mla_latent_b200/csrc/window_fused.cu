@@ -29,7 +29,7 @@
 // Bound by the tensor cores once the tiles flow (10 tiles of 128 tokens at d_c = 256 take 1.4 to
 // 1.8 us each, some 85% of the measured dense rate) and by the latency of its ends: about 6 us
 // from the launch to the first scores and 5 us from the last tile to the stored rows.  B200, 8
-// sequences x 64 queries, 32 KV heads, window 1024, d_c = 256: 33.7 us; 4-bit latent 51 us, where
+// sequences x 64 queries, 32 KV heads, window 1024, d_c = 256: 34.4 us; 4-bit latent 51 us, where
 // a tile's conversion (a thread per row, about 3 us) bounds it, and 33 us at d_c = 128.  The
 // head-row units with their absorption and merge launches take 179, 202 and 157 us there.
 #include <cuda.h>
@@ -89,6 +89,21 @@ __device__ __forceinline__ void mma_a_tmem(uint32_t d, uint32_t a, uint64_t b_de
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc),
       "r"(accumulate)
       : "memory");
+}
+
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+
+// sum + the dot product of eight bf16 pairs.
+__device__ __forceinline__ float dot8(uint4 u, uint4 v, float sum) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum = fmaf(hi_f(x[e]), hi_f(y[e]), fmaf(lo_f(x[e]), lo_f(y[e]), sum));
+  return sum;
 }
 
 // Bits 0 .. n-1 of 64 (n outside [0, 64] cut to it).
@@ -531,11 +546,44 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int t = 0; t < 64; ++t) mx[t & 3] = fmaxf(mx[t & 3], s[t]);
+        for (int t = 0; t < 64; ++t) mx[t & 3] = max_nan(mx[t & 3], s[t]);
+        float mine = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
+        if (mine != mine && valid) {
+          // A key that is not finite: the other KV heads' zeros times it are NaN.  The scores that
+          // came out NaN once more, with the row's own key (a latent that is not finite makes them
+          // NaN by the definition too); the tile stays until P is written.  (The test costs the
+          // Llama-shaped chunk 0.6 us of 34, the narrow one 0.3 of 17.)
+          uint64_t bad = 0;
+#pragma unroll
+          for (int t = 0; t < 64; ++t) bad |= s[t] != s[t] ? 1ull << t : 0ull;
+          (void)mbar_spin(bar(kBarFull + rt.slot), rt.parity, abort_flag, lim);   // (complete: S is)
+          if (QB) (void)mbar_spin(bar(kBarC + n % NST), (n / NST) & 1, abort_flag, lim);
+          const uint8_t* C = smem + a.off_ring + (uint32_t)rt.slot * a.stage;
+          const uint8_t* K = C + n_cbox * kBox;
+          const uint4 qr = *reinterpret_cast<const uint4*>(smem + a.off_qr + r * 64 + ((gi ^ (r >> 1)) & 3) * 16);
+#pragma unroll 1
+          while (bad) {
+            const int t = __ffsll(bad) - 1, tt = 64 * hf + t;
+            bad &= bad - 1;
+            float v = 0.f, zero = 0.f;   // zero: stays 0 while the latent is finite
+#pragma unroll 1
+            for (int c = 0; zero == 0.f && c < a.d_c / 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(C + (c >> 3) * kBox + sw128(tt, c));
+              zero = dot8(x, make_uint4(0, 0, 0, 0), zero);
+              v = dot8(x, *reinterpret_cast<const uint4*>(smem + (c >> 3) * kBox + sw128(r, c)), v);
+            }
+            v = dot8(*reinterpret_cast<const uint4*>(K + tt * 64 + ((gi ^ (tt >> 1)) & 3) * 16), qr, v + zero);
+#pragma unroll
+            for (int k = 0; k < 64; ++k) s[k] = k == t ? v : s[k];
+          }
+          mine = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 64; ++t) mine = fmaxf(mine, s[t]);
+        }
         // the row's maximum over both halves; past this barrier both have read their S, so P
         // may go over it
         float* xm = xchg + (n & 1) * 2 * kRows;
-        xm[hf * kRows + r] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        xm[hf * kRows + r] = mine;
         ok = pair_sync();
         if (!ok) break;
         const float top = fmaxf(xm[r], xm[kRows + r]);
@@ -588,7 +636,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         xl[hf * kRows + r] = l;
         ok = pair_sync();
         const float den = xl[r] + xl[kRows + r];
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = 1.f / den;   // (every score -inf: 0 / 0, as the definition has it)
         const int half = a.d_c / 2, c_at = hf * half;   // a multiple of 16 up to 128
         uint32_t lo2[8][8];
 #pragma unroll

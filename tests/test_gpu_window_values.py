@@ -71,3 +71,38 @@ def test_decode_window_keys(name, kernel, what):
             ref = layer.reference(q[b], bad[b], L - 1, n_sink, window)
             check(got[b], ref, layer.dtype, f"{name} {kernel} {what} sinks {n_sink} window {window} length {L}")
     plan.close()
+
+
+CHUNK_CASES = [("llama_dc64", 0), ("llama_dc256", 0), ("llama_int4", 0), ("llama_int2", 0), ("smollm", 0), ("h24_gqa2", 0),
+               ("h27_gqa3", 0), ("h32_gqa8_int2", 0), ("h20_dh40", 0), ("gqa64", 0), ("gqa64_int4", 0), ("llama_dc64", 3),
+               ("smollm", 3), ("gqa64_int4", 3)]
+
+
+@pytest.mark.parametrize("what", list(POISON))
+@pytest.mark.parametrize("name,kernel", CHUNK_CASES, ids=[f"{n}-{k}" for n, k in CHUNK_CASES])
+def test_chunk_window_keys(name, kernel, what):
+    """The same for chunks, where some queries of a sequence see a key and others do not."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**LAYERS[name], seed=22)
+    lens, Q = [600, 330, 40], 37
+    B, T_cap = len(lens), 640
+    seqs = [layer.sequence(L) for L in lens]
+    bad = [poisoned(layer, s, what) for s in seqs]
+    q = layer.queries(B, Q)
+    plan = layer.plan(mla)
+    mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+    for n_sink, window in [(1, 500), (1, 20), (3, 285)]:
+        cache = make_cache(mla, layer, B, T_cap, n_sink == 3)
+        for b, s in enumerate(bad):
+            store(cache, b, s, hidden_tokens(lens[b], lens[b] - Q, n_sink, window))
+        out = torch.full_like(q, 7.0, device="cuda")
+        ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, B, Q), dtype=torch.uint8, device="cuda")
+        mla.mla_decode_chunk_window(plan, cache.struct, torch.tensor(lens, dtype=torch.int32, device="cuda"), q.cuda(),
+                                    out, ws, n_sink, window)
+        assert mla.mla_device_error(plan) == 0
+        got = out.double().cpu()
+        for b, L in enumerate(lens):
+            for i in (0, 10, Q - 2, Q - 1):
+                ref = layer.reference(q[b, i], bad[b], L - Q + i, n_sink, window)
+                check(got[b, i], ref, "bf16", f"{name} {kernel} {what} sinks {n_sink} window {window} length {L} query {i}")
+    plan.close()
