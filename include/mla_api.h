@@ -463,8 +463,10 @@ MLA_API mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, 
                                      void* stream);
 
 /* Make room for tokens [seq_lens[b], new_lens[b]) of every sequence, so that they can be
- * appended: a free block for each column they touch that has none, and a private copy of a
- * partly filled last block (seq_lens[b] % 128 > 0) that others hold too.  Of several sequences
+ * appended: a free block for each column they touch that has none, or whose block others hold too
+ * (one behind the length, where the sequence went back to a shorter one: nothing is copied, the
+ * block loses a holder), and a private copy of a partly filled last block (seq_lens[b] % 128 > 0)
+ * that others hold too.  Of several sequences
  * in the table that write into the same block, in order of b, each copies while another holder
  * is left; with no holder elsewhere the last one keeps the block.  New blocks are the free
  * blocks of lowest id, given out in the order (b, column), with one holder each; the copied

@@ -178,7 +178,7 @@ class BlockPool:
 
     def reserve(self, seq_lens, new_lens, stream=None) -> None:
         """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence; shared, partly
-        filled blocks are copied on write."""
+        filled blocks are copied on write, shared ones behind the length replaced."""
         with self._on(stream):
             _lib.mla_blocks_reserve(self.table, self.refs, self._int32(seq_lens), self._int32(new_lens), self.table,
                                     self.refs, self.copies, self.status, self.workspace)

@@ -204,6 +204,7 @@ struct ReserveWs {
   int32_t* writers; // [n_blocks] rows that write into a shared block ...
   int32_t* last;    // [n_blocks] ... and the last of them (valid at shared blocks only; more than kThreads rows)
   int32_t* free_ids;  // [n_blocks]
+  int32_t* given_up;  // [n_blocks] the block that the k-th new one replaces, -1: none
 };
 constexpr int kSharedIds = 4096;   // new ids kept in shared memory (more of them: in the workspace)
 
@@ -234,7 +235,13 @@ __device__ __forceinline__ Row row_of(const Table& t, const int32_t* refs, const
   return r;
 }
 
-// Latency bound (5 to 6 us on 16 to 160 rows, 11 us with 65536 blocks).  CTA 0 decides while the others copy the table and the counts (calls that are not in place);
+// A column that tokens start gets a new block where it has none, and where others hold its block
+// too: a sequence that went back to a shorter length still names the blocks behind it, and what
+// it writes there must not reach a fork's.
+__device__ __forceinline__ bool held_too(const int32_t* refs, int e) { return __ldcg(refs + e) > 1; }
+
+// Latency bound (5 to 6 us on 16 to 160 rows, 11 us with 65536 blocks).  CTA 0 decides while the others
+// copy the table and the counts (calls that are not in place);
 // after the cluster's barrier CTA 0 writes what changes.  Decisions read the input only.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_lens,
@@ -291,28 +298,34 @@ reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_
     return r.shared >= 0 && (refs_in[r.shared] > __ldcg(ws.writers + r.shared) || __ldcg(ws.last + r.shared) != b);
   };
   // 2. new blocks per row (long runs of columns: a warp per row), then their prefix sums
-  bool any_long = false;
+  bool any_long = false, any_back = false;   // back: some column's block is held by others
+  auto wants = [&](int b, int j) {
+    const int e = entry(t, t.in[(size_t)b * t.C + j]);
+    const bool back = e >= 0 && held_too(refs_in, e);
+    any_back |= back;
+    return e < 0 || back ? 1 : 0;
+  };
   for (int b = tid; b < t.B; b += kThreads) {
     const Row r = row(b);
     int need = copies_block(r, b) ? 1 : 0;
     ws.copy[b] = need;
     if (r.c1 - r.c0 <= kShortRow)
-      for (int j = r.c0; j < r.c1; ++j) need += entry(t, t.in[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+      for (int j = r.c0; j < r.c1; ++j) need += wants(b, j);
     else
       any_long = true;
     ws.need[b] = need;
   }
-  any_long = __syncthreads_or(any_long);
-  if (any_long) {
+  if (__syncthreads_or(any_long || any_back)) {   // (neither in a step of single tokens)
     for (int b = warp; b < t.B; b += kThreads / 32) {
       const Row r = row_of(t, refs_in, seq_lens, new_lens, b, false);
       if (r.c1 - r.c0 <= kShortRow) continue;
       int n = 0;
-      for (int j = r.c0 + lane; j < r.c1; j += 32) n += entry(t, t.in[(size_t)b * t.C + j]) < 0 ? 1 : 0;
+      for (int j = r.c0 + lane; j < r.c1; j += 32) n += wants(b, j);
       n = __reduce_add_sync(0xffffffffu, n);
       if (lane == 0) ws.need[b] += n;
     }
-    __syncthreads();
+    any_long = __syncthreads_or(any_long);
+    any_back = __syncthreads_or(any_back);
   }
   int total = 0, n_copies = 0;
   for (int base = 0; base < t.B; base += kThreads) {
@@ -347,33 +360,38 @@ reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_
   }
   cluster_sync();   // the output holds the input's values, and the ids are listed
   if (!ok) return;
-  // 4. counts, table and copy list.  Rows are independent: row b's new ids are ids[need[b] ...].
+  // 4. table and copy list, and the new blocks' counts.  Rows are independent: row b's new ids are
+  // ids[need[b] ...].  Where counts decide (any_back) none changes yet (but a new block's, which was
+  // 0 at most): what is given up is noted and loses its holders after the last row.
   for (int b = tid; b < t.B; b += kThreads) {
-    // (not row_of: in place the counts change in this loop; copy[] and need[] carry what was decided)
+    // (not row_of: copy[] and need[] carry what was decided)
     int at = ws.need[b];
     const int L = seq_lens[b], N = new_lens[b];
+    auto take = [&](int32_t* e) {
+      const int old = *e, id = ids[at];
+      if (any_back) ws.given_up[at] = old >= 0 && old < t.n_blocks ? old : -1;
+      ++at;
+      *e = id;
+      t.refs[id] = 1;
+      return id;
+    };
     if (ws.copy[b] >= 0) {
       int32_t* e = t.out + (size_t)b * t.C + L / kBT;
       int32_t* c = copies + 3 * (size_t)ws.copy[b];
-      const int old = *e, id = ids[at++];
-      c[0] = old; c[1] = id; c[2] = L % kBT;
-      atomicSub(t.refs + old, 1);
-      t.refs[id] = 1;
-      *e = id;
+      c[0] = *e;
+      if (!any_back) atomicSub(t.refs + *e, 1);
+      c[1] = take(e);
+      c[2] = L % kBT;
     }
     if (!length_ok(t, L) || !length_ok(t, N) || N < L) continue;
     const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
     if (c1 - c0 > kShortRow) continue;
     for (int j = c0; j < c1; ++j) {
       int32_t* e = t.out + (size_t)b * t.C + j;
-      if (*e >= 0 && *e < t.n_blocks) continue;
-      const int id = ids[at++];
-      *e = id;
-      t.refs[id] = 1;
+      if (*e < 0 || *e >= t.n_blocks || (any_back && held_too(t.refs, *e))) take(e);
     }
   }
-  if (!any_long) return;
-  for (int b = warp; b < t.B; b += kThreads / 32) {
+  for (int b = warp; any_long && b < t.B; b += kThreads / 32) {
     const int L = seq_lens[b], N = new_lens[b];
     const int c0 = (int)(((long long)L + kBT - 1) / kBT), c1 = (int)(((long long)N + kBT - 1) / kBT);
     if (c1 - c0 <= kShortRow || !length_ok(t, L) || !length_ok(t, N)) continue;
@@ -381,15 +399,24 @@ reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_
     for (int j0 = c0; j0 < c1; j0 += 32) {
       const int j = j0 + lane;
       int32_t* e = t.out + (size_t)b * t.C + min(j, c1 - 1);
-      const bool none = j < c1 && (*e < 0 || *e >= t.n_blocks);
-      const uint32_t m = __ballot_sync(0xffffffffu, none);
-      if (none) {
-        const int id = ids[at + __popc(m & ((1u << lane) - 1))];
+      const int old = *e;
+      const bool none = old < 0 || old >= t.n_blocks, want = j < c1 && (none || (any_back && held_too(t.refs, old)));
+      const uint32_t m = __ballot_sync(0xffffffffu, want);
+      if (want) {
+        const int k = at + __popc(m & ((1u << lane) - 1)), id = ids[k];
+        if (any_back) ws.given_up[k] = none ? -1 : old;
         *e = id;
         t.refs[id] = 1;
       }
       at += __popc(m);
     }
+  }
+  // 5. what was given up loses a holder (and is free where every holder went back)
+  if (!any_back) return;
+  __syncthreads();
+  for (int k = tid; k < total; k += kThreads) {
+    const int old = ws.given_up[k];
+    if (old >= 0 && atomicSub(t.refs + old, 1) == 1) atomicSub(t.status + 2, 1);
   }
 }
 
@@ -576,8 +603,8 @@ mla_status_t check_table(const int32_t* table, const int32_t* refs, int32_t B, i
 
 mla_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
 
-// Workspace: two ints per row and three per block (reserve), two per block (compact).
-size_t workspace_ints(int32_t B, int32_t n_blocks) { return 2 * (size_t)B + 3 * (size_t)n_blocks; }
+// Workspace: two ints per row and four per block (reserve), two per block (compact).
+size_t workspace_ints(int32_t B, int32_t n_blocks) { return 2 * (size_t)B + 4 * (size_t)n_blocks; }
 
 }  // namespace blocks
 }  // namespace mla
@@ -616,6 +643,7 @@ mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* refs, int32
   ReserveWs ws;
   ws.need = w; ws.copy = w + B;
   ws.writers = w + 2 * (size_t)B; ws.last = ws.writers + n_blocks; ws.free_ids = ws.last + n_blocks;
+  ws.given_up = ws.free_ids + n_blocks;
   const Table t{table, table_out, refs_out, B, n_cols, n_blocks, status};
   return cuda_status(mla_launch_kernel(reserve_kernel, dim3(kCluster), dim3(kThreads), 0, s, true, t, refs, seq_lens,
                                        new_lens, ws, copies));

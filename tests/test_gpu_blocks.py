@@ -506,3 +506,83 @@ def test_ring_of_a_cut_fork(n):
         assert torch.equal(cache.c_resid[b, t % 128], cache.c_resid[2, t % 128])
     assert pool.errors() == 0 and mla.mla_device_error(plan) == 0
     plan.close()
+
+
+def m_reserve_shared(table, refs, lens, new):
+    """m_reserve where columns behind the length may hold blocks: those that others hold too are
+    given up for new ones."""
+    B, C = table.shape
+    out, cnt, copies, err = table.copy(), refs.copy(), [], 0
+    free = [i for i in range(len(refs)) if refs[i] <= 0]
+    writers = {}
+    for b in range(B):
+        L, N = int(lens[b]), int(new[b])
+        if L % BLOCK and N > L and table[b][L // BLOCK] >= 0:
+            writers.setdefault(int(table[b][L // BLOCK]), []).append(b)
+    n0 = len(free)
+    for b in range(B):
+        L, N = int(lens[b]), int(new[b])
+        if L % BLOCK and N > L:
+            e = int(table[b][L // BLOCK])
+            if refs[e] > 1 and (refs[e] > len(writers[e]) or writers[e][-1] != b):
+                cnt[e] -= 1
+                out[b][L // BLOCK] = free.pop(0)
+                copies.append((e, int(out[b][L // BLOCK]), L % BLOCK))
+                cnt[out[b][L // BLOCK]] += 1
+        for j in range(blocks_of(L), blocks_of(N)):
+            e = int(table[b][j])
+            if e >= 0 and refs[e] <= 1:
+                continue
+            if e >= 0:
+                cnt[e] -= 1
+            out[b][j] = free.pop(0)
+            cnt[out[b][j]] += 1
+    return out, cnt, copies, err, n0 - len(free)
+
+
+@pytest.mark.parametrize("inplace", [False, True], ids=["apart", "in_place"])
+@pytest.mark.parametrize("size", [(2, 6, 40), (5, 12, 200), (40, 60, 6000), (1200, 5, 20000)], ids=str)
+def test_reserve_behind_a_rolled_back_length(size, inplace):
+    """Sequences that went back to a shorter length (drafted tokens that were not taken) still name
+    the blocks behind it, which forks may share: a reserve gives them blocks of their own there."""
+    B, C, n_blocks = size
+    rng = np.random.default_rng(B)
+    for trial in range(3):
+        table, refs, lens = random_state(rng, B, C, n_blocks, share=0.8, holes=0.1 * (trial == 1))
+        back = np.where(rng.random(B) < 0.8, (lens * rng.random(B)).astype(np.int64), lens)
+        back = np.where(rng.random(B) < 0.2, back // BLOCK * BLOCK, back)
+        for b in range(B):   # a partly filled last block has to be there
+            if back[b] % BLOCK and table[b][back[b] // BLOCK] < 0:
+                back[b] = back[b] // BLOCK * BLOCK
+        new = np.minimum(back + rng.choice([0, 1, 129, 700, 9000], size=B), C * BLOCK)
+        d = Dev(table, refs)
+        want = m_reserve_shared(table, refs, back, new)
+        got = d.call("reserve", d.up(back), d.up(new), inplace=inplace)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+        assert got[2].tolist() == [len(want[2]), 0, int((want[1] > 0).sum()), want[4]]
+        assert d.listed(len(want[2])) == want[2]
+        # what a sequence may write into is its own
+        held = np.bincount(got[0][got[0] >= 0], minlength=n_blocks)
+        assert (got[1] == held).all()
+        for b in np.nonzero(new > back)[0]:
+            assert (held[got[0][b, int(back[b]) // BLOCK:blocks_of(int(new[b]))]] == 1).all()
+
+
+def test_a_rolled_back_sample_leaves_the_others_alone():
+    """Two samples share everything, one goes back and writes other tokens: the other's rows stay."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(d_c=64, seed=6)
+    pool = BlockPool(2, 1024, 20)
+    cache = pool.layer(layer.config(mla))
+    seq, other = layer.sequence(600), layer.sequence(600)
+    pool.reserve([0, 0], [600, 0])
+    cache.set_latent_rows(0, 0, seq["c_kv"])
+    pool.fork([0], [1], [600, 0])
+    for at in (300, 256):
+        pool.reserve([at, 600], [580, 600])
+        cache.set_latent_rows(0, at, other["c_kv"][at:580])
+        assert torch.equal(cache.latent_rows(1, 0, 600).cpu(), seq["c_kv"])
+        assert torch.equal(cache.latent_rows(0, 0, 580).cpu(), torch.cat([seq["c_kv"][:at], other["c_kv"][at:580]]))
+        pool.fork([1], [0], [0, 600])
+    assert pool.errors() == 0
