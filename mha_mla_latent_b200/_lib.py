@@ -193,12 +193,17 @@ def mla_select_pairs(cfg: MlaConfig, q_cal, k_cal, pair_idx, contrib=None, strea
     return st
 
 
+_I32 = torch.int32
+_TORCH_DTYPES = {MLA_F32: torch.float32, MLA_BF16: torch.bfloat16}
+
+
 class Plan:
     """Owner of an mla_plan_t* (mla_plan_create / mla_plan_destroy)."""
 
     def __init__(self, handle, cfg):
         self.handle = handle
         self.cfg = cfg
+        self.n_heads, self.head_dim, self.dtype = cfg.n_heads, cfg.head_dim, _TORCH_DTYPES[cfg.dtype]
 
     def __del__(self):
         self.close()
@@ -230,8 +235,13 @@ def mla_plan_set_option(plan: Plan, option: int, value: int):
 
 def cache_struct(c_kv, c_scales, k_rope, B, T_cap, c_resid=None, resid_pos=None, block_table=None,
                  n_blocks=0) -> MlaCache:
-    return MlaCache(_ptr(c_kv), _ptr(c_scales), _ptr(k_rope), int(B), int(T_cap), _ptr(c_resid),
-                    _ptr(resid_pos), _ptr(block_table), int(n_blocks))
+    c = MlaCache(_ptr(c_kv), _ptr(c_scales), _ptr(k_rope), int(B), int(T_cap), _ptr(c_resid),
+                 _ptr(resid_pos), _ptr(block_table), int(n_blocks))
+    # the device of its arrays, which hold no more than addresses (-1: the host, -2: several)
+    at = {t.get_device() for t in (c_kv, c_scales, k_rope, c_resid, resid_pos, block_table)
+          if isinstance(t, torch.Tensor)}
+    c.device = at.pop() if len(at) == 1 else -2 if at else None
+    return c
 
 
 def mla_append(plan: Plan, x, seq_idx, pos, cache: MlaCache, stream=None, check=True):
@@ -276,70 +286,104 @@ def mla_decode_chunk(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, s
     return st
 
 
+def _device(t, name):
+    """Index of the current device, which `t` must be on."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    dev = _current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device")
+    return dev
+
+
+def _workspace(t, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the current device")
+    return t.data_ptr(), t.nbytes
+
+
+def _cache_on(cache, dev):
+    """The cache view; refused where its arrays are known to be elsewhere (see cache_struct)."""
+    where = getattr(cache, "device", None)
+    if where is not None and where != dev:
+        raise ValueError("the cache must be on the current device")
+    return ctypes.byref(cache)
+
+
+def _window_call(fn, where, plan, cache, seq_lens, q, out, workspace, n_sink, window, stream, check, chunk):
+    """A windowed call on checked tensors (one expression: the checks cost 0.6 us of a call's host time)."""
+    shape = q.shape
+    if len(shape) != 3 + chunk or shape[-2] != plan.n_heads or shape[-1] != plan.head_dim:
+        raise ValueError(f"q must be {'[B][Q]' if chunk else '[B]'}[{plan.n_heads}][{plan.head_dim}]")
+    dev, dt, n = _device(q, "q"), plan.dtype, q.numel()
+    if not (q.dtype is dt and out.dtype is dt and seq_lens.dtype is _I32 and out.numel() >= n
+            and seq_lens.numel() >= shape[0] and out.get_device() == dev and seq_lens.get_device() == dev
+            and workspace.get_device() == dev and q.is_contiguous() and out.is_contiguous()
+            and seq_lens.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError(f"q and out must be {dt}, seq_lens int32 with an entry per sequence, out as large as q, "
+                         "and all of them and the workspace contiguous on the current device")
+    mid = (shape[0], shape[1]) if chunk else (shape[0],)
+    st = fn(plan.handle, _cache_on(cache, dev), seq_lens.data_ptr(), q.data_ptr(), *mid, n_sink, window, out.data_ptr(),
+            workspace.data_ptr(), workspace.nbytes, _raw_stream(dev) if stream is None else _stream(stream))
+    if check:
+        _check(st, where)
+    return st
+
+
 def mla_decode_window(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, n_sink, window, stream=None,
                       check=True):
-    """mla_decode over the first n_sink tokens and the newest `window` tokens of each sequence."""
-    st = _lib.mla_decode_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), q.shape[0], n_sink, window,
-                                _ptr(out), _ptr(workspace), workspace.nbytes, _stream(stream))
-    if check:
-        _check(st, "mla_decode_window")
-    return st
+    """mla_decode over the first n_sink tokens and the newest `window` tokens of each sequence.
+    ValueError for tensors of another shape, dtype or device than the call needs."""
+    return _window_call(_lib.mla_decode_window, "mla_decode_window", plan, cache, seq_lens, q, out, workspace, n_sink,
+                        window, stream, check, False)
 
 
 def mla_decode_chunk_window(plan: Plan, cache: MlaCache, seq_lens, q, out, workspace, n_sink, window, stream=None,
                             check=True):
     """mla_decode_chunk with each query seeing the first n_sink tokens and the `window` tokens
-    up to its own: q and out are [B][Q][H][d_h]."""
-    st = _lib.mla_decode_chunk_window(plan.handle, ctypes.byref(cache), _ptr(seq_lens), _ptr(q), q.shape[0], q.shape[1],
-                                      n_sink, window, _ptr(out), _ptr(workspace), workspace.nbytes, _stream(stream))
-    if check:
-        _check(st, "mla_decode_chunk_window")
-    return st
+    up to its own: q and out are [B][Q][H][d_h].  ValueError as for mla_decode_window."""
+    return _window_call(_lib.mla_decode_chunk_window, "mla_decode_chunk_window", plan, cache, seq_lens, q, out,
+                        workspace, n_sink, window, stream, check, True)
 
 
 def mla_blocks_workspace_bytes(B: int, n_cols: int, n_blocks: int) -> int:
     return int(_lib.mla_blocks_workspace_bytes(int(B), int(n_cols), int(n_blocks)))
 
 
-_I32 = torch.int32
-
-
-def _i32(t, name, n):
-    """Device pointer of a contiguous int32 device tensor of n elements."""
-    if t.dtype is not _I32 or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 device tensor of {n} elements")
+def _i32(t, name, n, dev):
+    """Pointer of a contiguous int32 tensor of n elements on device `dev`."""
+    if t.dtype is not _I32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on the current device")
     return t.data_ptr()
 
 
 def _table(table, refs):
-    """Sizes of a block table [B][n_cols] and its holder counts [n_blocks]."""
+    """Sizes of a block table [B][n_cols] and its holder counts [n_blocks], and the current device."""
     B, C = table.shape
-    if table.is_cuda and table.get_device() != _current_device():
-        raise ValueError("the block table must be on the current device")
-    return B, C, refs.numel()
+    return B, C, refs.numel(), _device(table, "the block table")
 
 
-def _block_status(status):
+def _block_status(status, dev):
     if status.numel() < MLA_BLOCKS_STATUS_INTS:
         raise ValueError(f"status holds {MLA_BLOCKS_STATUS_INTS} int32")
-    return _i32(status, "status", status.numel())
+    return _i32(status, "status", status.numel(), dev)
 
 
-def _block_copies(copies):
+def _block_copies(copies, dev):
     n, three = copies.shape
     if three != 3:
         raise ValueError("copies is [max_copies][3]")
-    return _i32(copies, "copies", 3 * n), n
+    return _i32(copies, "copies", 3 * n, dev), n
 
 
 def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status, stream=None, check=True):
     """Row dst[i] of the table shares the blocks of row src[i] (its first seq_lens[src[i]] tokens)."""
-    B, C, n = _table(table, refs)
+    B, C, n, dev = _table(table, refs)
     k = src.numel()
-    st = _lib.mla_blocks_fork(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n, _i32(src, "src", k),
-                              _i32(dst, "dst", k), k, _i32(seq_lens, "seq_lens", B),
-                              _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n),
-                              _block_status(status), _stream(stream))
+    st = _lib.mla_blocks_fork(_i32(table, "table", B * C, dev), _i32(refs, "refs", n, dev), B, C, n,
+                              _i32(src, "src", k, dev), _i32(dst, "dst", k, dev), k, _i32(seq_lens, "seq_lens", B, dev),
+                              _i32(table_out, "table_out", B * C, dev), _i32(refs_out, "refs_out", n, dev),
+                              _block_status(status, dev), _stream(stream))
     if check:
         _check(st, "mla_blocks_fork")
     return st
@@ -348,12 +392,12 @@ def mla_blocks_fork(table, refs, src, dst, seq_lens, table_out, refs_out, status
 def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, copies, status, workspace, stream=None,
                        check=True):
     """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence, shared partial blocks copied on write."""
-    B, C, n = _table(table, refs)
-    cp, n_cp = _block_copies(copies)
-    st = _lib.mla_blocks_reserve(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
-                                 _i32(seq_lens, "seq_lens", B), _i32(new_lens, "new_lens", B),
-                                 _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n), cp, n_cp,
-                                 _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
+    B, C, n, dev = _table(table, refs)
+    cp, n_cp = _block_copies(copies, dev)
+    st = _lib.mla_blocks_reserve(_i32(table, "table", B * C, dev), _i32(refs, "refs", n, dev), B, C, n,
+                                 _i32(seq_lens, "seq_lens", B, dev), _i32(new_lens, "new_lens", B, dev),
+                                 _i32(table_out, "table_out", B * C, dev), _i32(refs_out, "refs_out", n, dev), cp, n_cp,
+                                 _block_status(status, dev), *_workspace(workspace, dev), _stream(stream))
     if check:
         _check(st, "mla_blocks_reserve")
     return st
@@ -361,10 +405,11 @@ def mla_blocks_reserve(table, refs, seq_lens, new_lens, table_out, refs_out, cop
 
 def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, status, stream=None, check=True):
     """Releases the blocks without a token among the first n_sink or the newest `window` ones."""
-    B, C, n = _table(table, refs)
-    st = _lib.mla_blocks_trim(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
-                              _i32(seq_lens, "seq_lens", B), n_sink, window, _i32(table_out, "table_out", B * C),
-                              _i32(refs_out, "refs_out", n), _block_status(status), _stream(stream))
+    B, C, n, dev = _table(table, refs)
+    st = _lib.mla_blocks_trim(_i32(table, "table", B * C, dev), _i32(refs, "refs", n, dev), B, C, n,
+                              _i32(seq_lens, "seq_lens", B, dev), n_sink, window,
+                              _i32(table_out, "table_out", B * C, dev), _i32(refs_out, "refs_out", n, dev),
+                              _block_status(status, dev), _stream(stream))
     if check:
         _check(st, "mla_blocks_trim")
     return st
@@ -372,11 +417,11 @@ def mla_blocks_trim(table, refs, seq_lens, n_sink, window, table_out, refs_out, 
 
 def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspace, stream=None, check=True):
     """Moves the blocks in use to the lowest ids; `copies` lists the moves."""
-    B, C, n = _table(table, refs)
-    cp, n_cp = _block_copies(copies)
-    st = _lib.mla_blocks_compact(_i32(table, "table", B * C), _i32(refs, "refs", n), B, C, n,
-                                 _i32(table_out, "table_out", B * C), _i32(refs_out, "refs_out", n), cp, n_cp,
-                                 _block_status(status), _ptr(workspace), workspace.nbytes, _stream(stream))
+    B, C, n, dev = _table(table, refs)
+    cp, n_cp = _block_copies(copies, dev)
+    st = _lib.mla_blocks_compact(_i32(table, "table", B * C, dev), _i32(refs, "refs", n, dev), B, C, n,
+                                 _i32(table_out, "table_out", B * C, dev), _i32(refs_out, "refs_out", n, dev), cp, n_cp,
+                                 _block_status(status, dev), *_workspace(workspace, dev), _stream(stream))
     if check:
         _check(st, "mla_blocks_compact")
     return st
@@ -384,8 +429,10 @@ def mla_blocks_compact(table, refs, table_out, refs_out, copies, status, workspa
 
 def mla_blocks_copy(cfg: MlaConfig, cache: MlaCache, copies, status, stream=None, check=True):
     """Moves the listed rows in one layer's cache (run it once per layer)."""
-    cp, n_cp = _block_copies(copies)
-    st = _lib.mla_blocks_copy(ctypes.byref(cfg), ctypes.byref(cache), cp, n_cp, _block_status(status), _stream(stream))
+    dev = _device(copies, "copies")
+    cp, n_cp = _block_copies(copies, dev)
+    st = _lib.mla_blocks_copy(ctypes.byref(cfg), _cache_on(cache, dev), cp, n_cp, _block_status(status, dev),
+                              _stream(stream))
     if check:
         _check(st, "mla_blocks_copy")
     return st
@@ -395,10 +442,11 @@ def mla_ring_copy(cfg: MlaConfig, cache: MlaCache, src, dst, status, stream=None
     """Copies the residual windows of sequences src to sequences dst in one layer's cache; with
     the seq_lens of the fork, pairs that it skips for their length are skipped here too and
     tokens behind the length are left out."""
+    dev = _device(src, "src")
     n = src.numel()
-    lens = None if seq_lens is None else _i32(seq_lens, "seq_lens", cache.B)
-    st = _lib.mla_ring_copy(ctypes.byref(cfg), ctypes.byref(cache), _i32(src, "src", n), _i32(dst, "dst", n), n,
-                            lens, _block_status(status), _stream(stream))
+    lens = None if seq_lens is None else _i32(seq_lens, "seq_lens", cache.B, dev)
+    st = _lib.mla_ring_copy(ctypes.byref(cfg), _cache_on(cache, dev), _i32(src, "src", n, dev),
+                            _i32(dst, "dst", n, dev), n, lens, _block_status(status, dev), _stream(stream))
     if check:
         _check(st, "mla_ring_copy")
     return st

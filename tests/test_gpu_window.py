@@ -628,3 +628,29 @@ def test_refusals():
         rp = ring.plan(mla)
         rc = make_cache(mla, ring, 2, 256, False)
         mla.mla_decode_chunk_window(rp, rc.struct, lens, qc[:, :8].contiguous(), oc, ws, 0, 4)
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """Shapes, types and places that the kernels could not read safely: refused on the host."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(d_c=64, seed=23)
+    plan = layer.plan(mla)
+    cache = make_cache(mla, layer, 2, 256, False)
+    lens = torch.full((2,), 100, dtype=torch.int32, device="cuda")
+    q = layer.queries(2).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(mla.mla_decode_chunk_workspace_bytes(plan, 2, 3), dtype=torch.uint8, device="cuda")
+    assert mla.mla_decode_window(plan, cache.struct, lens, q, out, ws, 0, 4) == mla.MLA_OK
+    args = dict(p=plan, c=cache.struct, l=lens, q=q, o=out, w=ws, s=0, n=4)
+    run = lambda f, **kw: f(*[{**args, **kw}[k] for k in "pclqowsn"])  # noqa: E731
+    host = mla.cache_struct(torch.zeros(2, 256, 64, dtype=torch.bfloat16), None, cache.k_rope, 2, 256)
+    for kw in (dict(l=lens[:1]), dict(l=lens.long()), dict(l=lens.cpu()), dict(q=q.cpu()), dict(q=q.float()), dict(o=out[:1]),
+               dict(o=out.cpu()), dict(o=out.float()), dict(w=ws.cpu()), dict(c=host), dict(q=q[:, :16]), dict(q=q[None]),
+               dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), dict(w=ws[::2])):
+        with pytest.raises(ValueError):
+            run(mla.mla_decode_window, **kw)
+    with pytest.raises(ValueError):
+        run(mla.mla_decode_chunk_window)          # [B][H][d_h] where the chunk's [B][Q][H][d_h] belongs
+    torch.cuda.synchronize()
+    assert mla.mla_device_error(plan) == 0
+    plan.close()

@@ -103,3 +103,33 @@ def test_pool_refuses_bad_sizes(mla):
     for B, T, n in [(0, 128, 4), (1, 100, 4), (1, 128, 0)]:
         with pytest.raises(ValueError):
             BlockPool(B, T, n, device="cpu")
+
+
+def test_host_tensors_are_refused(mla):
+    """A pointer of a host tensor never reaches the device: every tensor of the window and block
+    calls has to be on the current one, the cache's arrays included."""
+    cfg = mla.make_config(64, 8, 4, 64, 4, 64)
+    plan = mla.Plan(None, cfg)   # refused before the plan is looked at
+    cache = mla.cache_struct(torch.zeros(2, 128, 64, dtype=torch.bfloat16), None,
+                             torch.zeros(2, 128, 4, 8, dtype=torch.bfloat16), 2, 128)
+    lens, ws = torch.ones(2, dtype=torch.int32), torch.zeros(1 << 16, dtype=torch.uint8)
+    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mla.mla_decode_window(plan, cache, lens, q, q, ws, 0, 4)
+    q4 = q.unsqueeze(1).expand(2, 3, 8, 64).contiguous()
+    with pytest.raises(ValueError):
+        mla.mla_decode_chunk_window(plan, cache, lens, q4, q4, ws, 0, 4)
+    for wrong in (q4, q[:, :7], q[..., :32]):   # not [B][H][d_h]: a chunk's queries, fewer heads or dims
+        with pytest.raises(ValueError, match="q must be"):
+            mla.mla_decode_window(plan, cache, lens, wrong, wrong, ws, 0, 4)
+    with pytest.raises(ValueError, match="q must be"):
+        mla.mla_decode_chunk_window(plan, cache, lens, q, q, ws, 0, 4)
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    table, refs, st, cp = i(2, 3), i(5), i(4), i(4, 3)
+    for call in (lambda: mla.mla_blocks_copy(cfg, cache, cp, st), lambda: mla.mla_ring_copy(cfg, cache, i(1), i(1), st),
+                 lambda: mla.mla_blocks_fork(table, refs, i(1), i(1), i(2), table, refs, st),
+                 lambda: mla.mla_blocks_reserve(table, refs, i(2), i(2), table, refs, cp, st, ws),
+                 lambda: mla.mla_blocks_compact(table, refs, table, refs, cp, st, ws)):
+        with pytest.raises(ValueError):
+            call()
+    assert cache.device == -1
