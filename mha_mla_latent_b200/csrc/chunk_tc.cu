@@ -1236,7 +1236,7 @@ cudaError_t mla_launch_chunk_tc(const mla_plan& p, const mla_cache_t& c, const i
   a.win = win;
   const bool paged = c.block_table != nullptr, resid = qbits == 4 && c.c_resid != nullptr;
   const AttnKernel kern = win.window > 0 ? attn_kernel<true>(rows, qbits, resid, paged) : attn_kernel<false>(rows, qbits, resid, paged);
-  cudaError_t e = mla_smem_limit((const void*)kern, L.total);
+  cudaError_t e = mla_smem_limit(p, (const void*)kern, L.total);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
   const int threads = rows == 32 && qbits ? Crew<32, 4>::WARPS * 32 : 256;

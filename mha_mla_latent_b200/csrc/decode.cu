@@ -638,7 +638,7 @@ cudaError_t launch_combine(const mla_plan& p, int units, int H, int n_kv, int q_
   const size_t smem_c = (size_t)cfg.d_c * (ca.ncols + RB) * sizeof(float) +
                         (size_t)RBP * (cfg.d_c + 8) * sizeof(__nv_bfloat16);   // + the MMA form's A tiles
   const int n_rbc = (units * G + RB - 1) / RB, n_dc = (cfg.head_dim + ca.ncols - 1) / ca.ncols;
-  cudaError_t e = mla_smem_limit((const void*)combine_kernel<T>, smem_c);
+  cudaError_t e = mla_smem_limit(p, (const void*)combine_kernel<T>, smem_c);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfCombine, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(combine_kernel<T>, dim3(n_kv * n_rbc * n_dc), dim3(256), smem_c, s, p.opt_pdl, ca);
@@ -665,7 +665,7 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
     size_t smem = sizeof(float) * ((size_t)H * cfg.d_c + H * 2 * cfg.r_pairs +
                                    kSimtTile * (cfg.d_c + 1) + kSimtTile * (p.R + 1) +
                                    kSimtTile * H + 3 * H);
-    e = mla_smem_limit((const void*)decode_simt_kernel<T, INT4>, smem);
+    e = mla_smem_limit(p, (const void*)decode_simt_kernel<T, INT4>, smem);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
     e = mla_launch_kernel(decode_simt_kernel<T, INT4>, dim3(L.G), dim3(256), smem, s, p.opt_pdl, da);
@@ -692,7 +692,7 @@ cudaError_t launch_decode_t(const mla_plan& p, const mla_cache_t& c, const int32
   size_t smem_abs;
   int nblk;
   absorb_setup<T>(p, c, seq_lens, q, B, ws, L, win, &aa, &smem_abs, &nblk);
-  cudaError_t e = mla_smem_limit((const void*)absorb_kernel<T>, smem_abs);
+  cudaError_t e = mla_smem_limit(p, (const void*)absorb_kernel<T>, smem_abs);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(absorb_kernel<T>, dim3(nblk), dim3(256), smem_abs, s, p.opt_pdl, aa);
@@ -747,7 +747,7 @@ cudaError_t launch_step_t(const mla_plan& p, const mla_cache_t& c, const int32_t
   sp.app_gy = (int)agrid.y;
   const int nblk = nabs + (int)(agrid.x * agrid.y * agrid.z);
   const size_t smem = std::max(smem_app, smem_abs);
-  cudaError_t e = mla_smem_limit((const void*)step_pre_kernel<INT4>, smem);
+  cudaError_t e = mla_smem_limit(p, (const void*)step_pre_kernel<INT4>, smem);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(step_pre_kernel<INT4>, dim3(nblk), dim3(256), smem, s, p.opt_pdl, sp);
@@ -770,7 +770,7 @@ cudaError_t launch_chunk(const mla_plan& p, const mla_cache_t& c, const int32_t*
   absorb_setup<bf16>(p, c, seq_lens, q, B * Q, ws, L, win, &aa, &smem_abs, &nblk);
   aa.q_chunk = Q;
   aa.q_block = kQB;
-  cudaError_t e = mla_smem_limit((const void*)absorb_kernel<bf16>, smem_abs);
+  cudaError_t e = mla_smem_limit(p, (const void*)absorb_kernel<bf16>, smem_abs);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAbsorb, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(absorb_kernel<bf16>, dim3(nblk), dim3(256), smem_abs, s, p.opt_pdl, aa);

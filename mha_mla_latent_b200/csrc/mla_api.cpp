@@ -5,7 +5,6 @@
 #include <string.h>
 
 #include <algorithm>
-#include <mutex>
 #include <new>
 #include <vector>
 
@@ -37,27 +36,27 @@ mla_status_t validate_config(const mla_config_t* c) {
 
 }  // namespace
 
-cudaError_t mla_smem_limit(const void* kern, size_t bytes) {
-  struct Entry {
-    const void* kern;
-    int device;
-    size_t bytes;
-  };
-  static std::mutex mutex;
-  static Entry known[256];
-  static int n = 0;
+// What was set is remembered in the plan, whose life lies within that of its device's context (a
+// reset takes the attribute and the plan's memory with it).  The limit set is the largest that the
+// kernel can have, so that no other plan's smaller one replaces it.
+cudaError_t mla_smem_limit(const mla_plan& p, const void* kern, size_t bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mutex);
   int i = 0;
-  while (i < n && !(known[i].kern == kern && known[i].device == dev)) ++i;
-  if (i < n && known[i].bytes >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
-  if (i == n && n < 256) known[n++] = Entry{kern, dev, 0};
-  if (i < n) known[i].bytes = bytes;
-  return cudaSuccess;
+  while (i < p.n_smem_set && !(p.smem_set[i].kern == kern && p.smem_set[i].device == dev)) ++i;
+  if (i == p.n_smem_set) {
+    cudaFuncAttributes fa;
+    int most = 0;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+    most -= (int)fa.sharedSizeBytes;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+    if (i == mla_plan::kSmemSets) i = p.n_smem_set = 0;   // (more kernels than a plan uses: begin again)
+    p.smem_set[i] = {kern, dev, (size_t)most};
+    p.n_smem_set = i + 1;
+  }
+  return bytes <= p.smem_set[i].bytes ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 mla_status_t mla_validate_config(const mla_config_t* c) { return validate_config(c); }

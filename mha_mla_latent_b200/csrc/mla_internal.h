@@ -85,6 +85,15 @@ struct mla_plan {
   int opt_pdl = 1;                            // programmatic dependent launch
   int64_t opt_wait_us = 1000000;              // bound of each pipeline wait (tensor-core kernel)
   int opt_skip_tile = 0;                      // testing: leave out one latent copy per CTA
+  // kernels whose shared memory limit was set (mla_smem_limit; calls on one plan do not overlap)
+  static constexpr int kSmemSets = 24;
+  struct SmemSet {
+    const void* kern;
+    int device;
+    size_t bytes;
+  };
+  mutable SmemSet smem_set[kSmemSets];
+  mutable int n_smem_set = 0;
 };
 
 // Launches a kernel, with programmatic stream serialization when `pdl` is set (the kernel
@@ -105,9 +114,9 @@ inline cudaError_t mla_launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 blo
   return cudaLaunchKernelEx(&lc, kern, std::forward<Args>(args)...);
 }
 
-// Allows `kern` `bytes` of dynamic shared memory on the current device (mla_api.cpp).  The
-// largest size set so far is remembered per kernel and device, so a call sets it at most once.
-cudaError_t mla_smem_limit(const void* kern, size_t bytes);
+// Allows `kern` `bytes` of dynamic shared memory on the current device (mla_api.cpp): set once per
+// plan and kernel (a call per launch takes the host some 0.5 us).
+cudaError_t mla_smem_limit(const mla_plan& p, const void* kern, size_t bytes);
 
 // Kernels of a call that the profiling options can bracket with events.
 enum MlaProfKernel { kProfAppend = 0, kProfAbsorb = 1, kProfAttention = 2, kProfCombine = 3 };

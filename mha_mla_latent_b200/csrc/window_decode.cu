@@ -1424,12 +1424,12 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   const int KP = (cfg.head_dim + 15) & ~15;
   const size_t smem_b = sizeof(__nv_bfloat16) * ((size_t)KP * (kACols + 8) + (size_t)kARows * (KP + 8));
   const int n_rba = (B * a.G + kARows - 1) / kARows, n_cca = (cfg.d_c + kACols - 1) / kACols;
-  cudaError_t e = mla_smem_limit((const void*)window_absorb_kernel, smem_b);
+  cudaError_t e = mla_smem_limit(p, (const void*)window_absorb_kernel, smem_b);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfAbsorb, false, s);
   if (e == cudaSuccess)
     e = mla_launch_kernel(window_absorb_kernel, dim3(cfg.n_kv_heads * n_rba * n_cca), dim3(kAThreads), smem_b, s, p.opt_pdl, b);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfAbsorb, true, s);
-  if (e == cudaSuccess) e = mla_smem_limit((const void*)kern, L.total);
+  if (e == cudaSuccess) e = mla_smem_limit(p, (const void*)kern, L.total);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfAttention, false, s);
   if (e == cudaSuccess)
     e = mla_launch_kernel(kern, dim3(D.G), dim3(qbits ? kThreadsOf<4> : kThreadsOf<0>), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_q, a);
@@ -1443,7 +1443,7 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
   const size_t smem = sizeof(__nv_bfloat16) * ((size_t)cfg.d_c * (kMCols + 8) + 2 * (size_t)kMRows * (cfg.d_c + 8));
   const int n_rb = (B * a.G + kMRows - 1) / kMRows, n_cc = (cfg.head_dim + kMCols - 1) / kMCols;
   const auto merge = cfg.d_c <= 64 ? window_merge_kernel<16> : cfg.d_c <= 128 ? window_merge_kernel<32> : window_merge_kernel<64>;
-  e = mla_smem_limit((const void*)merge, smem);
+  e = mla_smem_limit(p, (const void*)merge, smem);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfCombine, false, s);
   if (e == cudaSuccess)
     e = mla_launch_kernel(merge, dim3(cfg.n_kv_heads * n_rb * n_cc), dim3(kMThreads), smem, s, p.opt_pdl, m);

@@ -807,7 +807,7 @@ cudaError_t mla_launch_window_fused(const mla_plan& p, const mla_cache_t& c, con
     return qbits == 4 ? window_fused_kernel<PAGED, 4> : qbits == 2 ? window_fused_kernel<PAGED, 2> : window_fused_kernel<PAGED, 0>;
   };
   const auto kern = c.block_table ? pick(std::true_type()) : pick(std::false_type());
-  cudaError_t e = mla_smem_limit((const void*)kern, L.total);
+  cudaError_t e = mla_smem_limit(p, (const void*)kern, L.total);
   if (e != cudaSuccess) return e;
   if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
   e = mla_launch_kernel(kern, dim3((unsigned)units), dim3(qbits ? kThreadsOf<4> : kThreadsOf<0>), L.total, s, p.opt_pdl, tm_c, tm_kr, tm_uk, tm_uv, a);

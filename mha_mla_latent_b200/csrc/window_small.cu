@@ -353,7 +353,7 @@ cudaError_t mla_launch_window_small(const mla_plan& p, const mla_cache_t& c, con
   else
     kern = G == 1 ? window_small_kernel<__nv_bfloat16, 1> : G == 2 ? window_small_kernel<__nv_bfloat16, 2>
            : G == 3 ? window_small_kernel<__nv_bfloat16, 3> : window_small_kernel<__nv_bfloat16, 4>;
-  cudaError_t e = mla_smem_limit((const void*)kern, L.total);
+  cudaError_t e = mla_smem_limit(p, (const void*)kern, L.total);
   if (e == cudaSuccess) e = mla_profile_event(p, kProfAttention, false, s);
   if (e == cudaSuccess)
     e = mla_launch_kernel(kern, dim3((unsigned)(B * a.n_kv)), dim3(kThreads), L.total, s, p.opt_pdl, a);
