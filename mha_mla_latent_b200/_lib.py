@@ -125,8 +125,10 @@ def _ptr(t):
 
 
 # torch's current stream of the current device as a raw handle (torch.cuda.current_stream()
-# builds a Stream object each time: about 1.5 us of a call's host time)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# builds a Stream object each time: about 1.5 us of a call's host time); a torch without CUDA
+# serves the entry points that need no GPU
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 _current_device = torch.cuda.current_device
 
 

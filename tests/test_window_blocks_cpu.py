@@ -133,3 +133,18 @@ def test_host_tensors_are_refused(mla):
         with pytest.raises(ValueError):
             call()
     assert cache.device == -1
+
+
+def test_import_with_a_torch_without_cuda(mla):
+    """The entry points that need no GPU work where torch was built without CUDA."""
+    import os
+    import subprocess
+    import sys
+    program = ("import torch; del torch._C._cuda_getCurrentRawStream\n"
+               "import mha_mla_latent_b200._lib as L\n"
+               "cfg = L.make_config(64, 8, 4, 64, 4, 64)\n"
+               "print(L.mla_fixed_pairs(cfg, L.MLA_PAIRS_HIGH).tolist(), L.mla_cache_bytes_per_token(cfg))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split() == "[[0, 1, 2, 3], [0, 1, 2, 3], [0, 1, 2, 3], [0, 1, 2, 3]] 192".split()
