@@ -232,7 +232,9 @@ struct DecodeArgs {
 constexpr int kSimtTile = 32;
 constexpr int kSimtMaxE = 32;   // H*d_c / 256 owned accumulators per thread
 
-template <typename T, bool INT4>
+// WIN: sliding window with sinks (a form of its own: with the tests for hidden rows in it the
+// kernel without a window takes 5 to 8% longer).
+template <typename T, bool INT4, bool WIN>
 __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
   const int H = a.H, dc = a.d_c, R = a.R, r2 = 2 * a.r;
   const int G = H / a.n_kv;
@@ -258,18 +260,20 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeArgs a) {
     if (tid < H) { s_m[tid] = -INFINITY; s_l[tid] = 0.f; }
     // residual window: tokens from lo on may be read unquantised from the ring
     const int lo = (INT4 && a.cache.c_resid) ? __ldg(a.seq_lens + b) - MLA_RESID_WINDOW : INT_MAX;
-    const Span span = a.win.window > 0 ? unit_span(__ldg(a.seq_lens + b), 1, kSimtTile, a.win) : Span();
+    const Span span = WIN ? unit_span(__ldg(a.seq_lens + b), 1, kSimtTile, a.win) : Span();
     float O[kSimtMaxE];
 #pragma unroll
     for (int e = 0; e < kSimtMaxE; ++e) O[e] = 0.f;
     __syncthreads();
     for (int t = t0; t < t1; t += kSimtTile) {
       const int n = min(kSimtTile, t1 - t);
-      const int ta = span.token(t);                       // the tile's first cached token
+      const int ta = WIN ? span.token(t) : t;             // the tile's first cached token
       const MlaLoc lc = mla_loc(a.cache, b, ta, a.err);   // a 32-token tile lies in one block
-      // tile rows [hid0, hid1) lie between the sinks and the window: neither read nor scored
-      const int hid0 = a.win.window > 0 ? max(0, a.win.n_sink - ta) : 0, hid1 = span.lo - ta;
-      auto hidden = [&](int tt) { return tt >= hid0 && tt < hid1; };
+      // tile rows [hid0, hid1) lie between the sinks and the window: their latent is not read (it
+      // would meet P = 0), their keys are read with the tile's and their scores dropped (in the
+      // window's two border tiles at most; tests in those loops take longer than the loads)
+      const int hid0 = max(0, a.win.n_sink - ta), hid1 = span.lo - ta;
+      auto hidden = [&](int tt) { return WIN && tt >= hid0 && tt < hid1; };
       const size_t slot0 = (size_t)lc.pb * lc.cap + lc.pt;
       for (int i = tid; i < n * dc; i += 256) {
         int tt = i / dc, cc = i % dc;
@@ -665,10 +669,11 @@ cudaError_t launch_attention_combine(const mla_plan& p, const mla_cache_t& c, co
     size_t smem = sizeof(float) * ((size_t)H * cfg.d_c + H * 2 * cfg.r_pairs +
                                    kSimtTile * (cfg.d_c + 1) + kSimtTile * (p.R + 1) +
                                    kSimtTile * H + 3 * H);
-    e = mla_smem_limit(p, (const void*)decode_simt_kernel<T, INT4>, smem);
+    const auto kern = aa.win.window > 0 ? decode_simt_kernel<T, INT4, true> : decode_simt_kernel<T, INT4, false>;
+    e = mla_smem_limit(p, (const void*)kern, smem);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, false, s)) != cudaSuccess) return e;
-    e = mla_launch_kernel(decode_simt_kernel<T, INT4>, dim3(L.G), dim3(256), smem, s, p.opt_pdl, da);
+    e = mla_launch_kernel(kern, dim3(L.G), dim3(256), smem, s, p.opt_pdl, da);
     if (e != cudaSuccess) return e;
     if ((e = mla_profile_event(p, kProfAttention, true, s)) != cudaSuccess) return e;
   } else if (L.kernel == 4) {
