@@ -449,7 +449,7 @@ mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t* cache,
   DecodeLayout L = mla_decode_layout(*plan, B, kernel);
   if (ws_bytes < L.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const MlaWindow win = window_of(*cache, n_sink, window);
-  if (plan->opt_kernel == 0 && mla_window_small_pick(*plan, *cache, B, win))
+  if (plan->opt_kernel == 0 && mla_window_small_pick(*plan, *cache, B, win, kernel))
     return cuda_status(mla_launch_window_small(*plan, *cache, seq_lens, q, B, out, win, (cudaStream_t)stream));
   return cuda_status(mla_launch_decode(*plan, *cache, seq_lens, q, B, out, workspace, L, (cudaStream_t)stream, win));
 }

@@ -206,8 +206,9 @@ cudaError_t mla_launch_window_decode(const mla_plan& p, const mla_cache_t& c, co
                                      int B, void* out, void* ws, const DecodeLayout& D, MlaWindow win, cudaStream_t s);
 
 // The windowed decode of small problems in one launch (window_small.cu): whether this call is
-// one, and its launch.  It needs no workspace.
-bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win);
+// one (`kernel`: what else would run it, mla_pick_window_kernel), and its launch.  It needs no
+// workspace.
+bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win, int kernel);
 cudaError_t mla_launch_window_small(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q, int B,
                                     void* out, MlaWindow win, cudaStream_t s);
 

@@ -317,21 +317,33 @@ static bool small_shape(const mla_plan& p) {
          G * c.r_pairs <= mla::wsmall::kThreads && mla::wsmall::layout(c).total <= 200 * 1024;
 }
 
-// The rule.  Without the tensor-core form (float32, other numbers of kept pairs) it is taken for
-// up to 1152 visible tokens: 5.6 us against 15 us for the split CUDA-core form at 64 tokens of
-// the tiny float32 layer, 17 us against 24 us at 1000.  Else while a CTA's rows are few (66 KB
-// with 64 B for the keys and the look-up of each) and the CTAs run at once: Llama-shaped layer,
-// 4 sequences, one launch against three: d_c = 64 9.4 / 12.7 us at 256 tokens, 13.4 / 12.8 at
-// 512; d_c = 256 10.0 / 14.5 us at 16 tokens, 16.6 / 14.4 at 128; SmolLM-shaped, 16 sequences
-// 8.8 / 11.9 at 256, 12.6 / 12.1 at 516 (and 4 us less of the host's time for two launches fewer).
-bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win) {
+// The rule, from device times of 16 layers (1 to 32 KV heads, 1 to 4 query heads each, d_c 32 to
+// 256) at 1 to 192 sequences and 16 to 1100 visible tokens, one launch against the others:
+// where those run on the CUDA cores (float32, other numbers of kept pairs) it is always the faster
+// one (9 heads, r = 3, 16 sequences: 7.0 / 20.9 us at 16 tokens, 19.5 / 34.4 at 1100; float32, 32
+// heads, d_c = 128, 192 sequences: 124 / 333 and 1373 / 4231).  The tensor-core launches take 10
+// to 15 us (up to 32 heads) or 18 to 23 (the head-row kernel, more heads) while the call is small,
+// which is met by an estimate of this kernel: a CTA takes 6 us, time for its weights, and per token
+// the lanes of a row (a power of two of 16-byte units) times 1.6 ns + 0.5 per query head, a quarter
+// more with two CTAs on an SM; with more CTAs than run at once it is behind.  Crossings: 32 heads
+// over 32 KV heads, 4 sequences, d_c = 64 13.0 / 13.0 us at 400 tokens, d_c = 256 12.6 / 15.0 at 64
+// and 17.0 / 15.4 at 128; 9 heads over 3, d_c = 32, 16 sequences 11.1 / 12.5 at 400 and 13.6 / 13.3 at
+// 640; 64 heads over 32, d_c = 128, 4 sequences 16.8 / 20.5 at 256 and 24.2 / 20.3 at 400.  Over all
+// of them a choice costs 0.3% more than the better of the two.
+bool mla_window_small_pick(const mla_plan& p, const mla_cache_t& c, int B, MlaWindow win, int kernel) {
   if (!small_shape(p)) return false;
+  const mla_config_t& cfg = p.cfg;
   const long long tokens = std::min<long long>(c.T_cap, (long long)win.n_sink + win.window);
   if (tokens > mla::wsmall::kMaxTokens) return false;
-  if (!mla_window_decode_capable(p)) return true;
-  const long long bytes = tokens * (p.cfg.d_c * 2 + 64), ctas = (long long)B * p.cfg.n_kv_heads;
-  const int per_sm = mla::wsmall::layout(p.cfg).total <= 110 * 1024 ? 2 : 1;
-  return bytes <= 66 * 1024 && ctas <= (long long)per_sm * p.num_sms;
+  if (kernel == 1) return true;
+  const long long ctas = (long long)B * cfg.n_kv_heads;
+  const int per_sm = mla::wsmall::layout(cfg).total <= 110 * 1024 ? 2 : 1;
+  if (ctas > (long long)per_sm * p.num_sms) return false;
+  const int G = cfg.n_heads / cfg.n_kv_heads, units = cfg.d_c / 8;   // (bf16)
+  int lanes = 1;
+  while (lanes < units && lanes < 32) lanes <<= 1;
+  const float us = 6.f + 7e-5f * (G * cfg.head_dim * cfg.d_c) + lanes * (1.6e-3f + 0.5e-3f * G) * tokens;
+  return us * (ctas > p.num_sms ? 1.25f : 1.f) <= (kernel == 5 ? 13.f : 20.f);
 }
 
 cudaError_t mla_launch_window_small(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_lens, const void* q, int B,

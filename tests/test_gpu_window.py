@@ -654,3 +654,39 @@ def test_tensors_that_do_not_fit_are_refused():
     torch.cuda.synchronize()
     assert mla.mla_device_error(plan) == 0
     plan.close()
+
+
+@pytest.mark.parametrize("B", [2, 64])
+def test_default_kernel_keeps_up_with_a_forced_one(B):
+    """Layers with more heads than the windowed tensor-core kernel takes: the one-launch form is for
+    few rows only (at 64 sequences it takes seven times the head-row kernel's time)."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(H=64, n_kv=32, d_h=64, d_c=128, seed=24)
+    cache = make_cache(mla, layer, B, 1100, False)
+    cache.c_kv.normal_()
+    cache.k_rope.normal_()
+    plan = layer.plan(mla)
+    q = layer.queries(B).cuda()
+    out = torch.empty_like(q)
+    lens = torch.full((B,), 1100, dtype=torch.int32, device="cuda")
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, B), dtype=torch.uint8, device="cuda")
+    best = {}
+    for kernel in (0, 3):
+        mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+        graph = torch.cuda.CUDAGraph()
+        mla.mla_decode_window(plan, cache.struct, lens, q, out, ws, 0, 1100)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                mla.mla_decode_window(plan, cache.struct, lens, q, out, ws, 0, 1100)
+        times = []
+        for _ in range(6):
+            t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            t[0].record()
+            graph.replay()
+            t[1].record()
+            torch.cuda.synchronize()
+            times.append(t[0].elapsed_time(t[1]))
+        best[kernel] = min(times[1:])
+    assert best[0] <= 1.5 * best[3], best
+    plan.close()
