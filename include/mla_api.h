@@ -473,7 +473,8 @@ MLA_API mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, 
  * block loses a holder.  `copies` lists the rows to move, in order of b (at most one per
  * sequence: seq_lens[b] % 128 rows); run mla_blocks_copy with every layer's cache before the
  * append.  When the pool has too few free blocks nothing is allocated for any sequence: table
- * and counts stay, no copies are listed, and MLA_DEVERR_POOL is set.
+ * and counts stay, no copies are listed, and MLA_DEVERR_POOL is set; the append must then be held
+ * back, a shared block would take its rows (mla_append skips tokens at position -1).
  *   seq_lens, new_lens device [B] int32, 0 <= seq_lens <= new_lens <= 128 n_cols: a sequence
  *     outside that gets nothing and sets MLA_DEVERR_SEQ_LEN; one whose partly filled block is
  *     missing from the table sets MLA_DEVERR_BLOCK
@@ -486,7 +487,8 @@ MLA_API mla_status_t mla_blocks_reserve(const int32_t* table, const int32_t* ref
 /* Release what no later query reads: every table entry whose block holds no token of
  * [0, min(n_sink, L)) or [L - window, L), L = seq_lens[b], becomes -1 and its block loses a
  * holder.  With the n_sink and window of mla_decode_window the next steps of every sequence
- * keep all they see.  Blocks behind the length are released too; L = 0 frees the whole row.
+ * keep all they see.  Blocks behind the length are released too, room that a reserve made there
+ * included; L = 0 frees the whole row.
  *   seq_lens device [B] int32 in [0, 128 n_cols]: out of range leaves the row as it is and
  *     sets MLA_DEVERR_SEQ_LEN;  n_sink >= 0, window >= 0 (0 with n_sink = 0 frees every row) */
 MLA_API mla_status_t mla_blocks_trim(const int32_t* table, const int32_t* refs, int32_t B, int32_t n_cols,

@@ -178,7 +178,14 @@ class BlockPool:
 
     def reserve(self, seq_lens, new_lens, stream=None) -> None:
         """Blocks for tokens [seq_lens[b], new_lens[b]) of every sequence; shared, partly
-        filled blocks are copied on write, shared ones behind the length replaced."""
+        filled blocks are copied on write, shared ones behind the length replaced.
+
+        Nothing is returned, and nothing waits: where the pool has too few free blocks, no sequence
+        gets any, MLA_DEVERR_POOL is set in status[1] and a shared, partly filled block stays
+        shared.  An append must not follow then (it would write into the other holder's tokens):
+        look at `errors`, or keep the decision on the device, with
+        torch.where((pool.status[1] & MLA_DEVERR_POOL) != 0, -1, pos) as the append's positions
+        (tokens at -1 are skipped)."""
         with self._on(stream):
             _lib.mla_blocks_reserve(self.table, self.refs, self._int32(seq_lens), self._int32(new_lens), self.table,
                                     self.refs, self.copies, self.status, self.workspace)
@@ -186,7 +193,8 @@ class BlockPool:
 
     def trim(self, seq_lens, n_sink: int, window: int, stream=None) -> None:
         """Releases the blocks that mla_decode_window does not read any more; a sequence of
-        length 0 is freed."""
+        length 0 is freed.  Blocks behind the length are given back too, those that a reserve
+        just made room with included: trim first, or with the lengths that the reserve was for."""
         with self._on(stream):
             _lib.mla_blocks_trim(self.table, self.refs, self._int32(seq_lens), n_sink, window, self.table, self.refs,
                                  self.status)
