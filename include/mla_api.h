@@ -108,8 +108,8 @@ typedef struct {
  * multiple of 128 (the logical capacity: T_cap / 128 table entries per sequence).  The
  * README "MHA2MLA" runs ragged LongBench batches; 128-token blocks match the decode tile,
  * so each tile of the attention kernel reads one block.  A table entry outside
- * [0, n_blocks) flags MLA_DEVERR_BLOCK and reads or writes block 0 instead.  The arrays
- * may hold at most 2^31 - 1 token rows (B * T_cap, or n_blocks * 128 when paged); a larger
+ * [0, n_blocks) flags MLA_DEVERR_BLOCK; block 0 is read in its place, and an append writes
+ * nothing to the pool for the token.  The arrays may hold at most 2^31 - 1 token rows (B * T_cap, or n_blocks * 128 when paged); a larger
  * view is refused with MLA_ERR_UNSUPPORTED.
  *   c_kv      SAME: [B][T_cap][d_c] dtype;  INT4*: [B][T_cap][d_c/2] uint8 codes;
  *             INT2: [B][T_cap][d_c/4] uint8 codes
@@ -244,7 +244,8 @@ MLA_API mla_status_t mla_plan_set_option(mla_plan_t* plan, int32_t option, int64
  * at (seq_idx[n], pos[n]).  Notes §关键设计 (SVDjoint: c_kv = x W_dkv; partial-RoPE).
  *   x       device [N][d] dtype
  *   seq_idx device [N] int32 in [0, B);  pos device [N] int32 in [0, T_cap)
- * Tokens with an out-of-range seq_idx/pos are skipped and flag the device error word.
+ * Tokens with an out-of-range seq_idx/pos, or without a block in a paged cache's table, are
+ * skipped and flag the device error word.
  * Distinct tokens must target distinct (seq, pos) slots.  With the residual window
  * (MLA_CACHE_INT4_G32_R128) one call may carry any number of a sequence's tokens: a first
  * kernel raises resid_pos[slot] to the largest position of the call that maps to the slot,

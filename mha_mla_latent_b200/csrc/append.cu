@@ -53,7 +53,8 @@ __device__ void append_epilogue(const AppendArgs& a, const float* tile, int tok0
       if (col == 0) raise_error(a.err, MLA_DEVERR_APPEND_SLOT);
       continue;
     }
-    const MlaLoc lc = mla_loc(c, sq, p, a.err);
+    const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
+    if (lc.pb < 0) continue;   // no block to write into: another sequence's is not touched
     const size_t slot = (size_t)lc.pb * lc.cap + lc.pt;
     const float v0 = tile[t * COLS + 2 * cp], v1 = tile[t * COLS + 2 * cp + 1];
     if (col < a.d_c) {
@@ -83,10 +84,10 @@ __device__ void append_epilogue(const AppendArgs& a, const float* tile, int tok0
       int sq, p;
       append_slot(a, n, &sq, &p);
       if (sq < 0 || sq >= c.B || p < 0 || p >= c.T_cap) continue;
-      const MlaLoc lc = mla_loc(c, sq, p, a.err);
+      const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
       const size_t slot = (size_t)lc.pb * lc.cap + lc.pt;
       const float v = tile[t * COLS + gi * 32 + lane];
-      quant_group_store(c, slot, a.d_c, col, lane, v, a.qbits);
+      if (lc.pb >= 0) quant_group_store(c, slot, a.d_c, col, lane, v, a.qbits);
       const bool own = __shfl_sync(0xffffffffu, lane == 0 ? resid_owns(c, sq, p, a.step_lens != nullptr) : false, 0);
       if (own) resid_store(c, sq, p, a.d_c, col, v);
     }

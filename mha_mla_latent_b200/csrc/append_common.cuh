@@ -158,7 +158,8 @@ __device__ __forceinline__ void append_small_finish(const AppendSmallArgs& sa, f
       continue;
     }
     const float v0 = tileb[t * kSmCols + 2 * cp], v1 = tileb[t * kSmCols + 2 * cp + 1];
-    const MlaLoc lc = mla_loc(c, sq, p, a.err);
+    const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
+    if (lc.pb < 0) continue;   // no block to write into: another sequence's is not touched
     if (col < a.d_c) {
       if (!INT4) {
         T* dst = (T*)c.c_kv + ((size_t)lc.pb * lc.cap + lc.pt) * a.d_c + col;
@@ -180,10 +181,10 @@ __device__ __forceinline__ void append_small_finish(const AppendSmallArgs& sa, f
       const int n = tok0 + t;
       const int sq = s_sq[t], p = s_pos[t];
       if (n >= a.N || sq < 0 || sq >= c.B || p < 0 || p >= c.T_cap) continue;
-      const MlaLoc lc = mla_loc(c, sq, p, a.err);
+      const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
       const size_t slot = (size_t)lc.pb * lc.cap + lc.pt;
       const float v = tileb[t * kSmCols + lane];
-      quant_group_store(c, slot, a.d_c, col0 + lane, lane, v, a.qbits);
+      if (lc.pb >= 0) quant_group_store(c, slot, a.d_c, col0 + lane, lane, v, a.qbits);
       const bool own = __shfl_sync(0xffffffffu, lane == 0 ? resid_owns(c, sq, p, a.step_lens != nullptr) : false, 0);
       if (own) resid_store(c, sq, p, a.d_c, col0 + lane, v);
     }

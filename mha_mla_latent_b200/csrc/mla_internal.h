@@ -22,14 +22,21 @@ struct MlaLoc {
   int pb, pt, cap;
 };
 #ifdef __CUDACC__
-inline __device__ MlaLoc mla_loc(const mla_cache_t& c, int b, int t, int32_t* err) {
+// Without a block in the table: pb = -1, flagged.
+inline __device__ MlaLoc mla_loc_or_none(const mla_cache_t& c, int b, int t, int32_t* err) {
   if (!c.block_table) return MlaLoc{b, t, c.T_cap};
   int blk = __ldg(c.block_table + (size_t)b * (c.T_cap / MLA_BLOCK_TOKENS) + t / MLA_BLOCK_TOKENS);
   if (blk < 0 || blk >= c.n_blocks) {
     atomicOr(err, MLA_DEVERR_BLOCK);
-    blk = 0;
+    blk = -1;
   }
   return MlaLoc{blk, t & (MLA_BLOCK_TOKENS - 1), MLA_BLOCK_TOKENS};
+}
+// The same for reading: block 0 in its place.
+inline __device__ MlaLoc mla_loc(const mla_cache_t& c, int b, int t, int32_t* err) {
+  MlaLoc lc = mla_loc_or_none(c, b, t, err);
+  if (lc.pb < 0) lc.pb = 0;
+  return lc;
 }
 #endif
 // Token rows in the arrays of the cache (the pool's rows when paged).

@@ -200,3 +200,36 @@ def test_long_windows_on_the_other_kernels(name, kernel):
             ref = layer.reference(q[b], seqs[b], L - 1, n_sink, window).numpy()
             assert_close(got[b], ref, layer.dtype, f"{name} {kernel} sinks {n_sink} window {window} length {L}")
     plan.close()
+
+
+@pytest.mark.parametrize("kind", [dict(d_c=64), dict(d_c=128, cache="int4"), dict(d_c=128, cache="int4_r128"), dict(d_c=64, cache="int2"),
+                                  dict(dtype="f32", H=4, n_kv=4, d_h=32, r=2, d_c=32)], ids=str)
+def test_append_without_a_block_touches_no_other_sequence(kind):
+    """A token whose column has no block (no reserve, or trimmed since) goes nowhere: block 0 belongs to
+    whoever holds it."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(**kind, seed=36)
+    plan = full_plan(mla, layer, 6)
+    pool = BlockPool(2, 1024, 8)
+    cache = pool.layer(layer.config(mla))
+    g = torch.Generator().manual_seed(8)
+    i32 = lambda v: torch.as_tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows = lambda n: torch.randn(n, HIDDEN, generator=g).to(layer.td).cuda()  # noqa: E731
+    pool.reserve([0, 0], [300, 0])
+    assert pool.table[0, :3].tolist() == [0, 1, 2]
+    mla.mla_append(plan, rows(300), i32([0] * 300), i32(range(300)), cache.struct)
+    arrays = [a for a in (cache.c_kv, cache.c_scales, cache.k_rope) if a is not None]
+    before = [a.clone() for a in arrays]
+    for n in (1, 40, 500):       # each form of the append
+        mla.mla_append(plan, rows(n), i32([1] * n), i32(range(n)), cache.struct)
+        assert mla.mla_device_error(plan) == mla.MLA_DEVERR_BLOCK
+        assert all(torch.equal(a, b) for a, b in zip(arrays, before)), n
+    q = torch.randn(2, layer.H, layer.d_h, generator=g).to(layer.td).cuda()
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, 2), dtype=torch.uint8, device="cuda")
+    mla.mla_decode_step(plan, cache.struct, i32([300, 5]), rows(2), q, torch.empty_like(q), ws)   # row 0 rewrites token 299
+    assert mla.mla_device_error(plan) == mla.MLA_DEVERR_BLOCK
+    for a, b in zip(arrays, before):
+        b[2, 299 % 128] = a[2, 299 % 128]
+        assert torch.equal(a, b)
+    plan.close()
