@@ -509,14 +509,16 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(CombineArgs a) {
       if (lane < nc4) *reinterpret_cast<float4*>(o + 4 * lane) = make_float4(a0.x * inv, a0.y * inv, a0.z * inv, a0.w * inv);
       if (lane + 32 < nc4)
         *reinterpret_cast<float4*>(o + 4 * lane + 128) = make_float4(a1.x * inv, a1.y * inv, a1.z * inv, a1.w * inv);
-      for (int c4 = lane + 64; c4 < nc4; c4 += 32) {   // latents wider than 256
+      for (int c0 = 64; c0 < nc4; c0 += 32) {   // latents wider than 256 (the whole warp takes each turn: it shares the weights)
+        const int c4 = c0 + lane;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < np; ++j) {
           const float w = j < 32 ? __shfl_sync(0xffffffffu, wl, j) : exp2f(__ldg(ml + 2 * j) - M);
+          if (c4 >= nc4) continue;
           const float4 x = __ldg(reinterpret_cast<const float4*>(op + (size_t)j * ps) + c4);
           acc.x += w * x.x; acc.y += w * x.y; acc.z += w * x.z; acc.w += w * x.w;
         }
-        *reinterpret_cast<float4*>(o + 4 * c4) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (c4 < nc4) *reinterpret_cast<float4*>(o + 4 * c4) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       }
     } else {
       for (int c = lane; c < dc; c += 32) o[c] = 0.f;

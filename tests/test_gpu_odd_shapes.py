@@ -1,0 +1,45 @@
+"""Decode over layer shapes at the edges of what the CUDA-core kernels take: latents wider than 256
+or not a multiple of 16, head dims that are even but not multiples of four."""
+
+import pytest
+import torch
+
+from tests.helpers import assert_close
+from tests.window_helpers import Layer, hidden_tokens, make_cache, store
+
+pytestmark = pytest.mark.gpu
+
+
+def check_decode(**kw):
+    """mla_decode and mla_decode_window against the definition."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(**kw, seed=40)
+    lens, T_cap = [200, 1, 77, 130], 256
+    seqs = [layer.sequence(L) for L in lens]
+    q = layer.queries(len(lens))
+    plan = layer.plan(mla)
+    L32 = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, len(lens)), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    for kernel in (0, 1):
+        mla.mla_plan_set_option(plan, mla.MLA_OPT_DECODE_KERNEL, kernel)
+        for n_sink, window in [(0, 0), (5, 60), (0, 1000)]:   # (0, 0): no window
+            cache = make_cache(mla, layer, len(lens), T_cap, True)
+            for b, s in enumerate(seqs):
+                store(cache, b, s, hidden_tokens(lens[b], lens[b] - 1, n_sink, window) if window else None)
+            out = torch.full_like(q, float("nan"), device="cuda")
+            if window:
+                mla.mla_decode_window(plan, cache.struct, L32, q.cuda(), out, ws, n_sink, window)
+            else:
+                mla.mla_decode(plan, cache.struct, L32, q.cuda(), out, ws)
+            assert mla.mla_device_error(plan) == 0
+            for b, L in enumerate(lens):
+                ref = layer.reference(q[b], seqs[b], L - 1, n_sink, window or 1000).numpy()
+                assert_close(out[b].double().cpu().numpy(), ref, layer.dtype, f"{kw} kernel {kernel} {n_sink} {window} {L}")
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype,H,n_kv,d_h,r,d_c", [("f32", 8, 2, 64, 0, 300), ("f32", 4, 4, 32, 2, 260), ("bf16", 8, 2, 64, 3, 304),
+                                                    ("f32", 2, 1, 64, 4, 1020), ("f32", 4, 1, 64, 4, 512)])
+def test_latents_wider_than_256(dtype, H, n_kv, d_h, r, d_c):
+    """Their last columns are merged by part of a warp."""
+    check_decode(dtype=dtype, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
