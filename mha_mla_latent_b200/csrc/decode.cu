@@ -165,7 +165,8 @@ __device__ __forceinline__ void absorb_body(const AbsorbArgs& a, int blk_id, flo
   // ---- CUDA-core form: W slice and query rows as float in shared memory; warp r takes
   // row r, lane l columns 2l, 2l+1 of the chunk
   float* s_w = sm;                              // [dh][kAbsCols]
-  float* s_q = s_w + dh * kAbsCols;             // [kAbsRows][dh]
+  const int QLD = (dh + 3) & ~3;                // rows of whole 16 bytes: a head dim may be 2 more than a multiple of 4
+  float* s_q = s_w + dh * kAbsCols;             // [kAbsRows][QLD]
   const int ncol = min(kAbsCols, a.d_c - c0);
   if (ncol < kAbsCols)
     for (int i = tid; i < dh * kAbsCols; i += blockDim.x) s_w[i] = 0.f;   // columns past d_c
@@ -173,11 +174,11 @@ __device__ __forceinline__ void absorb_body(const AbsorbArgs& a, int blk_id, flo
                     [&](int j) { return W + (size_t)j * a.d_c + c0; });
   pdl_wait();
   pdl_trigger();
-  stage_rows_f32<T>(s_q, dh, nrow, dh, a.vec_ok, q_row);
+  stage_rows_f32<T>(s_q, QLD, nrow, dh, a.vec_ok, q_row);
   __syncthreads();
-  rope([&](int r, int d) { return (double)s_q[r * dh + d]; });
+  rope([&](int r, int d) { return (double)s_q[r * QLD + d]; });
   const int r = warp, row = row0 + r, c = c0 + 2 * lane;
-  const float* qn = s_q + r * dh;
+  const float* qn = s_q + r * QLD;
   float acc0 = 0.f, acc1 = 0.f;
   int j = 0;
   for (; j + 4 <= dh; j += 4) {
@@ -615,7 +616,7 @@ void absorb_setup(const mla_plan& p, const mla_cache_t& c, const int32_t* seq_le
   const int KP = (cfg.head_dim + 15) & ~15;
   const size_t smem_work =
       aa->mma ? sizeof(__nv_bfloat16) * ((size_t)KP * (kAbsCols + 8) + (size_t)kAbsRowsMma * (KP + 8))
-              : sizeof(float) * ((size_t)cfg.head_dim * kAbsCols + (size_t)kAbsRows * cfg.head_dim);
+              : sizeof(float) * ((size_t)cfg.head_dim * kAbsCols + (size_t)kAbsRows * ((cfg.head_dim + 3) & ~3));
   const size_t sched_ints = (size_t)9 * B + 4 * L.G + 2;
   *smem = std::min<size_t>(std::max(smem_work, sched_ints * sizeof(int32_t)), std::max<size_t>(smem_work, 160 * 1024));
   aa->sched_ints = (int)(*smem / sizeof(int32_t));

@@ -43,3 +43,10 @@ def check_decode(**kw):
 def test_latents_wider_than_256(dtype, H, n_kv, d_h, r, d_c):
     """Their last columns are merged by part of a warp."""
     check_decode(dtype=dtype, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
+
+
+@pytest.mark.parametrize("dtype,H,n_kv,d_h,r,d_c", [("f32", 6, 3, 30, 2, 32), ("f32", 4, 4, 18, 4, 20), ("bf16", 4, 2, 22, 3, 64),
+                                                    ("bf16", 8, 8, 34, 4, 32), ("f32", 40, 10, 26, 1, 64), ("bf16", 6, 1, 6, 1, 32)])
+def test_head_dims_that_are_not_multiples_of_four(dtype, H, n_kv, d_h, r, d_c):
+    """The query rows in shared memory start on whole 16 bytes."""
+    check_decode(dtype=dtype, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
