@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(CombineArgs a) {
   const int row0 = rb * RB, d0 = dcb * NCOL;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int dc = a.d_c;
-  // bf16 with whole 16-byte rows: the output product runs as warp MMAs on bf16 tiles
-  const bool mma = std::is_same<T, __nv_bfloat16>::value && a.vec_ok && NCOL == 64 && d0 + 64 <= a.dh;
+  // bf16 with whole 16-byte rows and whole steps of 16 latent columns: the output product runs as
+  // warp MMAs on bf16 tiles
+  const bool mma = std::is_same<T, __nv_bfloat16>::value && a.vec_ok && dc % 16 == 0 && NCOL == 64 && d0 + 64 <= a.dh;
   constexpr int WLD = 64 + 8;            // bf16 W tile row stride (conflict-free ldmatrix)
   const int ALD = dc + 8;                // bf16 A tile row stride
   float* s_w = sm;                       // f32 [d_c][NCOL], or bf16 [d_c][WLD] for the MMA form

@@ -50,3 +50,11 @@ def test_latents_wider_than_256(dtype, H, n_kv, d_h, r, d_c):
 def test_head_dims_that_are_not_multiples_of_four(dtype, H, n_kv, d_h, r, d_c):
     """The query rows in shared memory start on whole 16 bytes."""
     check_decode(dtype=dtype, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
+
+
+@pytest.mark.parametrize("H,n_kv,d_h,r,d_c", [(4, 2, 64, 3, 36), (8, 8, 128, 2, 20), (3, 1, 64, 5, 40), (8, 1, 96, 4, 100), (2, 2, 64, 3, 264),
+                                              (10, 2, 64, 4, 72)])
+def test_bf16_latents_that_are_not_multiples_of_16(H, n_kv, d_h, r, d_c):
+    """The merge's product with W_uv takes 16 latent columns a step on the tensor cores, or goes column
+    by column."""
+    check_decode(dtype="bf16", H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
