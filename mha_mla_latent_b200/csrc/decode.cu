@@ -638,13 +638,18 @@ cudaError_t launch_combine(const mla_plan& p, int units, int H, int n_kv, int q_
   ca.sched = sched; ca.W_uv = p.W_uv; ca.out = out; ca.P = L.P;
   // many rows per W_uv group (a chunk of queries): more rows per CTA, fewer W stagings
   const int G = H / n_kv;
-  ca.rpw = units * G >= 64 * kCmbRows ? kCmbMaxRpw : 1;
-  const int RB = kCmbRows * ca.rpw, RBP = (RB + 15) & ~15;
-  ca.ncols = (size_t)cfg.d_c * (64 + RB) * sizeof(float) <= 160 * 1024 ? 64 : 32;
   ca.vec_ok = cfg.head_dim % (16 / (int)sizeof(T)) == 0;
   ca.q_chunk = q_chunk; ca.q_block = q_block; ca.heads = cfg.n_heads;
-  const size_t smem_c = (size_t)cfg.d_c * (ca.ncols + RB) * sizeof(float) +
-                        (size_t)RBP * (cfg.d_c + 8) * sizeof(__nv_bfloat16);   // + the MMA form's A tiles
+  int RB = 0;
+  size_t smem_c = 0;
+  for (ca.rpw = units * G >= 64 * kCmbRows ? kCmbMaxRpw : 1;; ca.rpw = 1) {   // (one row per warp always fits)
+    RB = kCmbRows * ca.rpw;
+    const int RBP = (RB + 15) & ~15;
+    ca.ncols = (size_t)cfg.d_c * (64 + RB) * sizeof(float) <= 160 * 1024 ? 64 : 32;
+    smem_c = (size_t)cfg.d_c * (ca.ncols + RB) * sizeof(float) +
+             (size_t)RBP * (cfg.d_c + 8) * sizeof(__nv_bfloat16);   // + the MMA form's A tiles
+    if (ca.rpw == 1 || smem_c <= 220 * 1024) break;
+  }
   const int n_rbc = (units * G + RB - 1) / RB, n_dc = (cfg.head_dim + ca.ncols - 1) / ca.ncols;
   cudaError_t e = mla_smem_limit(p, (const void*)combine_kernel<T>, smem_c);
   if (e != cudaSuccess) return e;

@@ -58,3 +58,24 @@ def test_bf16_latents_that_are_not_multiples_of_16(H, n_kv, d_h, r, d_c):
     """The merge's product with W_uv takes 16 latent columns a step on the tensor cores, or goes column
     by column."""
     check_decode(dtype="bf16", H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
+
+
+def test_wide_latents_of_many_sequences():
+    """The merge takes fewer rows per CTA where the latents leave no room for more."""
+    import mha_mla_latent_b200 as mla
+    layer = Layer(dtype="f32", H=2, n_kv=1, d_h=32, r=4, d_c=1024, seed=41)
+    B = 300
+    seq = layer.sequence(40)
+    cache = make_cache(mla, layer, B, 40, False)
+    for b in range(B):
+        store(cache, b, seq)
+    plan = layer.plan(mla)
+    q = layer.queries(B)
+    out = torch.empty_like(q, device="cuda")
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, B), dtype=torch.uint8, device="cuda")
+    lens = torch.full((B,), 40, dtype=torch.int32, device="cuda")
+    mla.mla_decode(plan, cache.struct, lens, q.cuda(), out, ws)
+    assert mla.mla_device_error(plan) == 0
+    for b in (0, 151, 299):
+        assert_close(out[b].double().cpu().numpy(), layer.reference(q[b], seq, 39, 0, 40).numpy(), "f32", str(b))
+    plan.close()
