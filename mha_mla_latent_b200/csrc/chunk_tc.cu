@@ -1134,7 +1134,8 @@ typedef decltype(&attn_tc_kernel<128, 0, false, false, false>) AttnKernel;
 
 template <bool WIN> static AttnKernel attn_kernel(int rows, int qbits, bool resid, bool paged) {
   if (rows == 128)
-    return qbits == 4 ? (paged ? attn_tc_kernel<128, 4, false, true, WIN> : attn_tc_kernel<128, 4, false, false, WIN>)
+    return qbits == 4 ? (resid ? (paged ? attn_tc_kernel<128, 4, true, true, WIN> : attn_tc_kernel<128, 4, true, false, WIN>)
+                               : (paged ? attn_tc_kernel<128, 4, false, true, WIN> : attn_tc_kernel<128, 4, false, false, WIN>))
            : qbits == 2 ? (paged ? attn_tc_kernel<128, 2, false, true, WIN> : attn_tc_kernel<128, 2, false, false, WIN>)
                         : (paged ? attn_tc_kernel<128, 0, false, true, WIN> : attn_tc_kernel<128, 0, false, false, WIN>);
   return qbits == 4 ? (resid ? (paged ? attn_tc_kernel<32, 4, true, true, WIN> : attn_tc_kernel<32, 4, true, false, WIN>)
