@@ -17,7 +17,7 @@
 // merged in tensor memory when a piece (part of one sequence) ends.
 //
 // What bounds it is HBM: the cached rows of the visible tokens, read once (ncu: 1.01 times their
-// bytes).  The products take about a third of that time at d_c = 256 and the softmax a tenth.
+// bytes; the tensor pipe is active for 7.6% of the kernel's time at d_c = 256).
 // B200, whole calls: 32 sequences, 4160 visible tokens, 32 heads, d_c = 256: 45 us for 136 MB, of
 // which tiles flow for about 28 (4.9 TB/s); the rest is the hand-over between the three launches,
 // the first tiles and the last tile's chain.  64 sequences, 4005 tokens, 4-bit d_c = 128: 56 us.

@@ -29,7 +29,7 @@
 // Bound by the tensor cores once the tiles flow (10 tiles of 128 tokens at d_c = 256 take 1.4 to
 // 1.8 us each, some 85% of the measured dense rate) and by the latency of its ends: about 6 us
 // from the launch to the first scores and 5 us from the last tile to the stored rows.  B200, 8
-// sequences x 64 queries, 32 KV heads, window 1024, d_c = 256: 34.4 us; 4-bit latent 51 us, where
+// sequences x 64 queries, 32 KV heads, window 1024, d_c = 256: 34.1 us; 4-bit latent 52 us, where
 // a tile's conversion (a thread per row, about 3 us) bounds it, and 33 us at d_c = 128.  The
 // head-row units with their absorption and merge launches take 179, 202 and 157 us there.
 #include <cuda.h>
