@@ -318,7 +318,8 @@ MLA_API mla_status_t mla_decode_chunk(const mla_plan_t* plan, const mla_cache_t*
  * visible tokens, not the length.  With window >= T_cap it is mla_decode's attention.  A visible
  * RoPE key that is not finite changes the outputs of its own KV head only, as the definition has
  * it (a score of -inf weighs nothing, +inf and NaN make a head's output NaN); the rows next to it
- * then take some milliseconds.
+ * then take some milliseconds.  (mla_decode_chunk, and mla_decode with more than 32 heads, need
+ * finite keys: one that is not may reach every head.)
  *   n_sink >= 0, window >= 1; the other arguments, the workspace and L == 0 as for mla_decode
  * Every cache kind and shape that mla_decode's CUDA-core kernel takes, and more heads where a
  * tensor-core kernel does.  Kernel (MLA_OPT_DECODE_KERNEL = 0): one launch on the CUDA cores for
