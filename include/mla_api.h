@@ -109,8 +109,8 @@ typedef struct {
  * README "MHA2MLA" runs ragged LongBench batches; 128-token blocks match the decode tile,
  * so each tile of the attention kernel reads one block.  A table entry outside
  * [0, n_blocks) flags MLA_DEVERR_BLOCK; block 0 is read in its place, and an append writes
- * nothing to the pool for the token.  The arrays may hold at most 2^31 - 1 token rows (B * T_cap, or n_blocks * 128 when paged); a larger
- * view is refused with MLA_ERR_UNSUPPORTED.
+ * nothing to the pool for the token.  The arrays may hold at most 2^31 - 1 token rows
+ * (B * T_cap, or n_blocks * 128 when paged); a larger view is refused with MLA_ERR_UNSUPPORTED.
  *   c_kv      SAME: [B][T_cap][d_c] dtype;  INT4*: [B][T_cap][d_c/2] uint8 codes;
  *             INT2: [B][T_cap][d_c/4] uint8 codes
  *   c_scales  INT4*, INT2: [B][T_cap][d_c/32] fp16;  SAME: must be NULL
@@ -338,9 +338,9 @@ MLA_API mla_status_t mla_decode_window(const mla_plan_t* plan, const mla_cache_t
  * Per query this is mla_decode_window with length p + 1, for keys that are not finite too.  Cache
  * rows of tokens that no query of the sequence sees may hold anything; the latent of a token that
  * some of its queries see must be finite (queries share the tiles they read, so what another
- * one does to the sequence's other queries is unspecified).  Arguments, workspace (mla_decode_chunk_workspace_bytes) and
- * supported shapes as for mla_decode_chunk; n_sink >= 0, window >= 1; Q == 1 is
- * mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED.  Head dims that are
+ * one does to the sequence's other queries is unspecified).  Arguments, workspace
+ * (mla_decode_chunk_workspace_bytes) and supported shapes as for mla_decode_chunk; n_sink >= 0,
+ * window >= 1; Q == 1 is mla_decode_window; MLA_OPT_DECODE_KERNEL = 2 returns MLA_ERR_UNSUPPORTED.  Head dims that are
  * multiples of 16 up to 128 run in one launch, the others (and option 3) as the head-row units
  * of mla_decode_chunk. */
 MLA_API mla_status_t mla_decode_chunk_window(const mla_plan_t* plan, const mla_cache_t* cache,

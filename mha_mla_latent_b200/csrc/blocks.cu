@@ -240,9 +240,9 @@ __device__ __forceinline__ Row row_of(const Table& t, const int32_t* refs, const
 // it writes there must not reach a fork's.
 __device__ __forceinline__ bool held_too(const int32_t* refs, int e) { return __ldcg(refs + e) > 1; }
 
-// Latency bound (5 to 6 us on 16 to 160 rows, 11 us with 65536 blocks).  CTA 0 decides while the others
-// copy the table and the counts (calls that are not in place);
-// after the cluster's barrier CTA 0 writes what changes.  Decisions read the input only.
+// Latency bound (5 to 6 us on 16 to 160 rows, 11 us with 65536 blocks).  CTA 0 decides while the
+// others copy the table and the counts (calls that are not in place); after the cluster's barrier
+// CTA 0 writes what changes.  Decisions read the input only.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 reserve_kernel(Table t, const int32_t* refs_in, const int32_t* __restrict__ seq_lens,
                const int32_t* __restrict__ new_lens, ReserveWs ws, int32_t* copies) {

@@ -842,7 +842,11 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
           }
         }
         some = true;
-        // P row of this token, rounded to bf16 (the product's operand type)
+        // P row of this token, rounded to bf16: both operands of a product have the latent's type.
+        // Tokens' errors are independent, so they cost about as much as the output's own rounding
+        // does (error against 64 bits 0.0024 of the output's norm; the one-launch form, which keeps
+        // float32, 0.0017); P in two halves would double O's products and P's buffers.  The sum
+        // takes P as it was: rounding to nearest has no bias to make up for.
         uint32_t pk[N / 2];
 #pragma unroll
         for (int h = 0; h < N; h += 2) {
@@ -959,8 +963,9 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
 }
 
 // ------------------------------------------------------------------ absorption
-// q_lat[row][c] = scale x log2(e) x sum_d q[row][d] W_ukF[g][d][c] (bf16, the attention's operand
-// type) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
+// q_lat[row][c] = scale x log2(e) x sum_d q[row][d] W_ukF[g][d][c] (summed in float32, rounded once
+// to bf16, the type of the latents that it meets in the attention's product: 2^-9 of a score's
+// terms) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
 // kept pairs of the rows, rotated at L - 1.  Latency bound: the W_uk slice and the frequencies
 // come from the plan and are fetched before the kernel ahead is waited for; what follows the
 // wait is one round trip for queries and lengths.
@@ -1257,7 +1262,7 @@ __global__ void __launch_bounds__(kMThreads, 2) window_merge_kernel(const __grid
 #pragma unroll
     for (int e = 0; e < kAcc; ++e) {
       const int c = 128 * e + 4 * quad;
-      if (c >= a.d_c || sub > 0 ) continue;
+      if (c >= a.d_c || sub > 0) continue;
       const uint32_t h0 = pack2(acc[e].x, acc[e].y), h1 = pack2(acc[e].z, acc[e].w);
       const uint32_t l0 = pack2(acc[e].x - __uint_as_float(h0 << 16), acc[e].y - __uint_as_float(h0 & 0xFFFF0000u));
       const uint32_t l1 = pack2(acc[e].z - __uint_as_float(h1 << 16), acc[e].w - __uint_as_float(h1 & 0xFFFF0000u));
