@@ -47,6 +47,13 @@ def test_latents_wider_than_256(dtype, H, n_kv, d_h, r, d_c):
     check_decode(dtype=dtype, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
 
 
+@pytest.mark.parametrize("cache,H,n_kv,d_h,r,d_c", [("int4", 8, 4, 64, 4, 288), ("int2", 4, 1, 64, 3, 320), ("int4_r128", 6, 2, 48, 4, 416),
+                                                    ("int4", 8, 8, 30, 1, 1024), ("int4_r128", 2, 2, 128, 0, 512)])
+def test_wide_latents_in_groups(cache, H, n_kv, d_h, r, d_c):
+    """The same with 4- or 2-bit latents, and with the newest tokens from the ring."""
+    check_decode(dtype="bf16", cache=cache, H=H, n_kv=n_kv, d_h=d_h, r=r, d_c=d_c)
+
+
 @pytest.mark.parametrize("dtype,H,n_kv,d_h,r,d_c", [("f32", 6, 3, 30, 2, 32), ("f32", 4, 4, 18, 4, 20), ("bf16", 4, 2, 22, 3, 64),
                                                     ("bf16", 8, 8, 34, 4, 32), ("f32", 40, 10, 26, 1, 64), ("bf16", 6, 1, 6, 1, 32)])
 def test_head_dims_that_are_not_multiples_of_four(dtype, H, n_kv, d_h, r, d_c):
