@@ -109,7 +109,7 @@ typedef struct {
  * README "MHA2MLA" runs ragged LongBench batches; 128-token blocks match the decode tile,
  * so each tile of the attention kernel reads one block.  A table entry outside
  * [0, n_blocks) flags MLA_DEVERR_BLOCK; block 0 is read in its place, and an append writes
- * nothing to the pool for the token.  The arrays may hold at most 2^31 - 1 token rows
+ * nothing for the token (the residual window's ring included).  The arrays may hold at most 2^31 - 1 token rows
  * (B * T_cap, or n_blocks * 128 when paged); a larger view is refused with MLA_ERR_UNSUPPORTED.
  *   c_kv      SAME: [B][T_cap][d_c] dtype;  INT4*: [B][T_cap][d_c/2] uint8 codes;
  *             INT2: [B][T_cap][d_c/4] uint8 codes

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(256) resid_claim_kernel(const int32_t* __restr
   for (int n = blockIdx.x * blockDim.x + threadIdx.x; n < N; n += gridDim.x * blockDim.x) {
     const int sq = seq_idx[n], p = pos[n];
     if (sq < 0 || sq >= c.B || p < 0 || p >= c.T_cap) continue;   // reported by the append
+    if (c.block_table && mla_block_or_none(c, sq, p) < 0) continue;   // likewise: skipped as a whole
     atomicMax(c.resid_pos + (size_t)sq * MLA_RESID_WINDOW + (p & (MLA_RESID_WINDOW - 1)), p);
   }
 }
@@ -85,9 +86,10 @@ __device__ void append_epilogue(const AppendArgs& a, const float* tile, int tok0
       append_slot(a, n, &sq, &p);
       if (sq < 0 || sq >= c.B || p < 0 || p >= c.T_cap) continue;
       const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
+      if (lc.pb < 0) continue;   // (the whole warp) nor is the ring: its slot holds a token that is read
       const size_t slot = (size_t)lc.pb * lc.cap + lc.pt;
       const float v = tile[t * COLS + gi * 32 + lane];
-      if (lc.pb >= 0) quant_group_store(c, slot, a.d_c, col, lane, v, a.qbits);
+      quant_group_store(c, slot, a.d_c, col, lane, v, a.qbits);
       const bool own = __shfl_sync(0xffffffffu, lane == 0 ? resid_owns(c, sq, p, a.step_lens != nullptr) : false, 0);
       if (own) resid_store(c, sq, p, a.d_c, col, v);
     }

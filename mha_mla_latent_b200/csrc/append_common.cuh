@@ -182,9 +182,10 @@ __device__ __forceinline__ void append_small_finish(const AppendSmallArgs& sa, f
       const int sq = s_sq[t], p = s_pos[t];
       if (n >= a.N || sq < 0 || sq >= c.B || p < 0 || p >= c.T_cap) continue;
       const MlaLoc lc = mla_loc_or_none(c, sq, p, a.err);
+      if (lc.pb < 0) continue;   // (the whole warp) nor is the ring: its slot holds a token that is read
       const size_t slot = (size_t)lc.pb * lc.cap + lc.pt;
       const float v = tileb[t * kSmCols + lane];
-      if (lc.pb >= 0) quant_group_store(c, slot, a.d_c, col0 + lane, lane, v, a.qbits);
+      quant_group_store(c, slot, a.d_c, col0 + lane, lane, v, a.qbits);
       const bool own = __shfl_sync(0xffffffffu, lane == 0 ? resid_owns(c, sq, p, a.step_lens != nullptr) : false, 0);
       if (own) resid_store(c, sq, p, a.d_c, col0 + lane, v);
     }

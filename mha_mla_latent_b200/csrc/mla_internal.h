@@ -22,14 +22,16 @@ struct MlaLoc {
   int pb, pt, cap;
 };
 #ifdef __CUDACC__
+// The pool block that the table names for token t, -1: none.
+inline __device__ int mla_block_or_none(const mla_cache_t& c, int b, int t) {
+  const int blk = __ldg(c.block_table + (size_t)b * (c.T_cap / MLA_BLOCK_TOKENS) + t / MLA_BLOCK_TOKENS);
+  return blk >= 0 && blk < c.n_blocks ? blk : -1;
+}
 // Without a block in the table: pb = -1, flagged.
 inline __device__ MlaLoc mla_loc_or_none(const mla_cache_t& c, int b, int t, int32_t* err) {
   if (!c.block_table) return MlaLoc{b, t, c.T_cap};
-  int blk = __ldg(c.block_table + (size_t)b * (c.T_cap / MLA_BLOCK_TOKENS) + t / MLA_BLOCK_TOKENS);
-  if (blk < 0 || blk >= c.n_blocks) {
-    atomicOr(err, MLA_DEVERR_BLOCK);
-    blk = -1;
-  }
+  const int blk = mla_block_or_none(c, b, t);
+  if (blk < 0) atomicOr(err, MLA_DEVERR_BLOCK);
   return MlaLoc{blk, t & (MLA_BLOCK_TOKENS - 1), MLA_BLOCK_TOKENS};
 }
 // The same for reading: block 0 in its place.

@@ -233,3 +233,33 @@ def test_append_without_a_block_touches_no_other_sequence(kind):
         b[2, 299 % 128] = a[2, 299 % 128]
         assert torch.equal(a, b)
     plan.close()
+
+
+@pytest.mark.parametrize("n", [1, 40, 128])
+def test_append_without_a_block_leaves_the_ring(n):
+    """The token takes no slot of its sequence's residual window either: the slot still holds one of the
+    newest tokens."""
+    import mha_mla_latent_b200 as mla
+    from mha_mla_latent_b200.cache import BlockPool
+    layer = Layer(d_c=128, cache="int4_r128", seed=37)
+    plan = full_plan(mla, layer, 7)
+    pool = BlockPool(2, 1024, 8)
+    cache = pool.layer(layer.config(mla))
+    g = torch.Generator().manual_seed(9)
+    i32 = lambda v: torch.as_tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows = lambda k: torch.randn(k, HIDDEN, generator=g).to(layer.td).cuda()  # noqa: E731
+    pool.reserve([0, 0], [256, 130])
+    mla.mla_append(plan, rows(386), i32([0] * 256 + [1] * 130), i32([*range(256), *range(130)]), cache.struct)
+    assert mla.mla_device_error(plan) == 0
+    assert cache.resid_pos[0].tolist() == list(range(128, 256))
+    ring, pos = cache.c_resid.clone(), cache.resid_pos.clone()
+    mla.mla_append(plan, rows(n), i32([0] * n), i32(range(256, 256 + n)), cache.struct)   # no block from 256 on
+    assert mla.mla_device_error(plan) == mla.MLA_DEVERR_BLOCK
+    assert torch.equal(cache.resid_pos, pos) and torch.equal(cache.c_resid, ring)
+    q = torch.randn(2, layer.H, layer.d_h, generator=g).to(layer.td).cuda()
+    ws = torch.empty(mla.mla_decode_workspace_bytes(plan, 2), dtype=torch.uint8, device="cuda")
+    mla.mla_decode_step(plan, cache.struct, i32([257, 131]), rows(2), q, torch.empty_like(q), ws)
+    assert mla.mla_device_error(plan) == mla.MLA_DEVERR_BLOCK
+    assert torch.equal(cache.resid_pos[0], pos[0]) and torch.equal(cache.c_resid[0], ring[0])
+    assert cache.resid_pos[1, 2].item() == 130   # the other sequence's token has a block
+    plan.close()
