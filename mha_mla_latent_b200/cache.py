@@ -193,7 +193,8 @@ class BlockPool:
 
     def trim(self, seq_lens, n_sink: int, window: int, stream=None) -> None:
         """Releases the blocks that mla_decode_window does not read any more; a sequence of
-        length 0 is freed.  Blocks behind the length are given back too, those that a reserve
+        length 0 is freed (with a residual window, `reset_sequence` in every layer before another
+        one takes its row).  Blocks behind the length are given back too, those that a reserve
         just made room with included: trim first, or with the lengths that the reserve was for."""
         with self._on(stream):
             _lib.mla_blocks_trim(self.table, self.refs, self._int32(seq_lens), n_sink, window, self.table, self.refs,
