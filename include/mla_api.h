@@ -468,14 +468,15 @@ MLA_API mla_status_t mla_blocks_fork(const int32_t* table, const int32_t* refs, 
  * appended: a free block for each column they touch that has none, or whose block others hold too
  * (one behind the length, where the sequence went back to a shorter one: nothing is copied, the
  * block loses a holder), and a private copy of a partly filled last block (seq_lens[b] % 128 > 0)
- * that others hold too.  Of several sequences in the table that write into the same block, in order of b, each copies while another holder
- * is left; with no holder elsewhere the last one keeps the block.  New blocks are the free
- * blocks of lowest id, given out in the order (b, column), with one holder each; the copied
- * block loses a holder.  `copies` lists the rows to move, in order of b (at most one per
- * sequence: seq_lens[b] % 128 rows); run mla_blocks_copy with every layer's cache before the
- * append.  When the pool has too few free blocks nothing is allocated for any sequence: table
- * and counts stay, no copies are listed, and MLA_DEVERR_POOL is set; the append must then be held
- * back, a shared block would take its rows (mla_append skips tokens at position -1).
+ * that others hold too.  Of several sequences in the table that write into the same block, in
+ * order of b, each copies while another holder is left; with no holder elsewhere the last one
+ * keeps the block.  New blocks are the free blocks of lowest id, given out in the order
+ * (b, column), with one holder each; the copied block loses a holder.  `copies` lists the rows to
+ * move, in order of b (at most one per sequence: seq_lens[b] % 128 rows); run mla_blocks_copy with
+ * every layer's cache before the append.  When the pool has too few free blocks nothing is
+ * allocated for any sequence: table and counts stay, no copies are listed, and MLA_DEVERR_POOL is
+ * set; the append must then be held back, a shared block would take its rows (mla_append skips
+ * tokens at position -1).
  *   seq_lens, new_lens device [B] int32, 0 <= seq_lens <= new_lens <= 128 n_cols: a sequence
  *     outside that gets nothing and sets MLA_DEVERR_SEQ_LEN; one whose partly filled block is
  *     missing from the table sets MLA_DEVERR_BLOCK

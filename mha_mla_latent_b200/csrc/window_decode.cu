@@ -843,10 +843,10 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
         }
         some = true;
         // P row of this token, rounded to bf16: both operands of a product have the latent's type.
-        // Tokens' errors are independent, so they cost about as much as the output's own rounding
-        // does (error against 64 bits 0.0024 of the output's norm; the one-launch form, which keeps
-        // float32, 0.0017); P in two halves would double O's products and P's buffers.  The sum
-        // takes P as it was: rounding to nearest has no bias to make up for.
+        // Tokens' errors are independent: 0.0012 of the output's norm over few visible tokens, 0.0005
+        // over thousands, where the output's own rounding makes 0.0017; P in two halves would double
+        // O's products and P's buffers.  The sum takes P as it was: rounding to nearest has no bias
+        // to make up for.
         uint32_t pk[N / 2];
 #pragma unroll
         for (int h = 0; h < N; h += 2) {
@@ -964,8 +964,8 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
 
 // ------------------------------------------------------------------ absorption
 // q_lat[row][c] = scale x log2(e) x sum_d q[row][d] W_ukF[g][d][c] (summed in float32, rounded once
-// to bf16, the type of the latents that it meets in the attention's product: 2^-9 of a score's
-// terms) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
+// to bf16, the type of the latents that it meets in the attention's product, which makes 0.0016 of
+// the output's norm; in two halves it would double S's products) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
 // kept pairs of the rows, rotated at L - 1.  Latency bound: the W_uk slice and the frequencies
 // come from the plan and are fetched before the kernel ahead is waited for; what follows the
 // wait is one round trip for queries and lengths.
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(kAThreads) window_absorb_kernel(AbsorbArgs a) 
     const uint32_t xy = __ldg(reinterpret_cast<const uint32_t*>(a.q + o * a.d_h) + pair);
     const float x = __uint_as_float(xy << 16), y = __uint_as_float(xy & 0xFFFF0000u);
     // the special-function unit's sine and cosine of an angle reduced to [-pi, pi]: about 5e-7
-    // off, against the 2^-9 of the rounding to bf16 that the attention applies
+    // off, against the 2^-8 of the rounding to bf16 that the attention applies
     float sn, cs;
     __sincosf(rope_angle(L >= 1 && L <= a.T_cap ? L - 1 : 0, th), &sn, &cs);
     *reinterpret_cast<float2*>(a.qrope + o * 8 + 2 * (tid & 3)) = make_float2((x * cs - y * sn) * a.scale, (x * sn + y * cs) * a.scale);

@@ -452,7 +452,7 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // the special-function unit's sine and cosine of an angle reduced to [-pi, pi]:
-            // about 5e-7 off, against the 2^-9 of the bf16 rounding that follows
+            // about 5e-7 off, against the 2^-8 of the bf16 rounding that follows
             float sn, cs;
             __sincosf(rope_angle(p0 + qi, theta[j]), &sn, &cs);
             const float x = lo_f(xy[j]), y = hi_f(xy[j]);
@@ -469,7 +469,8 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
       tc_fence_before();
       arrive(kBarQ);
       // Q_lat: the accumulator's rows of each KV head, scaled, rounded once to bf16 (the type of the
-      // latents that it meets in S: 2^-9 of a score's terms)
+      // latents that it meets in S), which makes 0.0016 of the output's norm; in two halves it would
+      // take twice its shared memory and S's products
       bool ok = true;
 #pragma unroll 1
       for (int k = 0; ok && k < ng; ++k) {
@@ -615,9 +616,9 @@ window_fused_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_const
         const float mb = m == -INFINITY ? 0.f : m;   // masked scores are -inf: 2^(-inf) = 0
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         // P, rounded to bf16: both operands of a product have the latent's type.  Tokens' errors are
-        // independent and cost about as much as the output's own rounding does (error against 64
-        // bits 0.0026 of the output's norm, where that alone gives 0.0017); P in two halves would
-        // double O's products, which bound the kernel while tiles flow.
+        // independent: 0.0012 of the output's norm over few visible tokens, less over many, where the
+        // output's own rounding makes 0.0017; P in two halves would double O's products, which bound
+        // the kernel while tiles flow.
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
