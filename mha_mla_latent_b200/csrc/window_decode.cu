@@ -965,10 +965,10 @@ window_decode_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_cons
 // ------------------------------------------------------------------ absorption
 // q_lat[row][c] = scale x log2(e) x sum_d q[row][d] W_ukF[g][d][c] (summed in float32, rounded once
 // to bf16, the type of the latents that it meets in the attention's product, which makes 0.0016 of
-// the output's norm; in two halves it would double S's products) for 32 rows (sequence, query head of KV head g) and 64 latent columns per CTA, and the
-// kept pairs of the rows, rotated at L - 1.  Latency bound: the W_uk slice and the frequencies
-// come from the plan and are fetched before the kernel ahead is waited for; what follows the
-// wait is one round trip for queries and lengths.
+// the output's norm; in two halves it would double S's products) for 32 rows (sequence, query head
+// of KV head g) and 64 latent columns per CTA, and the kept pairs of the rows, rotated at L - 1.
+// Latency bound: the W_uk slice and the frequencies come from the plan and are fetched before the
+// kernel ahead is waited for; what follows the wait is one round trip for queries and lengths.
 constexpr int kARows = 32, kACols = 64, kAThreads = 256;
 struct AbsorbArgs {
   int B, H, G, n_kv, d_h, d_c, T_cap;
